@@ -329,6 +329,176 @@ int mamba2_ssd_backward_profile(const mamba2_dims* dims, const void* x, const vo
                                 float* dinit, void* workspace, size_t workspace_bytes,
                                 void* stream, float* stage_ms);
 
+/*
+ * The operators around the SSD
+ * ----------------------------
+ * What a layer built on the SSD computes next to it: the short causal
+ * convolution that makes x, B and C (conv1d), the same recurrence with a
+ * decay for each (channel, state) (selective_scan), and the norm of its
+ * input or gated output (norm).  The conventions above hold, with these
+ * additions:
+ * Strides: where dims has a <name>_stride, token t of batch b of that tensor
+ *        starts at element (b * L + t) * <name>_stride of it (row r of a norm
+ *        at r * <name>_stride): a tensor may be a column range of a wider
+ *        one.  0 means rows without gaps.  The base pointer is 16-byte
+ *        aligned; rows need not be (rows and sizes that are multiples of 16
+ *        bytes run faster).  Everything else is contiguous.
+ * lengths: int32 [B] or NULL (every sequence has L tokens): sequence b has
+ *        lengths[b] tokens, values outside 0 .. L are taken as the nearer
+ *        bound.  What stands in the inputs behind them is not read; outputs
+ *        and gradients there are written as zeros.  A final state is the
+ *        state after the sequence's own last token (the initial state where
+ *        it has none).
+ * Outputs do not overlap inputs, but final_state may be init_state.
+ * Gradients that are sums over tokens are formed from per-workgroup float32
+ * parts in a fixed order: the same call gives the same bits.
+ */
+typedef enum { MAMBA2_ACT_NONE = 0, MAMBA2_ACT_SILU = 1 } mamba2_activation;
+typedef enum { MAMBA2_NORM_RMS = 0, MAMBA2_NORM_LAYER = 1 } mamba2_norm_kind;
+
+typedef struct {
+  int64_t batch;      /* B >= 1 */
+  int64_t seqlen;     /* L >= 1 */
+  int64_t channels;   /* C >= 1 */
+  int64_t width;      /* W: 2, 3 or 4 taps */
+  int64_t part[3];    /* channels of the outputs y0, y1, y2; they add up to C, unused ones are 0 */
+  int64_t x_stride;   /* elements between tokens of x; 0: C */
+  int64_t dx_stride;  /* the same of dx (backward) */
+  int32_t dtype;      /* mamba2_dtype */
+  int32_t activation; /* mamba2_activation */
+} mamba2_conv_dims;
+
+/*
+ * conv1d: a causal depthwise convolution over the tokens, per channel c
+ *     p[t]  = bias + sum_k weight[c, k] * x[t - (W-1) + k],  k = 0 .. W-1
+ *     y[t]  = p[t] * sigmoid(p[t])   (MAMBA2_ACT_SILU)   or   p[t]
+ * where x[-j] is row W-1-j of init_state (zeros if NULL).
+ *     x             [B, L, C]       rows of x_stride
+ *     y0, y1, y2    [B, L, part[i]] contiguous: channels in order, so one
+ *                   call makes the x, B and C that mamba2_ssd_forward takes
+ *     weight        [C, W] float32; bias [C] float32 or NULL
+ *     init_state    [B, W-1, C] or NULL; final_state the same or NULL (not
+ *                   written): the last W-1 rows of [init_state; x]
+ * x, y and the states have the type of dims.  Sums are float32.  Supported:
+ * batch <= 65535, C <= 2^20, C * B * ceil(L / 8) <= 2^31.
+ */
+int mamba2_conv1d_forward(const mamba2_conv_dims* dims, const void* x, const float* weight,
+                          const float* bias, const void* init_state, const int32_t* lengths,
+                          void* y0, void* y1, void* y2, void* final_state, void* stream);
+
+/*
+ * Gradients of conv1d for the loss whose gradients with respect to y0, y1,
+ * y2 and final_state are dy0, dy1, dy2 and dfinal (NULL = zero):
+ *     dx [B, L, C] rows of dx_stride, dinit [B, W-1, C] (may be NULL: not
+ *     written), type of dims; dweight [C, W] and dbias [C] float32 (dbias
+ *     may be NULL).
+ * The convolution is recomputed; workspace at least
+ * mamba2_conv1d_backward_workspace_bytes(dims) (0: dims invalid), 256-byte
+ * aligned.
+ */
+size_t mamba2_conv1d_backward_workspace_bytes(const mamba2_conv_dims* dims);
+
+int mamba2_conv1d_backward(const mamba2_conv_dims* dims, const void* x, const float* weight,
+                           const float* bias, const void* init_state, const int32_t* lengths,
+                           const void* dy0, const void* dy1, const void* dy2, const void* dfinal,
+                           void* dx, float* dweight, float* dbias, void* dinit, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * One token of conv1d for every sequence: seqlen must be 1, x [B, C] with
+ * rows of x_stride, y0, y1, y2 [B, part[i]]; state [B, W-1, C] (the last
+ * rows of x) is read and moved on by one row in place.
+ */
+int mamba2_conv1d_step(const mamba2_conv_dims* dims, const void* x, const float* weight,
+                       const float* bias, void* state, void* y0, void* y1, void* y2,
+                       void* stream);
+
+#define MAMBA2_SCAN_MAX_STATE 64
+
+typedef struct {
+  int64_t batch;      /* B >= 1 */
+  int64_t seqlen;     /* L >= 1 */
+  int64_t channels;   /* D >= 1 */
+  int64_t dstate;     /* N: 1 .. MAMBA2_SCAN_MAX_STATE */
+  int64_t ngroups;    /* G, divides D: channel c reads B/C group c / (D/G) */
+  int64_t z_stride;   /* elements between tokens of z; 0: D */
+  int64_t b_stride;   /* the same of B and of C; 0: G * N */
+  int64_t c_stride;
+  int64_t dz_stride;  /* the same of dz (backward) */
+  int32_t dtype;      /* mamba2_dtype */
+  int32_t softplus;   /* 1: the time step is softplus(dt + dt_bias); 0: dt + dt_bias */
+} mamba2_scan_dims;
+
+/*
+ * selective_scan: the recurrence of the SSD with a decay of its own for each
+ * (channel, state).  For token t, channel c, group g = c / (D/G):
+ *     d    = softplus(dt[t, c] + dt_bias[c])
+ *     h[n] = exp(d * A[c, n]) * h[n] + d * u[t, c] * B[t, g, n]
+ *     s    = sum_n C[t, g, n] * h[n] + D[c] * u[t, c]
+ *     y    = s * z[t, c] * sigmoid(z[t, c])        (or s, z NULL)
+ *     u, dt, y      [B, L, D]; z [B, L, D] rows of z_stride, or NULL
+ *     B, C          [B, L, G, N] rows of b_stride and c_stride
+ *     A             [D, N] float32, <= 0; D, dt_bias [D] float32 or NULL
+ *     init_state, final_state [B, D, N] float32 or NULL
+ * u, dt, B, C, z and y have the type of dims; the recurrence is float32.
+ * Supported: batch <= 65535, B * D <= 2^26, B * L * D <= 2^35.  Workspace at
+ * least mamba2_selective_scan_workspace_bytes(dims) (0: dims invalid),
+ * 256-byte aligned.
+ */
+size_t mamba2_selective_scan_workspace_bytes(const mamba2_scan_dims* dims);
+
+int mamba2_selective_scan_forward(const mamba2_scan_dims* dims, const void* u, const void* dt,
+                                  const float* A, const void* B, const void* C, const float* D,
+                                  const void* z, const float* dt_bias, const float* init_state,
+                                  const int32_t* lengths, void* y, float* final_state,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of selective_scan for every sequence: seqlen must be 1; u, dt, z,
+ * y [B, D], B, C [B, G, N] (strides as above); state [B, D, N] float32, read
+ * and overwritten.  Bound by HBM on the state.
+ */
+int mamba2_selective_scan_step(const mamba2_scan_dims* dims, const void* u, const void* dt,
+                               const float* A, const void* B, const void* C, const float* D,
+                               const void* z, const float* dt_bias, float* state, void* y,
+                               void* stream);
+
+typedef struct {
+  int64_t rows;      /* R >= 1 */
+  int64_t channels;  /* D >= 1 */
+  int64_t ngroups;   /* groups of D/G channels that are normalised apart; D/G <= 8192 */
+  int64_t x_stride;  /* elements between rows of x; 0: D */
+  int64_t z_stride;  /* the same of z, and of dz (backward) */
+  int64_t dz_stride;
+  float eps;         /* >= 0 */
+  int32_t kind;      /* mamba2_norm_kind */
+  int32_t dtype;     /* mamba2_dtype */
+  int32_t reserved;  /* must be 0 */
+} mamba2_norm_dims;
+
+/*
+ * norm: per row and group, of v = x * z * sigmoid(z) (v = x where z is NULL),
+ *     RMS:   y = v / sqrt(mean(v^2) + eps) * weight + bias
+ *     layer: y = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
+ *     x, z, y [R, D] of the type of dims (x and z strided); weight [D]
+ *     float32; bias [D] float32 or NULL.  Statistics are float32.
+ */
+int mamba2_norm_forward(const mamba2_norm_dims* dims, const void* x, const void* z,
+                        const float* weight, const float* bias, void* y, void* stream);
+
+/*
+ * Gradients of norm from dy [R, D]: dx [R, D], dz [R, D] (rows of dz_stride;
+ * required exactly when z is given), dweight [D] and dbias [D] float32
+ * (dbias may be NULL: not written).  The statistics are recomputed; workspace
+ * at least mamba2_norm_backward_workspace_bytes(dims) (0: dims invalid),
+ * 256-byte aligned.
+ */
+size_t mamba2_norm_backward_workspace_bytes(const mamba2_norm_dims* dims);
+
+int mamba2_norm_backward(const mamba2_norm_dims* dims, const void* x, const void* z,
+                         const float* weight, const void* dy, void* dx, void* dz, float* dweight,
+                         float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* mamba2_status_string(int status);
 

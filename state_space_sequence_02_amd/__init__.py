@@ -51,6 +51,10 @@ EXPORTS = (
     "mamba2_decode_step", "mamba2_ssd_backward_workspace_bytes",
     "mamba2_ssd_backward", "mamba2_ssd_backward_profile", "mamba2_status_string",
     "mamba2_last_error", "mamba2_ssd_forward_noalloc",
+    "mamba2_conv1d_forward", "mamba2_conv1d_backward_workspace_bytes", "mamba2_conv1d_backward",
+    "mamba2_conv1d_step", "mamba2_selective_scan_workspace_bytes",
+    "mamba2_selective_scan_forward", "mamba2_selective_scan_step", "mamba2_norm_forward",
+    "mamba2_norm_backward_workspace_bytes", "mamba2_norm_backward",
 )
 
 # bytes of the static per-GPU scratch behind mamba2_ssd_forward_noalloc
@@ -66,6 +70,39 @@ class Mamba2Dims(ctypes.Structure):
 
     def __repr__(self):
         return "Mamba2Dims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class _Dims(ctypes.Structure):
+    def __repr__(self):
+        return type(self).__name__ + "(" + ", ".join(
+            f"{n}={list(v) if isinstance(v, ctypes.Array) else v}"
+            for n, v in ((n, getattr(self, n)) for n, _ in self._fields_)) + ")"
+
+
+class Mamba2ConvDims(_Dims):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+        ("width", ctypes.c_int64), ("part", ctypes.c_int64 * 3), ("x_stride", ctypes.c_int64),
+        ("dx_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+    ]
+
+
+class Mamba2ScanDims(_Dims):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+        ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+        ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("softplus", ctypes.c_int32),
+    ]
+
+
+class Mamba2NormDims(_Dims):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64),
+        ("eps", ctypes.c_float), ("kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
 
 
 class Mamba2Error(RuntimeError):
@@ -104,6 +141,20 @@ def _load():
         "mamba2_ssd_backward_profile": ([D] + [P] * 17 + [ctypes.c_size_t, P, P], ctypes.c_int),
         "mamba2_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "mamba2_last_error": ([], ctypes.c_char_p),
+    }
+    Z, CV, SC, NM = (ctypes.c_size_t, ctypes.POINTER(Mamba2ConvDims),
+                     ctypes.POINTER(Mamba2ScanDims), ctypes.POINTER(Mamba2NormDims))
+    sig |= {
+        "mamba2_conv1d_forward": ([CV] + [P] * 10, ctypes.c_int),
+        "mamba2_conv1d_backward_workspace_bytes": ([CV], Z),
+        "mamba2_conv1d_backward": ([CV] + [P] * 14 + [Z, P], ctypes.c_int),
+        "mamba2_conv1d_step": ([CV] + [P] * 8, ctypes.c_int),
+        "mamba2_selective_scan_workspace_bytes": ([SC], Z),
+        "mamba2_selective_scan_forward": ([SC] + [P] * 13 + [Z, P], ctypes.c_int),
+        "mamba2_selective_scan_step": ([SC] + [P] * 11, ctypes.c_int),
+        "mamba2_norm_forward": ([NM] + [P] * 6, ctypes.c_int),
+        "mamba2_norm_backward_workspace_bytes": ([NM], Z),
+        "mamba2_norm_backward": ([NM] + [P] * 9 + [Z, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -494,3 +545,13 @@ def stage_buffers(dims, device):
     st = torch.empty((dims.batch, nc, dims.nheads, dims.headdim, dims.dstate),
                      dtype=torch.float32, device=device)
     return cs, dtt, st
+
+
+# the operators around the SSD (their own module; part of this interface)
+from .layer import (  # noqa: E402
+    conv1d_backward, conv1d_forward, conv1d_step, make_conv_dims, make_norm_dims, make_scan_dims,
+    mamba2_conv1d_backward, mamba2_conv1d_backward_workspace_bytes, mamba2_conv1d_forward,
+    mamba2_conv1d_step, mamba2_norm_backward, mamba2_norm_backward_workspace_bytes,
+    mamba2_norm_forward, mamba2_selective_scan_forward, mamba2_selective_scan_step,
+    mamba2_selective_scan_workspace_bytes, norm_backward, norm_forward, selective_scan_forward,
+    selective_scan_step)

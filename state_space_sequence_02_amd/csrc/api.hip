@@ -1,15 +1,13 @@
 // C ABI of the SSD forward pass: argument checks on the host, workspace
 // carving, and stream-ordered launches of the stage kernels.  Declarations and
 // the contract of every entry point are in include/mamba2_ssd.h.
-#include <stdarg.h>
 #include <stdint.h>
-#include <stdio.h>
-#include <string.h>
 
 #include <mutex>
 
 #include "launch.h"
 #include "mamba2_ssd.h"
+#include "status.h"
 
 // Workspace of mamba2_ssd_forward_noalloc: one copy per GPU, held for the
 // process's lifetime.  Host code never uses this name as an address (it is a
@@ -18,23 +16,13 @@ static __device__ __align__(256) unsigned char scratch[MAMBA2_NOALLOC_SCRATCH_BY
 
 namespace {
 
-thread_local char g_last_error[512] = "";
-
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int status, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
-  va_end(ap);
-  return status;
-}
-
-int ok() {
-  g_last_error[0] = '\0';
-  return MAMBA2_OK;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+using m2::fail;
+using m2::hip_status;
+using m2::maybe;
+using m2::need;
+using m2::need_workspace;
+using m2::ok;
+using m2::round256;
 
 // Upper bounds that keep every index and grid size inside the kernels' types.
 constexpr int64_t kMaxSeq = (int64_t)1 << 30;
@@ -99,24 +87,6 @@ int validate(const mamba2_dims* d, m2::Dims* out) {
   }
   return MAMBA2_OK;
 }
-
-int need(const void* p, const char* name) {
-  if (!p) return fail(MAMBA2_ERR_NULL, "%s is NULL", name);
-  if (!aligned16(p)) return fail(MAMBA2_ERR_ALIGN, "%s is not 16-byte aligned", name);
-  return MAMBA2_OK;
-}
-
-int maybe(const void* p, const char* name) {
-  if (p && !aligned16(p)) return fail(MAMBA2_ERR_ALIGN, "%s is not 16-byte aligned", name);
-  return MAMBA2_OK;
-}
-
-int hip_status(hipError_t e, const char* where) {
-  if (e == hipSuccess) return ok();
-  return fail(MAMBA2_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
-}
-
-size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Workspace of mamba2_ssd_forward, exactly what its path uses (256-byte
 // aligned pieces): dA_cs and dt_T [B,H,nc,Q] f32; then
@@ -226,12 +196,6 @@ int check_forward_args(const mamba2_dims* dims, m2::Dims* d, const void* x, cons
                        const float* init_state, void* y, float* final_state, void* workspace,
                        size_t workspace_bytes);
 
-#define CHECK(expr)               \
-  do {                            \
-    const int rc_ = (expr);       \
-    if (rc_ != MAMBA2_OK) return rc_; \
-  } while (0)
-
 int check_forward_args(const mamba2_dims* dims, m2::Dims* d, const void* x, const void* dt,
                        const float* A, const void* B, const void* C, const float* D,
                        const float* init_state, void* y, float* final_state, void* workspace,
@@ -247,13 +211,7 @@ int check_forward_args(const mamba2_dims* dims, m2::Dims* d, const void* x, cons
   CHECK(need(y, "y"));
   CHECK(maybe(final_state, "final_state"));
   const Workspace w = plan(*d);
-  if (!workspace) return fail(MAMBA2_ERR_WORKSPACE, "workspace is NULL");
-  if (((uintptr_t)workspace & 255u) != 0)
-    return fail(MAMBA2_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-  if (workspace_bytes < w.total)
-    return fail(MAMBA2_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes,
-                w.total);
-  return MAMBA2_OK;
+  return need_workspace(workspace, workspace_bytes, w.total);
 }
 
 // Device address of `scratch` on the current device, looked up once per
@@ -499,13 +457,7 @@ int check_backward_args(const mamba2_dims* dims, m2::Dims* d, const void* x, con
   const BwdWorkspace w = plan_backward(*d);
   if (w.fast && w.wph > 128)  // the dx kernel's LDS holds at most 128 boundary parts
     return fail(MAMBA2_ERR_UNSUPPORTED, "state too large for the backward pass");
-  if (!workspace) return fail(MAMBA2_ERR_WORKSPACE, "workspace is NULL");
-  if (((uintptr_t)workspace & 255u) != 0)
-    return fail(MAMBA2_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-  if (workspace_bytes < w.total)
-    return fail(MAMBA2_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes,
-                w.total);
-  return MAMBA2_OK;
+  return need_workspace(workspace, workspace_bytes, w.total);
 }
 
 }  // namespace
@@ -775,6 +727,6 @@ const char* mamba2_status_string(int status) {
   }
 }
 
-const char* mamba2_last_error(void) { return g_last_error; }
+const char* mamba2_last_error(void) { return m2::last_error(); }
 
 }  // extern "C"

@@ -135,4 +135,64 @@ hipError_t launch_decode_step(const Dims& d, const void* x, const void* dt, cons
                               const void* B, const void* C, const float* D, float* state,
                               void* y, hipStream_t s);
 
+// The operators around the SSD (conv1d.hip, selective_scan.hip, norm.hip).
+// Token strides are in elements; batches follow each other at L token strides.
+struct ConvDims {
+  int64_t B, L, C, W, part[3], xs, dxs;
+  bool bf16, silu;
+};
+hipError_t launch_conv1d(const ConvDims& d, const void* x, const float* w, const float* bias,
+                         const void* init, const int32_t* lengths, void* const* y,
+                         void* final_state, hipStream_t s);
+size_t conv1d_part_bytes(const ConvDims& d);
+hipError_t launch_conv1d_backward(const ConvDims& d, const void* x, const float* w,
+                                  const float* bias, const void* init, const int32_t* lengths,
+                                  void* const* dy, const void* dfinal, void* dx, void* dinit,
+                                  float* dw, float* dbias, float* part, hipStream_t s);
+hipError_t launch_conv1d_step(const ConvDims& d, const void* x, const float* w, const float* bias,
+                              void* state, void* const* y, hipStream_t s);
+
+struct NormDims {
+  int64_t R, D, G, xs, zs, dzs;
+  float eps;
+  bool bf16, layer;
+};
+// Longest group of channels one workgroup holds in registers.
+constexpr int64_t kNormMaxGroup = 8192;
+hipError_t launch_norm(const NormDims& d, const void* x, const void* z, const float* w,
+                       const float* bias, void* y, hipStream_t s);
+size_t norm_part_bytes(const NormDims& d);
+hipError_t launch_norm_backward(const NormDims& d, const void* x, const void* z, const float* w,
+                                const void* dy, void* dx, void* dz, float* dw, float* dbias,
+                                float* part, hipStream_t s);
+
+struct ScanDims {
+  int64_t B, L, D, N, G, zs, bs, cs, dzs;
+  bool bf16, softplus;
+};
+// Chunks of the sequence that run in parallel and the tokens of each.
+struct ScanSplit {
+  int64_t chunks, len;
+};
+size_t scan_forward_bytes(const ScanDims& d);
+hipError_t launch_selective_scan(const ScanDims& d, const void* u, const void* dt, const float* A,
+                                 const void* B, const void* C, const float* D, const void* z,
+                                 const float* dt_bias, const float* init, const int32_t* lengths,
+                                 void* y, float* final_state, void* ws, hipStream_t s);
+size_t scan_backward_bytes(const ScanDims& d);
+hipError_t launch_selective_scan_backward(
+    const ScanDims& d, const void* u, const void* dt, const float* A, const void* B, const void* C,
+    const float* D, const void* z, const float* dt_bias, const float* init, const int32_t* lengths,
+    const void* dy, const float* dfinal, void* du, void* ddt, float* dA, void* dB, void* dC,
+    float* dD, void* dz, float* ddt_bias, float* dinit, void* ws, hipStream_t s);
+hipError_t launch_selective_scan_step(const ScanDims& d, const void* u, const void* dt,
+                                      const float* A, const void* B, const void* C, const float* D,
+                                      const void* z, const float* dt_bias, float* state, void* y,
+                                      hipStream_t s);
+
+// out[m] = sum over rows p of part[p][m], columns [0, ends[0]), [ends[0],
+// ends[1]) and [ends[1], ends[2]) going to outs[0..2] (NULL: not written).
+hipError_t launch_partial_sums(const float* part, int64_t P, int64_t M, const int64_t ends[3],
+                               float* const outs[3], hipStream_t s);
+
 }  // namespace m2
