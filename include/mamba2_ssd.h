@@ -441,8 +441,9 @@ typedef struct {
  *     A             [D, N] float32, <= 0; D, dt_bias [D] float32 or NULL
  *     init_state, final_state [B, D, N] float32 or NULL
  * u, dt, B, C, z and y have the type of dims; the recurrence is float32.
- * Supported: batch <= 65535, B * D <= 2^26, B * L * D <= 2^35.  Workspace at
- * least mamba2_selective_scan_workspace_bytes(dims) (0: dims invalid),
+ * Supported: batch <= 65535, B * D <= 2^26, (L / 16) * (D / 64) < 2^24,
+ * B * L * G * N <= 2^28 (a problem too large gives MAMBA2_ERR_UNSUPPORTED).
+ * Workspace at least mamba2_selective_scan_workspace_bytes(dims) (0: dims invalid),
  * 256-byte aligned.
  */
 size_t mamba2_selective_scan_workspace_bytes(const mamba2_scan_dims* dims);
@@ -452,6 +453,29 @@ int mamba2_selective_scan_forward(const mamba2_scan_dims* dims, const void* u, c
                                   const void* z, const float* dt_bias, const float* init_state,
                                   const int32_t* lengths, void* y, float* final_state,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of selective_scan from dy [B, L, D] and dfinal [B, D, N] float32
+ * (NULL = zero):
+ *     du, ddt [B, L, D]; dz [B, L, D] rows of dz_stride (required exactly
+ *     when z is given); dB, dC [B, L, G, N]: type of dims
+ *     dA [D, N]; dD, ddt_bias [D] and dinit [B, D, N] (each may be NULL: not
+ *     written): float32
+ * ddt is the gradient with respect to dt as passed (before bias and
+ * softplus); dB and dC are summed over the channels of a group.  The states
+ * are recomputed; workspace at least
+ * mamba2_selective_scan_backward_workspace_bytes(dims) (0: dims invalid),
+ * 256-byte aligned.
+ */
+size_t mamba2_selective_scan_backward_workspace_bytes(const mamba2_scan_dims* dims);
+
+int mamba2_selective_scan_backward(const mamba2_scan_dims* dims, const void* u, const void* dt,
+                                   const float* A, const void* B, const void* C, const float* D,
+                                   const void* z, const float* dt_bias, const float* init_state,
+                                   const int32_t* lengths, const void* dy, const float* dfinal,
+                                   void* du, void* ddt, float* dA, void* dB, void* dC, float* dD,
+                                   void* dz, float* ddt_bias, float* dinit, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /*
  * One token of selective_scan for every sequence: seqlen must be 1; u, dt, z,

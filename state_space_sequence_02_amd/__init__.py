@@ -53,7 +53,8 @@ EXPORTS = (
     "mamba2_last_error", "mamba2_ssd_forward_noalloc",
     "mamba2_conv1d_forward", "mamba2_conv1d_backward_workspace_bytes", "mamba2_conv1d_backward",
     "mamba2_conv1d_step", "mamba2_selective_scan_workspace_bytes",
-    "mamba2_selective_scan_forward", "mamba2_selective_scan_step", "mamba2_norm_forward",
+    "mamba2_selective_scan_forward", "mamba2_selective_scan_backward_workspace_bytes",
+    "mamba2_selective_scan_backward", "mamba2_selective_scan_step", "mamba2_norm_forward",
     "mamba2_norm_backward_workspace_bytes", "mamba2_norm_backward",
 )
 
@@ -151,6 +152,8 @@ def _load():
         "mamba2_conv1d_step": ([CV] + [P] * 8, ctypes.c_int),
         "mamba2_selective_scan_workspace_bytes": ([SC], Z),
         "mamba2_selective_scan_forward": ([SC] + [P] * 13 + [Z, P], ctypes.c_int),
+        "mamba2_selective_scan_backward_workspace_bytes": ([SC], Z),
+        "mamba2_selective_scan_backward": ([SC] + [P] * 22 + [Z, P], ctypes.c_int),
         "mamba2_selective_scan_step": ([SC] + [P] * 11, ctypes.c_int),
         "mamba2_norm_forward": ([NM] + [P] * 6, ctypes.c_int),
         "mamba2_norm_backward_workspace_bytes": ([NM], Z),
@@ -552,6 +555,7 @@ from .layer import (  # noqa: E402
     conv1d_backward, conv1d_forward, conv1d_step, make_conv_dims, make_norm_dims, make_scan_dims,
     mamba2_conv1d_backward, mamba2_conv1d_backward_workspace_bytes, mamba2_conv1d_forward,
     mamba2_conv1d_step, mamba2_norm_backward, mamba2_norm_backward_workspace_bytes,
-    mamba2_norm_forward, mamba2_selective_scan_forward, mamba2_selective_scan_step,
-    mamba2_selective_scan_workspace_bytes, norm_backward, norm_forward, selective_scan_forward,
-    selective_scan_step)
+    mamba2_norm_forward, mamba2_selective_scan_backward,
+    mamba2_selective_scan_backward_workspace_bytes, mamba2_selective_scan_forward,
+    mamba2_selective_scan_step, mamba2_selective_scan_workspace_bytes, norm_backward, norm_forward,
+    selective_scan_backward, selective_scan_forward, selective_scan_step)

@@ -26,6 +26,8 @@ constexpr int64_t kMaxChannels = (int64_t)1 << 20;
 constexpr int64_t kMaxStride = (int64_t)1 << 24;    // elements between tokens
 constexpr int64_t kMaxUnits = (int64_t)1 << 31;     // channels * batch * ceil(seqlen / 8)
 constexpr int64_t kMaxRows = (int64_t)1 << 26;      // batch * channels of a scan
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;  // workgroups of 256 along x
+constexpr int64_t kMaxSums = (int64_t)1 << 30;
 
 int check_dtype(int32_t dtype) {
   if (dtype != MAMBA2_DTYPE_F32 && dtype != MAMBA2_DTYPE_BF16)
@@ -128,7 +130,12 @@ int validate(const mamba2_scan_dims* p, m2::ScanDims* d) {
   CHECK(check_stride(&d->dzs, d->D, "dz_stride"));
   d->bf16 = p->dtype == MAMBA2_DTYPE_BF16;
   d->softplus = p->softplus != 0;
-  if (d->B * d->D > kMaxRows || d->B * d->L > kMaxUnits * 16 / d->D)
+  // the backward's workgroups (at least 16 tokens of 64 channels of a group)
+  // and its [B, L, G, states] sums, whose states are padded to a power of two
+  const int64_t tiles = d->G * ((d->D / d->G + 63) / 64);
+  const int64_t padded = d->N < 2 ? 4 : 2 * d->N;
+  if (d->B * d->D > kMaxRows || (d->L + 15) / 16 > kMaxGroups / tiles ||
+      d->B * d->L > kMaxSums / (d->G * padded))
     return fail(MAMBA2_ERR_UNSUPPORTED, "problem too large for one call");
   return MAMBA2_OK;
 }
@@ -275,6 +282,50 @@ int mamba2_selective_scan_forward(const mamba2_scan_dims* dims, const void* u, c
                                               lengths, y, final_state, workspace,
                                               (hipStream_t)stream),
                     "selective_scan launch");
+}
+
+size_t mamba2_selective_scan_backward_workspace_bytes(const mamba2_scan_dims* dims) {
+  m2::ScanDims d;
+  if (validate(dims, &d) != MAMBA2_OK) return 0;
+  return at_least_256(m2::scan_backward_bytes(d));
+}
+
+int mamba2_selective_scan_backward(const mamba2_scan_dims* dims, const void* u, const void* dt,
+                                   const float* A, const void* B, const void* C, const float* D,
+                                   const void* z, const float* dt_bias, const float* init_state,
+                                   const int32_t* lengths, const void* dy, const float* dfinal,
+                                   void* du, void* ddt, float* dA, void* dB, void* dC, float* dD,
+                                   void* dz, float* ddt_bias, float* dinit, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  m2::ScanDims d;
+  CHECK(validate(dims, &d));
+  CHECK(need(u, "u"));
+  CHECK(need(dt, "dt"));
+  CHECK(need(A, "A"));
+  CHECK(need(B, "B"));
+  CHECK(need(C, "C"));
+  CHECK(maybe(D, "D"));
+  CHECK(maybe(z, "z"));
+  CHECK(maybe(dt_bias, "dt_bias"));
+  CHECK(maybe(init_state, "init_state"));
+  CHECK(maybe(lengths, "lengths"));
+  CHECK(need(dy, "dy"));
+  CHECK(maybe(dfinal, "dfinal"));
+  CHECK(need(du, "du"));
+  CHECK(need(ddt, "ddt"));
+  CHECK(need(dA, "dA"));
+  CHECK(need(dB, "dB"));
+  CHECK(need(dC, "dC"));
+  CHECK(maybe(dD, "dD"));
+  if (z) CHECK(need(dz, "dz"));
+  CHECK(maybe(ddt_bias, "ddt_bias"));
+  CHECK(maybe(dinit, "dinit"));
+  CHECK(need_workspace(workspace, workspace_bytes, at_least_256(m2::scan_backward_bytes(d))));
+  return hip_status(
+      m2::launch_selective_scan_backward(d, u, dt, A, B, C, D, z, dt_bias, init_state, lengths, dy,
+                                         dfinal, du, ddt, dA, dB, dC, dD, z ? dz : nullptr,
+                                         ddt_bias, dinit, workspace, (hipStream_t)stream),
+      "selective_scan backward launch");
 }
 
 int mamba2_selective_scan_step(const mamba2_scan_dims* dims, const void* u, const void* dt,

@@ -1,0 +1,662 @@
+// Backward pass of the selective scan.  With q = dy silu(z) (dy without a
+// gate), d the time step, w = d u, a = exp(d A), per token t, channel and
+// state n:
+//
+//     g[t] = q[t] C[t] + a[t+1] g[t+1]          (the gradient of h[t]; dfinal at the end)
+//     dC = sum over channels q h                dB = sum over channels g w
+//     du = d sum_n g B + D q                    dD = sum q u
+//     dd = sum_n A g (a h[t-1]) + u sum_n g B   dA = sum over tokens d g (a h[t-1])
+//     ddt = dd softplus'(dt + bias)             ddt_bias = sum over tokens ddt
+//     dz = dy silu'(z) (sum_n C h + D u)        dinit = a[0] g[0]
+//
+// The states are recomputed.  The sequence is cut into short chunks (64
+// tokens at 16 states) that run at once:
+//   1. scan_bwd_ends: per chunk the state reached from zero, the decay over
+//      the chunk, and the gradient its tokens send to its start.  All three
+//      go forward in time, from one exponential per (token, channel, state):
+//      the last is sum_t (a[0] .. a[t]) q[t] C[t].
+//   2. scan_bwd_carry: start states forward over the chunks, end gradients
+//      backward over them.
+//   3. scan_bwd_main: per chunk the states at the start of each tile of
+//      tokens (kept in LDS), then the tiles in reverse, each with its states
+//      and decays in registers.
+//   4. the sums over channels (dB, dC) and over chunks (dA, dD, ddt_bias).
+//
+// A lane holds K of a channel's 4 K states, four lanes (a quad) a channel, a
+// wavefront 16 channels, a workgroup 64 of one group.  Each lane of a quad
+// loads every fourth token and hands it to the other three through the quad
+// permutation that an instruction's operand can carry; sums over a channel's
+// states cross the quad the same way, so nothing waits for another wavefront
+// inside a chunk.  Sums over the channels of a wavefront (dB, dC) exchange
+// halves of the values while they add: the count of values halves with the
+// count of lanes, two operations per value instead of eight.
+#include "selective_scan.h"
+
+namespace m2 {
+
+namespace {
+
+constexpr int kQuadWaves = 4;
+
+// Tokens of a tile whose states and decays stay in registers, and tokens of a
+// chunk: the workgroup's tile-start states take at most 64 KB of LDS.
+constexpr int bwd_tile(int K) { return K <= 4 ? 8 : 4; }
+constexpr int bwd_chunk(int K) { return K <= 4 ? 64 : K == 8 ? 32 : 16; }
+
+inline int bwd_k(int64_t N) {
+  int k = 1;
+  while (4 * k < N) k *= 2;
+  return k;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// The value of lane J of this lane's quad.
+template <int J>
+__device__ __forceinline__ float of_lane(float v) { return dpp<J * 0x55>(v); }
+__device__ __forceinline__ float quad_sum(float v) {
+  v += dpp<0xB1>(v);  // lanes 1 0 3 2
+  v += dpp<0x4E>(v);  // lanes 2 3 0 1
+  return v;
+}
+// The value of the lane 8 and 4 lanes away (exclusive or) in a row of 16: a
+// rotation by 8; the mirror of 8 lanes after that of each quad.
+__device__ __forceinline__ float from_xor8(float v) { return dpp<0x128>(v); }
+__device__ __forceinline__ float from_xor4(float v) { return dpp<0x141>(dpp<0x1B>(v)); }
+
+// Sums v over the 16 lanes of the wavefront that hold the same quarter of the
+// states.  M values per lane become ceil(M / 16): lane (b5 b4 b3 b2 j) ends
+// with the totals of v[b5 M/2 + b4 M/4 + b3 M/8 + b2 M/16 + r].
+template <int M>
+__device__ __forceinline__ void sum_channels(float (&v)[M], int lane) {
+  static_assert(M >= 8, "");
+#pragma unroll
+  for (int m = 0; m < M / 2; ++m) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, v[m]),
+                                                    __builtin_bit_cast(unsigned, v[m + M / 2]),
+                                                    false, false);
+    const unsigned x = s[0], y = s[1];  // a bit cast of s[1] itself reads s[0]
+    v[m] = __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+  }
+#pragma unroll
+  for (int m = 0; m < M / 4; ++m) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, v[m]),
+                                                    __builtin_bit_cast(unsigned, v[m + M / 4]),
+                                                    false, false);
+    const unsigned x = s[0], y = s[1];
+    v[m] = __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+  }
+#pragma unroll
+  for (int m = 0; m < M / 8; ++m) {
+    const bool hi = lane & 8;
+    const float keep = hi ? v[m + M / 8] : v[m], send = hi ? v[m] : v[m + M / 8];
+    v[m] = keep + from_xor8(send);
+  }
+  if constexpr (M >= 16) {
+#pragma unroll
+    for (int m = 0; m < M / 16; ++m) {
+      const bool hi = lane & 4;
+      const float keep = hi ? v[m + M / 16] : v[m], send = hi ? v[m] : v[m + M / 16];
+      v[m] = keep + from_xor4(send);
+    }
+  } else {
+    v[0] += from_xor4(v[0]);
+  }
+}
+
+template <int K>
+struct States {
+  float v[K];
+  __device__ __forceinline__ void load(const float* p) {
+    if constexpr (K >= 4) {
+#pragma unroll
+      for (int k = 0; k < K; k += 4) {
+        const f32x4 q = *(const f32x4*)(p + k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k + e] = q[e];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] = p[k];
+    }
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    if constexpr (K >= 4) {
+#pragma unroll
+      for (int k = 0; k < K; k += 4) *(f32x4*)(p + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) p[k] = v[k];
+    }
+  }
+  __device__ __forceinline__ void load_n(const float* p, int n0, int N, float by = 1.f) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = n0 + k < N ? by * p[n0 + k] : 0.f;
+  }
+  __device__ __forceinline__ void store_n(float* p, int n0, int N) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (n0 + k < N) p[n0 + k] = v[k];
+  }
+};
+
+// As scan_place, with this lane's channel: four lanes to each.
+__device__ __forceinline__ ScanPlace quad_place(const ScanArgs& a) {
+  ScanPlace p = scan_place(a);
+  const int64_t dg = a.Dm / a.G;
+  const int64_t in = (int64_t)(blockIdx.x % (unsigned)(a.G * a.tiles) % (unsigned)a.tiles) * 64 +
+                     wave_id() * 16 + (lane_id() >> 2);
+  p.live = in < dg;
+  p.c = (int64_t)p.g * dg + (p.live ? in : 0);
+  return p;
+}
+
+// B and C of a chunk into LDS as float32, zero past N and past the sequence.
+template <typename T, int NP, int Q>
+__device__ __forceinline__ void stage_bc(const ScanArgs& a, const ScanPlace& p, int64_t end,
+                                         float (*sB)[NP], float (*sC)[NP]) {
+  const T* Bb = (const T*)a.B + p.b * a.L * a.bs + (int64_t)p.g * a.N;
+  const T* Cb = (const T*)a.C + p.b * a.L * a.cs + (int64_t)p.g * a.N;
+#pragma unroll
+  for (int i = threadIdx.x; i < Q * NP; i += 64 * kQuadWaves) {
+    const int t = i / NP, n = i % NP;
+    const int64_t q = p.t0 + t;
+    const bool in = n < a.N && q < end;
+    sB[t][n] = in ? to_f32(Bb[q * a.bs + n]) : 0.f;
+    sC[t][n] = in ? to_f32(Cb[q * a.cs + n]) : 0.f;
+  }
+}
+
+// What a lane loads of its tokens of a tile, and what comes of it.
+template <typename T, int TT>
+struct Tokens {
+  static constexpr int OWN = TT / 4;
+  T u[OWN], dt[OWN], dy[OWN], z[OWN];
+  __device__ __forceinline__ void load(const ScanArgs& a, const ScanPlace& p, const T* dyp,
+                                       int64_t t, int64_t end, int j, bool grad) {
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      const int64_t q = t + 4 * i + j;
+      u[i] = dt[i] = dy[i] = z[i] = (T)0.f;
+      if (q < end && p.live) {
+        const int64_t at = (p.b * a.L + q) * a.Dm + p.c;
+        u[i] = ((const T*)a.u)[at];
+        dt[i] = ((const T*)a.dt)[at];
+        if (grad) {
+          dy[i] = dyp[at];
+          if (a.z) z[i] = ((const T*)a.z)[(p.b * a.L + q) * a.zs + p.c];
+        }
+      }
+    }
+  }
+};
+
+template <typename T, int K>
+__global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_ends_kernel(
+    ScanArgs a, const T* __restrict__ dy, float* __restrict__ hs, float* __restrict__ decay,
+    float* __restrict__ ge) {
+  constexpr int NP = 4 * K, Q = bwd_chunk(K), TT = Q < 16 ? Q : 16, OWN = TT / 4;
+  __shared__ __align__(16) float sB[Q][NP], sC[Q][NP];
+  const int j = lane_id() & 3;
+  const ScanPlace p = quad_place(a);
+  const int64_t end = p.t1 < p.len ? p.t1 : p.len;
+  stage_bc<T, NP, Q>(a, p, end, sB, sC);
+  const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
+  States<K> A2, h, P, e;
+  A2.load_n(a.A + p.c * a.N, K * j, a.N, kLog2e);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    h.v[k] = e.v[k] = 0.f;
+    P.v[k] = 1.f;
+  }
+  Tokens<T, TT> cur, nxt;
+  cur.load(a, p, dy, p.t0, end, j, true);
+  __syncthreads();
+  for (int64_t t = p.t0; t < end; t += TT) {
+    if (t + TT < end) nxt.load(a, p, dy, t + TT, end, j, true);
+    float d[OWN], w[OWN], q[OWN];
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      d[i] = to_f32(cur.dt[i]) + bias;
+      if (a.softplus) d[i] = softplus_f32(d[i]);
+      if (t + 4 * i + j >= end) d[i] = 0.f;
+      w[i] = d[i] * to_f32(cur.u[i]);
+      q[i] = to_f32(cur.dy[i]);
+      if (a.z) {
+        const float zv = to_f32(cur.z[i]);
+        q[i] *= zv * sigmoid_f32(zv);
+      }
+    }
+    const int r0 = (int)(t - p.t0);
+    auto token = [&](int i, float dv, float wv, float qv) {
+      States<K> B, C;
+      B.load(&sB[r0 + i][K * j]);
+      C.load(&sC[r0 + i][K * j]);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float x = fast_exp2(dv * A2.v[k]);
+        h.v[k] = __builtin_fmaf(x, h.v[k], wv * B.v[k]);
+        P.v[k] *= x;
+        e.v[k] = __builtin_fmaf(P.v[k], qv * C.v[k], e.v[k]);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      token(4 * i, of_lane<0>(d[i]), of_lane<0>(w[i]), of_lane<0>(q[i]));
+      token(4 * i + 1, of_lane<1>(d[i]), of_lane<1>(w[i]), of_lane<1>(q[i]));
+      token(4 * i + 2, of_lane<2>(d[i]), of_lane<2>(w[i]), of_lane<2>(q[i]));
+      token(4 * i + 3, of_lane<3>(d[i]), of_lane<3>(w[i]), of_lane<3>(q[i]));
+    }
+    cur = nxt;
+  }
+  if (!p.live) return;
+  const int64_t row = ((p.b * a.chunks + p.chunk) * a.Dm + p.c) * NP + K * j;
+  h.store(hs + row);
+  P.store(decay + row);
+  e.store(ge + row);
+}
+
+// Over the chunks, per (batch, channel, state): hs from "reached from zero" to
+// "starts from", ge from "sent to its start" to "arrives at its end".  A
+// workgroup takes 64 columns; each of its 16 wavefronts composes its share of
+// the chunks, the shares are carried through LDS, and each wavefront walks
+// its share again.
+constexpr int kCarryWaves = 16;
+constexpr int kCarryLoads = 8;  // chunks whose loads are in flight together
+
+__global__ void __launch_bounds__(64 * kCarryWaves) scan_bwd_carry_kernel(
+    ScanArgs a, int NP, float* __restrict__ hs, const float* __restrict__ decay,
+    float* __restrict__ ge, const float* __restrict__ dfinal) {
+  __shared__ float sh[kCarryWaves][64], sg[kCarryWaves][64], sp[kCarryWaves][64];
+  const int lane = lane_id(), wave = wave_id();
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane, cols = a.Dm * NP, b = blockIdx.y;
+  const bool live = col < cols;
+  const int n = (int)(col % NP);
+  const int64_t c = col / NP;
+  const int64_t share = (a.chunks + kCarryWaves - 1) / kCarryWaves;
+  const int64_t c0 = wave * share, c1 = c0 + share < a.chunks ? c0 + share : a.chunks;
+  const int64_t base = b * a.chunks * cols + col;
+  // this share as one chunk: state reached, decay, gradient sent to its start
+  float h = 0.f, P = 1.f, e = 0.f;
+  if (live) {
+    for (int64_t q = c0; q < c1; q += kCarryLoads) {
+      float x[kCarryLoads], hl[kCarryLoads], el[kCarryLoads];
+#pragma unroll
+      for (int k = 0; k < kCarryLoads; ++k) {
+        const int64_t i = base + (q + k < c1 ? q + k : c1 - 1) * cols;
+        x[k] = decay[i];
+        hl[k] = hs[i];
+        el[k] = ge[i];
+      }
+#pragma unroll
+      for (int k = 0; k < kCarryLoads; ++k) {
+        if (q + k < c1) {
+          e = __builtin_fmaf(P, el[k], e);
+          h = __builtin_fmaf(x[k], h, hl[k]);
+          P *= x[k];
+        }
+      }
+    }
+  }
+  sh[wave][lane] = h;
+  sg[wave][lane] = e;
+  sp[wave][lane] = P;
+  __syncthreads();
+  if (!live) return;
+  const int64_t st = (b * a.Dm + c) * a.N + n;
+  float run = a.init && n < a.N ? a.init[st] : 0.f;
+  for (int w = 0; w < wave; ++w) run = __builtin_fmaf(sp[w][lane], run, sh[w][lane]);
+  float back = dfinal && n < a.N ? dfinal[st] : 0.f;
+  for (int w = kCarryWaves - 1; w > wave; --w)
+    back = __builtin_fmaf(sp[w][lane], back, sg[w][lane]);
+  for (int64_t q = c0; q < c1; q += kCarryLoads) {
+    float x[kCarryLoads], hl[kCarryLoads];
+#pragma unroll
+    for (int k = 0; k < kCarryLoads; ++k) {
+      const int64_t i = base + (q + k < c1 ? q + k : c1 - 1) * cols;
+      x[k] = decay[i];
+      hl[k] = hs[i];
+    }
+#pragma unroll
+    for (int k = 0; k < kCarryLoads; ++k) {
+      if (q + k < c1) {
+        hs[base + (q + k) * cols] = run;
+        run = __builtin_fmaf(x[k], run, hl[k]);
+      }
+    }
+  }
+  for (int64_t q = c1 - 1; q >= c0; q -= kCarryLoads) {
+    float x[kCarryLoads], el[kCarryLoads];
+#pragma unroll
+    for (int k = 0; k < kCarryLoads; ++k) {
+      const int64_t i = base + (q - k > c0 ? q - k : c0) * cols;
+      x[k] = decay[i];
+      el[k] = ge[i];
+    }
+#pragma unroll
+    for (int k = 0; k < kCarryLoads; ++k) {
+      if (q - k >= c0) {
+        ge[base + (q - k) * cols] = back;
+        back = __builtin_fmaf(x[k], back, el[k]);
+      }
+    }
+  }
+}
+
+// part_bc: [2][tiles][B][L][G][NP] parts of dB and dC, one for each channel
+// tile of a group.  part_a: [B * chunks][D * NP + 2 D] parts of dA, dD and
+// ddt_bias.
+template <typename T, int K, bool GATE>
+__global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
+    ScanArgs a, const T* __restrict__ dy, const float* __restrict__ dfinal,
+    const float* __restrict__ hs, const float* __restrict__ ge, T* __restrict__ du,
+    T* __restrict__ ddt, T* __restrict__ dz, int64_t dzs, float* __restrict__ dinit,
+    float* __restrict__ part_bc, float* __restrict__ part_a) {
+  constexpr int NP = 4 * K, Q = bwd_chunk(K), TT = bwd_tile(K), OWN = TT / 4, NT = Q / TT;
+  constexpr int M = TT * K;
+  __shared__ __align__(16) float sB[Q][NP], sC[Q][NP];
+  // per wavefront and tile: the states at its start, then its dB and dC
+  __shared__ __align__(16) float slot[kQuadWaves][NT][64 * K];
+  const int lane = lane_id(), wave = wave_id(), j = lane & 3;
+  const ScanPlace p = quad_place(a);
+  const int64_t end = p.t1 < p.len ? p.t1 : p.len;
+  stage_bc<T, NP, Q>(a, p, end, sB, sC);
+  const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
+  const float Dv = a.D ? a.D[p.c] : 0.f;
+  const int64_t srow = (p.b * a.Dm + p.c) * a.N;
+  const int64_t row = ((p.b * a.chunks + p.chunk) * a.Dm + p.c) * NP + K * j;
+  States<K> A2, h, ag, dA;
+  A2.load_n(a.A + p.c * a.N, K * j, a.N, kLog2e);
+#pragma unroll
+  for (int k = 0; k < K; ++k) h.v[k] = ag.v[k] = dA.v[k] = 0.f;
+  if (a.chunks > 1) {
+    h.load(hs + row);
+    ag.load(ge + row);
+  } else {
+    if (a.init) h.load_n(a.init + srow, K * j, a.N);
+    if (dfinal) ag.load_n(dfinal + srow, K * j, a.N);
+  }
+  const int tiles = (int)((p.t1 - p.t0 + TT - 1) / TT);
+  Tokens<T, TT> cur, nxt;
+  cur.load(a, p, dy, p.t0, end, j, tiles == 1);
+  __syncthreads();
+
+  // states at the start of every tile
+  for (int i = 0; i < tiles; ++i) {
+    h.store(&slot[wave][i][lane * K]);
+    if (i + 1 == tiles) break;
+    const int64_t t = p.t0 + (int64_t)i * TT;
+    nxt.load(a, p, dy, t + TT, end, j, i + 2 == tiles);
+    float d[OWN], w[OWN];
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      d[o] = to_f32(cur.dt[o]) + bias;
+      if (a.softplus) d[o] = softplus_f32(d[o]);
+      if (t + 4 * o + j >= end) d[o] = 0.f;
+      w[o] = d[o] * to_f32(cur.u[o]);
+    }
+    auto token = [&](int r, float dv, float wv) {
+      States<K> B;
+      B.load(&sB[i * TT + r][K * j]);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        h.v[k] = __builtin_fmaf(fast_exp2(dv * A2.v[k]), h.v[k], wv * B.v[k]);
+    };
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      token(4 * o, of_lane<0>(d[o]), of_lane<0>(w[o]));
+      token(4 * o + 1, of_lane<1>(d[o]), of_lane<1>(w[o]));
+      token(4 * o + 2, of_lane<2>(d[o]), of_lane<2>(w[o]));
+      token(4 * o + 3, of_lane<3>(d[o]), of_lane<3>(w[o]));
+    }
+    cur = nxt;
+  }
+
+  float dDs = 0.f, dbs = 0.f;
+  for (int i = tiles - 1; i >= 0; --i) {
+    const int64_t t = p.t0 + (int64_t)i * TT;
+    if (i > 0) nxt.load(a, p, dy, t - TT, end, j, true);
+    float d[OWN], w[OWN], q[OWN], raw[OWN], s1[OWN], s2[OWN], s3[OWN];
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      raw[o] = to_f32(cur.dt[o]) + bias;
+      d[o] = a.softplus ? softplus_f32(raw[o]) : raw[o];
+      if (t + 4 * o + j >= end) d[o] = 0.f;
+      w[o] = d[o] * to_f32(cur.u[o]);
+      q[o] = to_f32(cur.dy[o]);
+      if constexpr (GATE) {
+        const float zv = to_f32(cur.z[o]);
+        q[o] *= zv * sigmoid_f32(zv);
+      }
+      s1[o] = s2[o] = s3[o] = 0.f;
+    }
+    float x[TT][K], hh[TT][K];
+    States<K> h0;
+    h0.load(&slot[wave][i][lane * K]);
+    auto forward = [&](int r, float dv, float wv) {
+      States<K> B;
+      B.load(&sB[i * TT + r][K * j]);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        x[r][k] = fast_exp2(dv * A2.v[k]);
+        hh[r][k] = __builtin_fmaf(x[r][k], r ? hh[r ? r - 1 : 0][k] : h0.v[k], wv * B.v[k]);
+      }
+    };
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      forward(4 * o, of_lane<0>(d[o]), of_lane<0>(w[o]));
+      forward(4 * o + 1, of_lane<1>(d[o]), of_lane<1>(w[o]));
+      forward(4 * o + 2, of_lane<2>(d[o]), of_lane<2>(w[o]));
+      forward(4 * o + 3, of_lane<3>(d[o]), of_lane<3>(w[o]));
+    }
+    float vB[M], vC[M];
+    auto reverse = [&](int r, int o, float dv, float wv, float qv) {
+      States<K> B, C;
+      B.load(&sB[i * TT + r][K * j]);
+      C.load(&sC[i * TT + r][K * j]);
+      float gB = 0.f, gA = 0.f, y = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float g = __builtin_fmaf(qv, C.v[k], ag.v[k]);
+        vC[r * K + k] = qv * hh[r][k];
+        vB[r * K + k] = g * wv;
+        gB = __builtin_fmaf(g, B.v[k], gB);
+        ag.v[k] = x[r][k] * g;
+        const float m = ag.v[k] * (r ? hh[r ? r - 1 : 0][k] : h0.v[k]);
+        gA = __builtin_fmaf(A2.v[k], m, gA);
+        dA.v[k] = __builtin_fmaf(dv, m, dA.v[k]);
+        if constexpr (GATE) y = __builtin_fmaf(C.v[k], hh[r][k], y);
+      }
+      gB = quad_sum(gB);
+      gA = quad_sum(gA);
+      if constexpr (GATE) y = quad_sum(y);
+      if ((r & 3) == j) {
+        s1[o] = gB;
+        s2[o] = gA;
+        s3[o] = y;
+      }
+    };
+#pragma unroll
+    for (int o = OWN - 1; o >= 0; --o) {
+      reverse(4 * o + 3, o, of_lane<3>(d[o]), of_lane<3>(w[o]), of_lane<3>(q[o]));
+      reverse(4 * o + 2, o, of_lane<2>(d[o]), of_lane<2>(w[o]), of_lane<2>(q[o]));
+      reverse(4 * o + 1, o, of_lane<1>(d[o]), of_lane<1>(w[o]), of_lane<1>(q[o]));
+      reverse(4 * o, o, of_lane<0>(d[o]), of_lane<0>(w[o]), of_lane<0>(q[o]));
+    }
+    sum_channels<M>(vB, lane);
+    sum_channels<M>(vC, lane);
+    {
+      const int m = (lane >> 5) * (M / 2) + (lane >> 4 & 1) * (M / 4) + (lane >> 3 & 1) * (M / 8) +
+                    (M >= 16 ? (lane >> 2 & 1) * (M / 16) : 0);
+      float* o = &slot[wave][i][0];
+#pragma unroll
+      for (int r = 0; r < (M >= 16 ? M / 16 : 1); ++r) {
+        const int at = (m + r) / K * NP + K * j + (m + r) % K;  // [token][state]
+        o[at] = vB[r];
+        o[TT * NP + at] = vC[r];
+      }
+    }
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      const int64_t tq = t + 4 * o + j;
+      const float u = to_f32(cur.u[o]);
+      const bool in = tq < end;
+      const float dd = in ? __builtin_fmaf(s1[o], u, s2[o] * (1.f / kLog2e)) : 0.f;
+      const float dr = a.softplus ? dd * sigmoid_f32(raw[o]) : dd;
+      const float duv = __builtin_fmaf(s1[o], d[o], Dv * q[o]);
+      dDs = __builtin_fmaf(q[o], u, dDs);
+      if (p.live) dbs += dr;
+      if (p.live && tq < p.t1) {
+        const int64_t at = (p.b * a.L + tq) * a.Dm + p.c;
+        du[at] = from_f32<T>(duv);
+        ddt[at] = from_f32<T>(dr);
+        if constexpr (GATE) {
+          const float zv = to_f32(cur.z[o]), sg = sigmoid_f32(zv);
+          const float y = __builtin_fmaf(Dv, u, s3[o]);
+          dz[(p.b * a.L + tq) * dzs + p.c] =
+              from_f32<T>(to_f32(cur.dy[o]) * y * (sg * __builtin_fmaf(zv, 1.f - sg, 1.f)));
+        }
+      }
+    }
+    cur = nxt;
+  }
+
+  if (p.live) {
+    if (dinit && p.chunk == 0) ag.store_n(dinit + srow, K * j, a.N);
+    float* pa = part_a + (p.b * a.chunks + p.chunk) * (a.Dm * (a.N + 2));
+    dA.store_n(pa + p.c * a.N, K * j, a.N);
+    dDs = quad_sum(dDs);
+    dbs = quad_sum(dbs);
+    if (j == 0) {
+      pa[a.Dm * a.N + p.c] = dDs;
+      pa[a.Dm * (a.N + 1) + p.c] = dbs;
+    }
+  }
+
+  // dB and dC of the chunk: the four wavefronts' sums
+  __syncthreads();
+  const int64_t tile = blockIdx.x % (unsigned)(a.G * a.tiles) % (unsigned)a.tiles;
+  const int64_t B = gridDim.y;
+#pragma unroll
+  for (int arr = 0; arr < 2; ++arr) {
+    float* out = part_bc + ((arr * a.tiles + tile) * B + p.b) * a.L * a.G * NP;
+    for (int i = threadIdx.x; i < Q * NP; i += 64 * kQuadWaves) {
+      const int t = i / NP, n = i % NP;
+      if (p.t0 + t < p.t1) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kQuadWaves; ++w)
+          s += slot[w][t / TT][arr * TT * NP + t % TT * NP + n];
+        out[((p.t0 + t) * a.G + p.g) * NP + n] = s;
+      }
+    }
+  }
+}
+
+// dB and dC [B, L, G, N] from the channel tiles' parts.
+template <typename T>
+__global__ void __launch_bounds__(256) scan_bwd_bc_kernel(const float* __restrict__ part,
+                                                          int64_t tiles, int64_t count, int NP,
+                                                          int N, T* __restrict__ dB,
+                                                          T* __restrict__ dC) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= 2 * count) return;
+  const int64_t arr = id / count, i = id % count;
+  const int n = (int)(i % NP);
+  if (n >= N) return;
+  const float* p = part + arr * tiles * count + i;
+  float s = 0.f;
+#pragma unroll 8
+  for (int64_t t = 0; t < tiles; ++t) s += p[t * count];
+  (arr ? dC : dB)[i / NP * N + n] = from_f32<T>(s);
+}
+
+ScanSplit backward_split(const ScanDims& d) {
+  ScanSplit p;
+  p.len = bwd_chunk(bwd_k(d.N));
+  p.chunks = (d.L + p.len - 1) / p.len;
+  return p;
+}
+
+struct BwdParts {
+  size_t states, bc, sums, total;  // bytes; states: each of hs, decay, ge
+};
+
+BwdParts backward_parts(const ScanDims& d) {
+  const ScanSplit p = backward_split(d);
+  const int64_t NP = 4 * bwd_k(d.N), tiles = (d.D / d.G + 63) / 64;
+  auto round = [](int64_t n) { return ((size_t)n * sizeof(float) + 255) & ~(size_t)255; };
+  BwdParts w;
+  w.states = p.chunks > 1 ? round(d.B * p.chunks * d.D * NP) : 0;
+  w.bc = round(2 * tiles * d.B * d.L * d.G * NP);
+  w.sums = round(d.B * p.chunks * d.D * (d.N + 2));
+  w.total = 3 * w.states + w.bc + w.sums;
+  return w;
+}
+
+template <typename T, int K>
+hipError_t backward_t(const ScanDims& d, const ScanSplit& p, const ScanArgs& a, const void* dy,
+                      const float* dfinal, void* du, void* ddt, float* dA, void* dB, void* dC,
+                      float* dD, void* dz, float* ddt_bias, float* dinit, char* ws,
+                      hipStream_t s) {
+  constexpr int NP = 4 * K, threads = 64 * kQuadWaves;
+  const BwdParts w = backward_parts(d);
+  float* hs = (float*)ws;
+  float* decay = (float*)(ws + w.states);
+  float* ge = (float*)(ws + 2 * w.states);
+  float* bc = (float*)(ws + 3 * w.states);
+  float* sums = (float*)(ws + 3 * w.states + w.bc);
+  const dim3 grid((unsigned)(p.chunks * scan_channel_tiles(d)), (unsigned)d.B);
+  if (p.chunks > 1) {
+    scan_bwd_ends_kernel<T, K><<<grid, threads, 0, s>>>(a, (const T*)dy, hs, decay, ge);
+    const dim3 cols((unsigned)((d.D * NP + 63) / 64), (unsigned)d.B);
+    scan_bwd_carry_kernel<<<cols, 64 * kCarryWaves, 0, s>>>(a, NP, hs, decay, ge, dfinal);
+  }
+  if (a.z)
+    scan_bwd_main_kernel<T, K, true><<<grid, threads, 0, s>>>(
+        a, (const T*)dy, dfinal, hs, ge, (T*)du, (T*)ddt, (T*)dz, d.dzs, dinit, bc, sums);
+  else
+    scan_bwd_main_kernel<T, K, false><<<grid, threads, 0, s>>>(
+        a, (const T*)dy, dfinal, hs, ge, (T*)du, (T*)ddt, nullptr, 0, dinit, bc, sums);
+  const int64_t count = d.B * d.L * d.G * NP;
+  scan_bwd_bc_kernel<T><<<(unsigned)((2 * count + 255) / 256), 256, 0, s>>>(
+      bc, a.tiles, count, NP, a.N, (T*)dB, (T*)dC);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t ends[3] = {d.D * d.N, d.D * (d.N + 1), d.D * (d.N + 2)};
+  float* const outs[3] = {dA, dD, ddt_bias};
+  return launch_partial_sums(sums, d.B * p.chunks, d.D * (d.N + 2), ends, outs, s);
+}
+
+template <typename T, typename... R>
+hipError_t backward_by_k(const ScanDims& d, R... r) {
+  switch (bwd_k(d.N)) {
+    case 1: return backward_t<T, 1>(d, r...);
+    case 2: return backward_t<T, 2>(d, r...);
+    case 4: return backward_t<T, 4>(d, r...);
+    case 8: return backward_t<T, 8>(d, r...);
+    default: return backward_t<T, 16>(d, r...);
+  }
+}
+
+}  // namespace
+
+size_t scan_backward_bytes(const ScanDims& d) { return backward_parts(d).total; }
+
+hipError_t launch_selective_scan_backward(
+    const ScanDims& d, const void* u, const void* dt, const float* A, const void* B, const void* C,
+    const float* D, const void* z, const float* dt_bias, const float* init, const int32_t* lengths,
+    const void* dy, const float* dfinal, void* du, void* ddt, float* dA, void* dB, void* dC,
+    float* dD, void* dz, float* ddt_bias, float* dinit, void* ws, hipStream_t s) {
+  const ScanSplit p = backward_split(d);
+  const ScanArgs a = scan_args(d, p, u, dt, A, B, C, D, z, dt_bias, init, lengths);
+  return d.bf16 ? backward_by_k<bf16>(d, p, a, dy, dfinal, du, ddt, dA, dB, dC, dD, dz, ddt_bias,
+                                      dinit, (char*)ws, s)
+                : backward_by_k<float>(d, p, a, dy, dfinal, du, ddt, dA, dB, dC, dD, dz, ddt_bias,
+                                       dinit, (char*)ws, s);
+}
+
+}  // namespace m2

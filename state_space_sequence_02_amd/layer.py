@@ -320,6 +320,38 @@ def mamba2_selective_scan_forward(dims, u, dt, A, B, C, D, z, dt_bias, init_stat
           _ptr(workspace), int(workspace_bytes))
 
 
+def mamba2_selective_scan_backward_workspace_bytes(dims) -> int:
+    return int(_lib.mamba2_selective_scan_backward_workspace_bytes(ctypes.byref(dims)))
+
+
+def mamba2_selective_scan_backward(dims, u, dt, A, B, C, D, z, dt_bias, init_state, lengths, dy,
+                                   dfinal, du, ddt, dA, dB, dC, dD, dz, ddt_bias, dinit, workspace,
+                                   workspace_bytes, stream=None):
+    w = "mamba2_selective_scan_backward"
+    _scan_args(w, dims, u, dt, A, B, C, D, z, dt_bias)
+    io, full = _io(dims), (dims.batch, dims.seqlen, dims.channels)
+    state, ch = (dims.batch, dims.channels, dims.dstate), (dims.channels,)
+    bc = (dims.batch, dims.seqlen, dims.ngroups, dims.dstate)
+    for name, t in (("init_state", init_state), ("dfinal", dfinal), ("dinit", dinit)):
+        _want(w, name, t, state, _F32, optional=True)
+    _want(w, "lengths", lengths, (dims.batch,), _I32, optional=True)
+    for name, t in (("dy", dy), ("du", du), ("ddt", ddt)):
+        _want(w, name, t, full, io)
+    _want(w, "dA", dA, (dims.channels, dims.dstate), _F32)
+    _want(w, "dB", dB, bc, io)
+    _want(w, "dC", dC, bc, io)
+    _want(w, "dD", dD, ch, _F32, optional=True)
+    _want(w, "dz", dz, full, io, optional=z is None, stride=dims.dz_stride, lead=2)
+    _want(w, "ddt_bias", ddt_bias, ch, _F32, optional=True)
+    _req_bytes(w, "workspace", workspace, workspace_bytes)
+    _call(w, stream, (u, dt, A, B, C, D, z, dt_bias, init_state, lengths, dy, dfinal, du, ddt, dA,
+                      dB, dC, dD, dz, ddt_bias, dinit, workspace),
+          ctypes.byref(dims), _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+          _ptr(dt_bias), _ptr(init_state), _ptr(lengths), _ptr(dy), _ptr(dfinal), _ptr(du),
+          _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(dz), _ptr(ddt_bias),
+          _ptr(dinit), _ptr(workspace), int(workspace_bytes))
+
+
 def mamba2_selective_scan_step(dims, u, dt, A, B, C, D, z, dt_bias, state, y, stream=None):
     w = "mamba2_selective_scan_step"
     _scan_args(w, dims, u, dt, A, B, C, D, z, dt_bias, step=True)
@@ -362,6 +394,32 @@ def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, init_st
     mamba2_selective_scan_forward(dims, u, dt, A, B, C, D, z, dt_bias, init_state, lengths, y,
                                   final, workspace, n, stream)
     return y, final
+
+
+def selective_scan_backward(u, dt, A, B, C, D, z, dt_bias, init_state, dy, dfinal=None, *,
+                            softplus=True, lengths=None, workspace=None, stream=None):
+    """Gradients of selective_scan_forward: a dict with du, ddt, dA, dB, dC, dD (None
+    without D), dz (None without z), ddt_bias (None without dt_bias) and dinit."""
+    where = "selective_scan_backward"
+    dims = _scan_dims(where, u, A, B, C, z, softplus)
+    dev = u.device
+    with _owner(stream, u):
+        workspace, n = _workspace(mamba2_selective_scan_backward_workspace_bytes(dims), workspace,
+                                  u)
+        g = {"du": torch.empty(u.shape, dtype=u.dtype, device=dev),
+             "ddt": torch.empty(u.shape, dtype=u.dtype, device=dev),
+             "dA": torch.empty_like(A),
+             "dB": torch.empty(B.shape, dtype=u.dtype, device=dev),
+             "dC": torch.empty(C.shape, dtype=u.dtype, device=dev),
+             "dD": None if D is None else torch.empty_like(D),
+             "dz": None if z is None else torch.empty(u.shape, dtype=u.dtype, device=dev),
+             "ddt_bias": None if dt_bias is None else torch.empty_like(dt_bias),
+             "dinit": torch.empty((dims.batch, dims.channels, dims.dstate), dtype=_F32,
+                                  device=dev)}
+    mamba2_selective_scan_backward(dims, u, dt, A, B, C, D, z, dt_bias, init_state, lengths, dy,
+                                   dfinal, g["du"], g["ddt"], g["dA"], g["dB"], g["dC"], g["dD"],
+                                   g["dz"], g["ddt_bias"], g["dinit"], workspace, n, stream)
+    return g
 
 
 def selective_scan_step(u, dt, A, B, C, D, z, dt_bias, state, *, softplus=True, stream=None):

@@ -140,6 +140,44 @@ def scan_bounds(u, dt, A, B, C, D, z, dt_bias, init, lengths, use_softplus, dtyp
     return torch.stack(out, 1), 2 * e + U * h.abs()
 
 
+def scan_gradient_sizes(u, dt, A, B, C, D, z, dt_bias, init, lengths, use_softplus, dy, dfinal):
+    """The backward formulas with every term by its size: what a rounding's
+    relative error multiplies.  Order as the inputs."""
+    b, n, ch = u.shape
+    ns, groups = A.shape[1], B.shape[2]
+    raw = dt if dt_bias is None else dt + dt_bias
+    d = softplus(raw) if use_softplus else raw
+    lens = torch.tensor(lengths_of(lengths, b, n))
+    live = (torch.arange(n) < lens[:, None])[..., None]
+    d = torch.where(live, d, torch.zeros_like(d)).abs()
+    u, dy = (torch.where(live, v, torch.zeros_like(v)).abs() for v in (u, dy))
+    Bs, Cs = (torch.where(live[..., None], v, torch.zeros_like(v)).abs().repeat_interleave(
+        ch // groups, 2) for v in (B, C))
+    a = torch.exp(-d[..., None] * A.abs())
+    h, hs = init.abs(), [init.abs()]
+    for t in range(n):
+        h = a[:, t] * h + (d * u)[:, t, :, None] * Bs[:, t]
+        hs.append(h)
+    hs = torch.stack(hs, 1)
+    q = dy if z is None else dy * silu(z).abs()
+    g, gs = dfinal.abs(), []
+    for t in range(n - 1, -1, -1):
+        g = g + q[:, t, :, None] * Cs[:, t]
+        gs.append(g)
+        g = a[:, t] * g
+    gs = torch.stack(gs[::-1], 1)
+    m = gs * a * hs[:, :-1]
+    gB = (gs * Bs).sum(-1)
+    Ds = torch.zeros(ch, dtype=F) if D is None else D.abs()
+    ddt = (m * A.abs()).sum(-1) + gB * u
+    y = (hs[:, 1:] * Cs).sum(-1) + Ds * u
+    by_group = (b, n, groups, -1, ns)
+    return (gB * d + Ds * q, ddt, (m * d[..., None]).sum((0, 1)),
+            (gs * (d * u)[..., None]).view(by_group).sum(3),
+            (hs[:, 1:] * q[..., None]).view(by_group).sum(3), (q * u).sum((0, 1)),
+            None if z is None else 1.1 * dy * y * (1 + z.abs() / 4), ddt.sum((0, 1)), g)
+
+
 # ------------------------------------------------------------------------ norm
 
 

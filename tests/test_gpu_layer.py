@@ -307,6 +307,67 @@ def test_scan_steps_are_the_scan(m2, case):
     within("state", state, wfin, bf)
 
 
+@pytest.mark.parametrize("case", SCAN, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_scan_backward(m2, case):
+    """Bounds: the gradient of the sizes (every factor by its size, sums of sizes
+    for sums), which the roundings of all that goes into an element multiply.
+    A decay's relative error (scan_bounds) is at most 40 U at these inputs
+    where the decay itself is not negligible, and a state or gradient of a
+    state that has run over m tokens holds at most m of them; each of a
+    token's own factors adds at most 60 U.  With decays of at most exp(-|d A|)
+    what lies further back than the length of a sequence does not exist:
+    m <= L, and what is carried forward and backward meets in dA and ddt: 2 L."""
+    say(f"scan backward {case}")
+    dtype, b, n, ch, ns, g, gate, D, bias, init, lengths, sp, extra = case
+    io = TYPES[dtype]
+    t = _scan_case(case)
+    k = _scan_gpu(t, case)
+    got = m2.selective_scan_backward(**k, init_state=_cuda(t["init"]),
+                                     dy=_behind(t["dy"], lengths).cuda(),
+                                     dfinal=t["dfinal"].cuda(), softplus=sp,
+                                     lengths=_lengths(lengths))
+    torch.cuda.synchronize()
+    a = _scan64(t)
+    if a[8] is None:
+        a[8] = torch.zeros(b, ch, ns, dtype=F)
+    dy, df = to64(t["dy"]), to64(t["dfinal"])
+    want = ref.grads(lambda *v: ref.scan(*v, lengths, sp), a, (dy, df))
+    names = ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dinit")
+    sizes = ref.scan_gradient_sizes(*a, lengths, sp, dy, df)
+    most = max(ref.lengths_of(lengths, b, n))
+    for name, w, size in zip(names, want, sizes):
+        if w is None:
+            assert got[name] is None, name
+            continue
+        e = (2 * 40 * most + 60 + (b * n + 64 if name in ("dA", "dD", "ddt_bias") else 0)) * U * size
+        if name not in ("dA", "dD", "ddt_bias", "dinit"):
+            e = e + half_step(io) * (w.abs() + e)
+        within(name, got[name], w, e)
+
+
+def test_scan_gate_gradient_into_wider_rows(m2):
+    case = SCAN[3]
+    t = _scan_case(case)
+    k = _scan_gpu(t, case)
+    b, n, ch, ns, g = case[1:6]
+    lens, dy = _lengths(case[10]), t["dy"].cuda()
+    want = m2.selective_scan_backward(**k, init_state=None, dy=dy, lengths=lens)
+    wide = torch.full((b, n, 2 * ch + 3), 7.0, device="cuda")
+    dims = m2.make_scan_dims(b, n, ch, ns, g, torch.float32, z_stride=k["z"].stride(1),
+                             b_stride=k["B"].stride(1), c_stride=k["C"].stride(1),
+                             dz_stride=2 * ch + 3)
+    size = m2.mamba2_selective_scan_backward_workspace_bytes(dims)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    o = {q: torch.empty_like(v) for q, v in want.items()}
+    m2.mamba2_selective_scan_backward(dims, k["u"], k["dt"], k["A"], k["B"], k["C"], k["D"], k["z"],
+                                      k["dt_bias"], None, lens, dy, None, o["du"], o["ddt"],
+                                      o["dA"], o["dB"], o["dC"], None, wide[..., :ch], None, None,
+                                      ws, size)
+    assert torch.equal(wide[..., :ch], want["dz"]) and (wide[..., ch:] == 7).all()
+    for q in ("du", "ddt", "dA", "dB", "dC"):
+        assert torch.equal(o[q], want[q]), q
+
+
 def test_scan_final_state_over_the_initial_one(m2):
     for case in (SCAN[0], SCAN[2]):  # one chunk, several
         t = _scan_case(case)

@@ -65,6 +65,14 @@ def scan_forward(d, **over):
     return m2._lib.mamba2_selective_scan_forward(ctypes.byref(d), *a.values(), 0)
 
 
+def scan_backward(d, **over):
+    a = dict(u=OK, dt=OK, A=OK, B=OK, C=OK, D=None, z=None, bias=None, init=None, lens=None, dy=OK,
+             dfin=None, du=OK, ddt=OK, dA=OK, dB=OK, dC=OK, dD=None, dz=None, dbias=None,
+             dinit=None, ws=OK, n=BIG)
+    a.update(over)
+    return m2._lib.mamba2_selective_scan_backward(ctypes.byref(d), *a.values(), 0)
+
+
 def scan_step(d, **over):
     a = dict(u=OK, dt=OK, A=OK, B=OK, C=OK, D=None, z=None, bias=None, state=OK, y=OK)
     a.update(over)
@@ -90,7 +98,9 @@ def _refused(rc, status, word):
 
 @pytest.mark.parametrize("call,make,bytes_of", [
     (conv_forward, _conv, None), (conv_backward, _conv, "mamba2_conv1d_backward_workspace_bytes"),
-    (scan_forward, _scan, "mamba2_selective_scan_workspace_bytes"), (norm_forward, _norm, None),
+    (scan_forward, _scan, "mamba2_selective_scan_workspace_bytes"),
+    (scan_backward, _scan, "mamba2_selective_scan_backward_workspace_bytes"),
+    (norm_forward, _norm, None),
     (norm_backward, _norm, "mamba2_norm_backward_workspace_bytes")])
 def test_sizes_refused(call, make, bytes_of):
     def no(status, word, **kw):
@@ -140,8 +150,12 @@ def test_scan_sizes():
     no(scan_forward(_scan(dstate=65)), m2.MAMBA2_ERR_UNSUPPORTED, "dstate")
     no(scan_forward(_scan(b_stride=31)), m2.MAMBA2_ERR_SHAPE, "b_stride")
     no(scan_forward(_scan(c_stride=31)), m2.MAMBA2_ERR_SHAPE, "c_stride")
-    no(scan_forward(_scan(batch=60000, seqlen=1, channels=1 << 20, ngroups=1)),
-       m2.MAMBA2_ERR_UNSUPPORTED, "large")
+    for kw in (dict(batch=60000, seqlen=1, channels=1 << 20, ngroups=1),
+               dict(batch=1, seqlen=1 << 29, channels=128, ngroups=1),
+               dict(batch=1, seqlen=1 << 27, channels=4, ngroups=4)):
+        no(scan_forward(_scan(**kw)), m2.MAMBA2_ERR_UNSUPPORTED, "large")
+        no(scan_backward(_scan(**kw)), m2.MAMBA2_ERR_UNSUPPORTED, "large")
+    no(scan_backward(_scan(dz_stride=95)), m2.MAMBA2_ERR_SHAPE, "dz_stride")
     d = _scan()
     d.softplus = 2
     no(scan_forward(d), m2.MAMBA2_ERR_SHAPE, "softplus")
@@ -171,6 +185,8 @@ def test_norm_sizes():
     (conv_backward, _conv(), "x w dy0 dy1 dy2 dx dw", "b init lens dfin db dinit"),
     (conv_step, _conv(seqlen=1), "x w state y0 y1 y2", "b"),
     (scan_forward, _scan(), "u dt A B C y", "D z bias init lens fin"),
+    (scan_backward, _scan(), "u dt A B C dy du ddt dA dB dC",
+     "D z bias init lens dfin dD dbias dinit"),
     (scan_step, _scan(seqlen=1), "u dt A B C state y", "D z bias"),
     (norm_forward, _norm(), "x w y", "z b"),
     (norm_backward, _norm(), "x w dy dx dw", "db"),
@@ -186,11 +202,14 @@ def test_pointers_refused(call, dims, needed, optional):
 def test_gate_gradient_is_required_with_a_gate():
     _refused(norm_backward(_norm(), z=OK), m2.MAMBA2_ERR_NULL, "dz")
     _refused(norm_backward(_norm(), z=OK, dz=OK + 2), m2.MAMBA2_ERR_ALIGN, "dz")
+    _refused(scan_backward(_scan(), z=OK), m2.MAMBA2_ERR_NULL, "dz")
+    _refused(scan_backward(_scan(), z=OK, dz=OK + 2), m2.MAMBA2_ERR_ALIGN, "dz")
 
 
 @pytest.mark.parametrize("call,dims,bytes_of", [
     (conv_backward, _conv(), "mamba2_conv1d_backward_workspace_bytes"),
     (scan_forward, _scan(seqlen=4096), "mamba2_selective_scan_workspace_bytes"),
+    (scan_backward, _scan(seqlen=4096), "mamba2_selective_scan_backward_workspace_bytes"),
     (norm_backward, _norm(), "mamba2_norm_backward_workspace_bytes")])
 def test_workspace_refused(call, dims, bytes_of):
     n = getattr(m2, bytes_of)(dims)
