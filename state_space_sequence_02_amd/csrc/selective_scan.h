@@ -75,7 +75,9 @@ inline ScanArgs scan_args(const ScanDims& d, const ScanSplit& p, const void* u, 
 // Where this workgroup is: blockIdx.x = chunk * (G * tiles) + group * tiles +
 // tile, blockIdx.y = batch.
 struct ScanPlace {
-  int64_t b, chunk, c;  // c: this lane's channel
+  int64_t b, chunk, c;  // c: this lane's channel, c0 + at
+  int64_t c0;           // the tile's first channel
+  unsigned at;          // this lane's channel in the tile (0 where there is none)
   int g;
   bool live;            // the channel exists
   int64_t t0, t1, len;  // this chunk's tokens, and the sequence's length
@@ -89,9 +91,11 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a) {
   const unsigned r = blockIdx.x % per;
   p.g = (int)(r / (unsigned)a.tiles);
   const int64_t dg = a.Dm / a.G;
-  const int64_t in = (int64_t)(r % (unsigned)a.tiles) * 64 + lane_id();
-  p.live = in < dg;
-  p.c = (int64_t)p.g * dg + (p.live ? in : 0);
+  const int64_t first = (int64_t)(r % (unsigned)a.tiles) * 64;
+  p.live = first + lane_id() < dg;
+  p.c0 = (int64_t)p.g * dg + first;
+  p.at = p.live ? (unsigned)lane_id() : 0u;
+  p.c = p.c0 + p.at;
   p.t0 = p.chunk * a.chunk;
   p.t1 = p.t0 + a.chunk < a.L ? p.t0 + a.chunk : a.L;
   p.len = a.L;

@@ -23,12 +23,18 @@ namespace m2 {
 
 namespace {
 
-// Tokens of a tile that one thread loads: raw values of u, dt and z.
+// Tokens of a tile that one thread loads: raw values of u, dt and z, and one
+// element of B and of C.
 template <typename T, int ROWS>
 struct Held {
   T u[ROWS], dt[ROWS], z[ROWS], b, c;
 };
 
+// The vector ALU bounds this kernel, so what is the same for a wavefront stays
+// off it: a row's address is scalar and lanes add a constant 32-bit offset;
+// token counts are 32-bit and scalar; tiles inside the sequence skip the
+// masks; two tiles per round alternate the registers of the tile in hand and
+// of the one being loaded.
 template <typename T, int WV, bool GATE, bool OUT>
 __global__ void __launch_bounds__(64 * WV) scan_fwd_kernel(ScanArgs a, T* __restrict__ y,
                                                            float* __restrict__ hs,
@@ -43,20 +49,25 @@ __global__ void __launch_bounds__(64 * WV) scan_fwd_kernel(ScanArgs a, T* __rest
   __shared__ float sy[2][OUT ? WV : 1][OUT ? TT : 1][64];
   const int lane = lane_id(), wave = wave_id();
   const ScanPlace p = scan_place(a);
-  const int64_t row0 = p.b * a.L;
-  const T* ub = (const T*)a.u + row0 * a.Dm + p.c;
-  const T* db = (const T*)a.dt + row0 * a.Dm + p.c;
-  const T* zb = GATE ? (const T*)a.z + row0 * a.zs + p.c : nullptr;
-  T* yb = OUT ? y + row0 * a.Dm + p.c : nullptr;
+  const int n = (int)(p.t1 - p.t0);  // tokens of this chunk, and those that are no padding
+  const int64_t left = p.len - p.t0;
+  const int valid = left <= 0 ? 0 : left < n ? (int)left : n;
+  const int64_t row0 = p.b * a.L + p.t0;
+  const T* ub = (const T*)a.u + row0 * a.Dm + p.c0;
+  const T* db = (const T*)a.dt + row0 * a.Dm + p.c0;
+  const T* zb = GATE ? (const T*)a.z + row0 * a.zs + p.c0 : nullptr;
+  T* yb = OUT ? y + row0 * a.Dm + p.c0 : nullptr;
+  const unsigned off = p.at * (unsigned)sizeof(T);
   const int bt = threadIdx.x / NP, bn = threadIdx.x % NP;  // the element of B and C it loads
   const bool bc = bt < TT && bn < a.N;
-  const T* Bb = (const T*)a.B + row0 * a.bs + (int64_t)p.g * a.N + bn;
-  const T* Cb = (const T*)a.C + row0 * a.cs + (int64_t)p.g * a.N + bn;
+  const T* Bb = (const T*)a.B + row0 * a.bs + (int64_t)p.g * a.N;
+  const T* Cb = (const T*)a.C + row0 * a.cs + (int64_t)p.g * a.N;
+  const unsigned boff = bc ? (unsigned)(bt * (int)a.bs + bn) * (unsigned)sizeof(T) : 0u;
+  const unsigned coff = bc ? (unsigned)(bt * (int)a.cs + bn) * (unsigned)sizeof(T) : 0u;
   const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
   const float Dv = OUT && a.D ? a.D[p.c] : 0.f;
   const int n0 = kScanK * wave;
   const f32x4 A2 = load_A2(a, p.c, n0);
-  const int64_t end = p.t1 < p.len ? p.t1 : p.len;  // tokens from here on are padding
 
   f32x4 h = {0.f, 0.f, 0.f, 0.f};
   const int64_t hrow = ((p.b * a.chunks + p.chunk) * a.Dm + p.c) * NP + n0;
@@ -67,49 +78,68 @@ __global__ void __launch_bounds__(64 * WV) scan_fwd_kernel(ScanArgs a, T* __rest
       h = load_states(a.init + (p.b * a.Dm + p.c) * a.N, n0, a.N);
   }
 
-  Held<T, ROWS> cur, nxt;
-  auto load = [&](Held<T, ROWS>& r, int64_t t) {
+  auto load = [&](Held<T, ROWS>& r, int t) {
+    const int first = t + wave * ROWS;
+    if (t + TT <= valid) {
+      if (wave < LOADERS) {
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const int64_t q = t + wave * ROWS + i;
-      r.u[i] = r.dt[i] = r.z[i] = (T)0.f;
-      if (wave < LOADERS && q < end) {
-        r.u[i] = ub[q * a.Dm];
-        r.dt[i] = db[q * a.Dm];
-        if constexpr (GATE && OUT) r.z[i] = zb[q * a.zs];
+        for (int i = 0; i < ROWS; ++i) {
+          r.u[i] = lane_at(ub + (int64_t)(first + i) * a.Dm, off);
+          r.dt[i] = lane_at(db + (int64_t)(first + i) * a.Dm, off);
+          if constexpr (GATE && OUT) r.z[i] = lane_at(zb + (int64_t)(first + i) * a.zs, off);
+        }
       }
-    }
-    r.b = r.c = (T)0.f;
-    if (bc && t + bt < end) {
-      r.b = Bb[(t + bt) * a.bs];
-      if constexpr (OUT) r.c = Cb[(t + bt) * a.cs];
+      if (bc) {
+        r.b = lane_at(Bb + (int64_t)t * a.bs, boff);
+        if constexpr (OUT) r.c = lane_at(Cb + (int64_t)t * a.cs, coff);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        r.u[i] = r.dt[i] = r.z[i] = (T)0.f;
+        if (wave < LOADERS && first + i < valid) {
+          r.u[i] = lane_at(ub + (int64_t)(first + i) * a.Dm, off);
+          r.dt[i] = lane_at(db + (int64_t)(first + i) * a.Dm, off);
+          if constexpr (GATE && OUT) r.z[i] = lane_at(zb + (int64_t)(first + i) * a.zs, off);
+        }
+      }
+      r.b = r.c = (T)0.f;
+      if (bc && t + bt < valid) {
+        r.b = lane_at(Bb + (int64_t)t * a.bs, boff);
+        if constexpr (OUT) r.c = lane_at(Cb + (int64_t)t * a.cs, coff);
+      }
     }
   };
   float total = 0.f;  // sum of d over the chunk's tokens that this thread loaded
-  auto stage = [&](const Held<T, ROWS>& r, int64_t t, int buf) {
+  auto stage = [&](const Held<T, ROWS>& r, int t, int buf) {
     if (wave < LOADERS) {
+      float d[ROWS];
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) d[i] = to_f32(r.dt[i]) + bias;
+      if (a.softplus) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) d[i] = softplus_f32(d[i]);
+      }
+      if (t + TT > valid) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) d[i] = t + wave * ROWS + i < valid ? d[i] : 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        float d = to_f32(r.dt[i]) + bias;
-        if (a.softplus) d = softplus_f32(d);
-        if (t + wave * ROWS + i >= end) d = 0.f;
-        sd[buf][wave * ROWS + i][lane] = d;
-        su[buf][wave * ROWS + i][lane] = d * to_f32(r.u[i]);
-        if constexpr (!OUT) total += d;
+        sd[buf][wave * ROWS + i][lane] = d[i];
+        su[buf][wave * ROWS + i][lane] = d[i] * to_f32(r.u[i]);
+        if constexpr (!OUT) total += d[i];
       }
     }
     if (bt < TT) {
-      sB[buf][bt][bn] = to_f32(r.b);
-      if constexpr (OUT) sC[buf][bt][bn] = to_f32(r.c);
+      sB[buf][bt][bn] = bc ? to_f32(r.b) : 0.f;
+      if constexpr (OUT) sC[buf][bt][bn] = bc ? to_f32(r.c) : 0.f;
     }
   };
-
-  load(cur, p.t0);
-  stage(cur, p.t0, 0);
-  __syncthreads();
-  int buf = 0;
-  for (int64_t t = p.t0; t < p.t1; t += TT, buf ^= 1) {
-    const bool more = t + TT < p.t1;
+  // One tile: `cur` is staged in buffer `buf`, the next tile is loaded into
+  // `nxt` meanwhile and staged in the other buffer.
+  auto tile = [&](const Held<T, ROWS>& cur, Held<T, ROWS>& nxt, int t, int buf) {
+    const bool more = t + TT < n;
     if (more) load(nxt, t + TT);
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
@@ -129,21 +159,40 @@ __global__ void __launch_bounds__(64 * WV) scan_fwd_kernel(ScanArgs a, T* __rest
     __syncthreads();
     if constexpr (OUT) {
       if (wave < LOADERS && p.live) {
+        float s[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-          const int64_t q = t + wave * ROWS + i;
-          float s = Dv * to_f32(cur.u[i]);
+          s[i] = Dv * to_f32(cur.u[i]);
 #pragma unroll
-          for (int w = 0; w < WV; ++w) s += sy[buf][w][wave * ROWS + i][lane];
+          for (int w = 0; w < WV; ++w) s[i] += sy[buf][w][wave * ROWS + i][lane];
           if constexpr (GATE) {
             const float zv = to_f32(cur.z[i]);
-            s *= zv * sigmoid_f32(zv);
+            s[i] *= zv * sigmoid_f32(zv);
           }
-          if (q < p.t1) yb[q * a.Dm] = from_f32<T>(q < end ? s : 0.f);
+        }
+        const int first = t + wave * ROWS;
+        if (t + TT <= valid) {
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i)
+            lane_at(yb + (int64_t)(first + i) * a.Dm, off) = from_f32<T>(s[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i)
+            if (first + i < n)
+              lane_at(yb + (int64_t)(first + i) * a.Dm, off) =
+                  from_f32<T>(first + i < valid ? s[i] : 0.f);
         }
       }
     }
-    cur = nxt;
+  };
+
+  Held<T, ROWS> r0, r1;
+  load(r0, 0);
+  stage(r0, 0, 0);
+  __syncthreads();
+  for (int t = 0; t < n; t += 2 * TT) {
+    tile(r0, r1, t, 0);
+    if (t + TT < n) tile(r1, r0, t + TT, 1);
   }
 
   if constexpr (OUT) {
@@ -164,10 +213,12 @@ __global__ void __launch_bounds__(64 * WV) scan_fwd_kernel(ScanArgs a, T* __rest
 }
 
 // hs: the states the chunks reach from zero -> the states they start from.
-// One thread per (batch, channel, padded state).
+// One thread per (batch, channel, padded state); the loads of 16 chunks are in
+// flight together.
 __global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs a, int NP, int64_t total,
                                                          float* __restrict__ hs,
                                                          const float* __restrict__ sum_d) {
+  constexpr int LOADS = 16;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= total) return;
   const int n = (int)(id % NP);
@@ -176,10 +227,21 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs a, int NP, int
   float run = a.init && n < a.N ? a.init[(b * a.Dm + c) * a.N + n] : 0.f;
   float* hp = hs + (b * a.chunks * a.Dm + c) * NP + n;
   const float* sp = sum_d + b * a.chunks * a.Dm + c;
-  for (int64_t q = 0; q < a.chunks; ++q) {
-    const float reached = hp[q * a.Dm * NP];
-    hp[q * a.Dm * NP] = run;
-    run = __builtin_fmaf(fast_exp2(A2 * sp[q * a.Dm]), run, reached);
+  for (int64_t q = 0; q < a.chunks; q += LOADS) {
+    float reached[LOADS], d[LOADS];
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) {
+      const int64_t i = q + k < a.chunks ? q + k : a.chunks - 1;
+      reached[k] = hp[i * a.Dm * NP];
+      d[k] = sp[i * a.Dm];
+    }
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) {
+      if (q + k < a.chunks) {
+        hp[(q + k) * a.Dm * NP] = run;
+        run = __builtin_fmaf(fast_exp2(A2 * d[k]), run, reached[k]);
+      }
+    }
   }
 }
 

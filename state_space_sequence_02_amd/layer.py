@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -27,24 +28,15 @@ _ACTIVATIONS = {"none": 0, "silu": 1}
 _KINDS = {"rms": 0, "layer": 1}
 
 
-def _dtype_code(where, name, t):
-    if t.dtype is _BF16:
-        return MAMBA2_DTYPE_BF16
-    if t.dtype is _F32:
-        return MAMBA2_DTYPE_F32
-    raise Mamba2Error(MAMBA2_ERR_DTYPE, where, f"{name} is {t.dtype}, needs float32 or bfloat16")
-
-
 def _io(dims):
     return _F32 if dims.dtype == MAMBA2_DTYPE_F32 else _BF16
 
 
-def _stride(where, name, t, lead):
-    """Elements between the tokens of ``t``, whose first ``lead`` axes are tokens
-    in order; the axes after them have to be without gaps."""
-    shape, st = t.shape, t.stride()
+def _stride(where, name, shape, st, lead):
+    """Elements between the tokens of a tensor of this shape and strides, whose first
+    ``lead`` axes are tokens in order; the axes after them have to be without gaps."""
     row = 1
-    for i in range(t.dim() - 1, lead - 1, -1):
+    for i in range(len(shape) - 1, lead - 1, -1):
         if shape[i] != 1 and st[i] != row:
             raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
                               f"{name} has gaps inside a token (strides {st})")
@@ -92,7 +84,7 @@ def _want(where, name, t, shape, dtype, optional=False, stride=None, lead=0):
     tokens = 1
     for n in shape[:lead]:
         tokens *= n
-    got = _stride(where, name, t, lead)
+    got = _stride(where, name, t.shape, t.stride(), lead)
     if tokens > 1 and got != (stride or row):
         raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
                           f"{name}'s tokens are {got} elements apart, dims says {stride or row}")
@@ -114,6 +106,33 @@ def _call(where, stream, tensors, *args):
         with torch.cuda.device(index):
             status = fn(*args, stream)
     _check(status, where)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _launch(fn, where, index, stream, *args):
+    """The C call for tensors that are known to be right, on device ``index``."""
+    if stream is None:
+        stream = _raw_stream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if index == _raw_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status:
+        raise Mamba2Error(status, where)
+
+
+def _plain(t, dtype, shape, index):
+    """Whether t is a contiguous tensor of this type and shape on device ``index``.  The
+    short functions ask this first and launch at once where it holds for all inputs; else
+    the mamba2_* function looks closer and says what is wrong."""
+    return (t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == index)
 
 
 def _owner(stream, t):
@@ -208,19 +227,33 @@ def mamba2_conv1d_step(dims, x, weight, bias, state, y0, y1, y2, stream=None):
           _ptr(weight), _ptr(bias), _ptr(state), _ptr(y0), _ptr(y1), _ptr(y2))
 
 
-def _conv_dims(where, x, weight, parts, activation, step=False):
+@functools.lru_cache(maxsize=256)
+def _conv_plan(where, shape, strides, wshape, parts, activation, dtype, step):
+    """dims, the states' shape and the outputs' shapes of a call with these sizes."""
     lead = 1 if step else 2
-    if x.dim() != lead + 1 or weight.dim() != 2:
+    if len(shape) != lead + 1 or len(wshape) != 2:
         raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
-                          f"x {tuple(x.shape)} must be {lead + 1}-d and weight "
-                          f"{tuple(weight.shape)} 2-d")
-    _dtype_code(where, "x", x)
-    if parts is not None and sum(parts) != x.shape[-1]:
+                          f"x {tuple(shape)} must be {lead + 1}-d and weight {tuple(wshape)} 2-d")
+    if dtype is not _F32 and dtype is not _BF16:
+        raise Mamba2Error(MAMBA2_ERR_DTYPE, where, f"x is {dtype}, needs float32 or bfloat16")
+    C = shape[-1]
+    if parts is not None and sum(parts) != C:
         raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
-                          f"parts {tuple(parts)} do not add up to x's {x.shape[-1]} channels")
-    return make_conv_dims(x.shape[0], 1 if step else x.shape[1], x.shape[-1], weight.shape[1],
-                          parts, x.dtype, activation=activation,
-                          x_stride=_stride(where, "x", x, lead))
+                          f"parts {parts} do not add up to x's {C} channels")
+    dims = make_conv_dims(shape[0], 1 if step else shape[1], C, wshape[1], parts, dtype,
+                          activation=activation, x_stride=_stride(where, "x", shape, strides, lead))
+    return (dims, ctypes.byref(dims), torch.Size((shape[0], wshape[1] - 1, C)),
+            [torch.Size(tuple(shape[:-1]) + (p,)) for p in (parts or (C,))],
+            torch.Size((C, wshape[1])), torch.Size((C,)),
+            mamba2_conv1d_backward_workspace_bytes(dims))
+
+
+def _parts(parts):
+    return None if parts is None else tuple(parts)
+
+
+def _optional(t, dtype, shape, index):
+    return t is None or _plain(t, dtype, shape, index)
 
 
 def conv1d_forward(x, weight, bias=None, init_state=None, *, parts=None, activation="silu",
@@ -230,15 +263,22 @@ def conv1d_forward(x, weight, bias=None, init_state=None, *, parts=None, activat
     counts that add up to C; the output then comes as that many contiguous tensors,
     e.g. (H*P, G*N, G*N) for the x, B and C of an SSD call.  ``activation``: "silu"
     or "none".  Returns (y or tuple of parts, final_state[B,W-1,C])."""
-    where = "conv1d_forward"
-    dims = _conv_dims(where, x, weight, parts, activation)
-    b, L, C = x.shape
+    dims, ref, state, shapes, wshape, bshape, _ = _conv_plan(
+        "conv1d_forward", x.shape, x.stride(), weight.shape, _parts(parts), activation, x.dtype,
+        False)
     with _owner(stream, x):
-        ys = [torch.empty((b, L, p), dtype=x.dtype, device=x.device)
-              for p in ((C,) if parts is None else parts)]
-        final = torch.empty((b, dims.width - 1, C), dtype=x.dtype, device=x.device)
-    mamba2_conv1d_forward(dims, x, weight, bias, init_state, lengths,
-                          *(ys + [None] * (3 - len(ys))), final, stream)
+        ys = [x.new_empty(p) for p in shapes]
+        final = x.new_empty(state)
+    out = ys + [None] * (3 - len(ys))
+    i = x.get_device()
+    if (i >= 0 and _plain(weight, _F32, wshape, i) and _optional(bias, _F32, bshape, i)
+            and _optional(init_state, x.dtype, state, i)
+            and _optional(lengths, _I32, x.shape[:1], i)):
+        _launch(_lib.mamba2_conv1d_forward, "conv1d_forward", i, stream, ref, x.data_ptr(),
+                weight.data_ptr(), _ptr(bias), _ptr(init_state), _ptr(lengths), *map(_ptr, out),
+                final.data_ptr())
+    else:
+        mamba2_conv1d_forward(dims, x, weight, bias, init_state, lengths, *out, final, stream)
     return (ys[0] if parts is None else tuple(ys)), final
 
 
@@ -247,31 +287,47 @@ def conv1d_backward(x, weight, bias, init_state, dys, dfinal=None, *, activation
     """Gradients of conv1d_forward: ``dys`` is the gradient of y, or a tuple of the
     parts' gradients.  Returns a dict with dx, dweight, dbias (None without bias)
     and dinit."""
-    where = "conv1d_backward"
     dys = (dys,) if isinstance(dys, torch.Tensor) else tuple(dys)
-    dims = _conv_dims(where, x, weight, tuple(d.shape[-1] for d in dys), activation)
+    dims, ref, state, shapes, wshape, bshape, need = _conv_plan(
+        "conv1d_backward", x.shape, x.stride(), weight.shape, tuple(d.shape[-1] for d in dys),
+        activation, x.dtype, False)
     with _owner(stream, x):
-        workspace, n = _workspace(mamba2_conv1d_backward_workspace_bytes(dims), workspace, x)
-        g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
-             "dweight": torch.empty_like(weight),
+        workspace, n = _workspace(need, workspace, x)
+        g = {"dx": x.new_empty(x.shape), "dweight": torch.empty_like(weight),
              "dbias": None if bias is None else torch.empty_like(bias),
-             "dinit": torch.empty((x.shape[0], dims.width - 1, x.shape[2]), dtype=x.dtype,
-                                  device=x.device)}
-    mamba2_conv1d_backward(dims, x, weight, bias, init_state, lengths,
-                           *(dys + (None,) * (3 - len(dys))), dfinal, g["dx"], g["dweight"],
-                           g["dbias"], g["dinit"], workspace, n, stream)
+             "dinit": x.new_empty(state)}
+    dy3 = dys + (None,) * (3 - len(dys))
+    i = x.get_device()
+    if (i >= 0 and n >= need > 0 and _plain(weight, _F32, wshape, i)
+            and _optional(bias, _F32, bshape, i) and _optional(init_state, x.dtype, state, i)
+            and _optional(dfinal, x.dtype, state, i) and _optional(lengths, _I32, x.shape[:1], i)
+            and all(_plain(d, x.dtype, p, i) for d, p in zip(dys, shapes))
+            and workspace.is_contiguous() and workspace.get_device() == i):
+        _launch(_lib.mamba2_conv1d_backward, "conv1d_backward", i, stream, ref, x.data_ptr(),
+                weight.data_ptr(), _ptr(bias), _ptr(init_state), _ptr(lengths), *map(_ptr, dy3),
+                _ptr(dfinal), g["dx"].data_ptr(), g["dweight"].data_ptr(), _ptr(g["dbias"]),
+                g["dinit"].data_ptr(), workspace.data_ptr(), n)
+    else:
+        mamba2_conv1d_backward(dims, x, weight, bias, init_state, lengths, *dy3, dfinal, g["dx"],
+                               g["dweight"], g["dbias"], g["dinit"], workspace, n, stream)
     return g
 
 
 def conv1d_step(x, weight, bias, state, *, parts=None, activation="silu", stream=None):
     """One token of every sequence: x[B,C], ``state``[B,W-1,C] moved on in place.
     Returns y[B,C] or the tuple of its parts."""
-    where = "conv1d_step"
-    dims = _conv_dims(where, x, weight, parts, activation, step=True)
+    dims, ref, sshape, shapes, wshape, bshape, _ = _conv_plan(
+        "conv1d_step", x.shape, x.stride(), weight.shape, _parts(parts), activation, x.dtype, True)
     with _owner(stream, x):
-        ys = [torch.empty((x.shape[0], p), dtype=x.dtype, device=x.device)
-              for p in ((x.shape[1],) if parts is None else parts)]
-    mamba2_conv1d_step(dims, x, weight, bias, state, *(ys + [None] * (3 - len(ys))), stream)
+        ys = [x.new_empty(p) for p in shapes]
+    out = ys + [None] * (3 - len(ys))
+    i = x.get_device()
+    if (i >= 0 and _plain(state, x.dtype, sshape, i)
+            and _plain(weight, _F32, wshape, i) and _optional(bias, _F32, bshape, i)):
+        _launch(_lib.mamba2_conv1d_step, "conv1d_step", i, stream, ref, x.data_ptr(),
+                weight.data_ptr(), _ptr(bias), state.data_ptr(), *map(_ptr, out))
+    else:
+        mamba2_conv1d_step(dims, x, weight, bias, state, *out, stream)
     return ys[0] if parts is None else tuple(ys)
 
 
@@ -362,21 +418,45 @@ def mamba2_selective_scan_step(dims, u, dt, A, B, C, D, z, dt_bias, state, y, st
           _ptr(y))
 
 
-def _scan_dims(where, u, A, B, C, z, softplus, step=False):
+@functools.lru_cache(maxsize=256)
+def _scan_plan(where, shape, ashape, bshape, bstrides, cshape, cstrides, zstrides, dtype, softplus,
+               step):
+    """dims, the states' shape and the workspaces of a call with these sizes."""
     lead = 1 if step else 2
-    if u.dim() != lead + 1 or B.dim() != lead + 2 or C.dim() != lead + 2:
+    if len(shape) != lead + 1 or len(bshape) != lead + 2 or len(cshape) != lead + 2 or \
+            len(ashape) != 2:
         raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
-                          f"u {tuple(u.shape)} must be {lead + 1}-d, B {tuple(B.shape)} and C "
-                          f"{tuple(C.shape)} {lead + 2}-d")
-    if not isinstance(A, torch.Tensor) or A.dim() != 2:
-        raise Mamba2Error(MAMBA2_ERR_NULL if A is None else MAMBA2_ERR_SHAPE, where,
-                          "A must be a tensor [D, N]")
-    _dtype_code(where, "u", u)
-    return make_scan_dims(u.shape[0], 1 if step else u.shape[1], u.shape[-1], A.shape[1],
-                          B.shape[-2], u.dtype, softplus=softplus,
-                          z_stride=0 if z is None else _stride(where, "z", z, lead),
-                          b_stride=_stride(where, "B", B, lead),
-                          c_stride=_stride(where, "C", C, lead))
+                          f"u {tuple(shape)} must be {lead + 1}-d, A {tuple(ashape)} 2-d, B "
+                          f"{tuple(bshape)} and C {tuple(cshape)} {lead + 2}-d")
+    if dtype is not _F32 and dtype is not _BF16:
+        raise Mamba2Error(MAMBA2_ERR_DTYPE, where, f"u is {dtype}, needs float32 or bfloat16")
+    ch, n, g = shape[-1], ashape[1], bshape[-2]
+    dims = make_scan_dims(
+        shape[0], 1 if step else shape[1], ch, n, g, dtype, softplus=softplus,
+        z_stride=0 if zstrides is None else _stride(where, "z", shape, zstrides, lead),
+        b_stride=_stride(where, "B", bshape, bstrides, lead),
+        c_stride=_stride(where, "C", cshape, cstrides, lead))
+    return (dims, ctypes.byref(dims), torch.Size((shape[0], ch, n)), torch.Size((ch, n)),
+            torch.Size((ch,)), torch.Size(tuple(shape[:-1]) + (g, n)),
+            mamba2_selective_scan_workspace_bytes(dims),
+            mamba2_selective_scan_backward_workspace_bytes(dims))
+
+
+def _scan_plan_of(where, u, A, B, C, z, softplus, step=False):
+    if A is None or B is None or C is None:
+        raise Mamba2Error(MAMBA2_ERR_NULL, where, "A, B and C are required")
+    return _scan_plan(where, u.shape, A.shape, B.shape, B.stride(), C.shape, C.stride(),
+                      None if z is None else z.stride(), u.dtype, bool(softplus), step)
+
+
+def _scan_plain(i, u, dt, A, B, C, D, z, dt_bias, ashape, cshape, bcshape):
+    io = u.dtype
+    return (i >= 0 and u.is_contiguous() and _plain(dt, io, u.shape, i)
+            and _plain(A, _F32, ashape, i) and B.dtype is io and B.shape == bcshape
+            and B.get_device() == i and C.dtype is io and C.shape == bcshape
+            and C.get_device() == i and _optional(D, _F32, cshape, i)
+            and (z is None or (z.dtype is io and z.shape == u.shape and z.get_device() == i))
+            and _optional(dt_bias, _F32, cshape, i))
 
 
 def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, init_state=None, *,
@@ -385,14 +465,23 @@ def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, init_st
     with softplus=False), decays A[D,N], B and C [B,L,G,N], skip D[D] and gate z[B,L,D]
     (z, B and C may be column ranges of wider rows).  Returns (y[B,L,D],
     final_state[B,D,N])."""
-    where = "selective_scan_forward"
-    dims = _scan_dims(where, u, A, B, C, z, softplus)
+    dims, ref, state, ashape, cshape, bc, need, _ = _scan_plan_of(
+        "selective_scan_forward", u, A, B, C, z, softplus)
     with _owner(stream, u):
-        workspace, n = _workspace(mamba2_selective_scan_workspace_bytes(dims), workspace, u)
-        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
-        final = torch.empty((dims.batch, dims.channels, dims.dstate), dtype=_F32, device=u.device)
-    mamba2_selective_scan_forward(dims, u, dt, A, B, C, D, z, dt_bias, init_state, lengths, y,
-                                  final, workspace, n, stream)
+        workspace, n = _workspace(need, workspace, u)
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
+        final = u.new_empty(state, dtype=_F32)
+    i = u.get_device()
+    if (n >= need > 0 and _scan_plain(i, u, dt, A, B, C, D, z, dt_bias, ashape, cshape, bc)
+            and _optional(init_state, _F32, state, i) and _optional(lengths, _I32, u.shape[:1], i)
+            and workspace.is_contiguous() and workspace.get_device() == i):
+        _launch(_lib.mamba2_selective_scan_forward, "selective_scan_forward", i, stream, ref,
+                u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
+                _ptr(z), _ptr(dt_bias), _ptr(init_state), _ptr(lengths), y.data_ptr(),
+                final.data_ptr(), workspace.data_ptr(), n)
+    else:
+        mamba2_selective_scan_forward(dims, u, dt, A, B, C, D, z, dt_bias, init_state, lengths, y,
+                                      final, workspace, n, stream)
     return y, final
 
 
@@ -400,36 +489,51 @@ def selective_scan_backward(u, dt, A, B, C, D, z, dt_bias, init_state, dy, dfina
                             softplus=True, lengths=None, workspace=None, stream=None):
     """Gradients of selective_scan_forward: a dict with du, ddt, dA, dB, dC, dD (None
     without D), dz (None without z), ddt_bias (None without dt_bias) and dinit."""
-    where = "selective_scan_backward"
-    dims = _scan_dims(where, u, A, B, C, z, softplus)
-    dev = u.device
+    dims, ref, state, ashape, cshape, bc, _, need = _scan_plan_of(
+        "selective_scan_backward", u, A, B, C, z, softplus)
     with _owner(stream, u):
-        workspace, n = _workspace(mamba2_selective_scan_backward_workspace_bytes(dims), workspace,
-                                  u)
-        g = {"du": torch.empty(u.shape, dtype=u.dtype, device=dev),
-             "ddt": torch.empty(u.shape, dtype=u.dtype, device=dev),
-             "dA": torch.empty_like(A),
-             "dB": torch.empty(B.shape, dtype=u.dtype, device=dev),
-             "dC": torch.empty(C.shape, dtype=u.dtype, device=dev),
-             "dD": None if D is None else torch.empty_like(D),
-             "dz": None if z is None else torch.empty(u.shape, dtype=u.dtype, device=dev),
-             "ddt_bias": None if dt_bias is None else torch.empty_like(dt_bias),
-             "dinit": torch.empty((dims.batch, dims.channels, dims.dstate), dtype=_F32,
-                                  device=dev)}
-    mamba2_selective_scan_backward(dims, u, dt, A, B, C, D, z, dt_bias, init_state, lengths, dy,
-                                   dfinal, g["du"], g["ddt"], g["dA"], g["dB"], g["dC"], g["dD"],
-                                   g["dz"], g["ddt_bias"], g["dinit"], workspace, n, stream)
-    return g
+        workspace, n = _workspace(need, workspace, u)
+        du, ddt = u.new_empty(u.shape), u.new_empty(u.shape)
+        dA, dB, dC = torch.empty_like(A), u.new_empty(B.shape), u.new_empty(C.shape)
+        dD = None if D is None else torch.empty_like(D)
+        dz = None if z is None else u.new_empty(u.shape)
+        dbias = None if dt_bias is None else torch.empty_like(dt_bias)
+        dinit = u.new_empty(state, dtype=_F32)
+    i = u.get_device()
+    if (n >= need > 0 and _scan_plain(i, u, dt, A, B, C, D, z, dt_bias, ashape, cshape, bc)
+            and _plain(dy, u.dtype, u.shape, i)
+            and _optional(init_state, _F32, state, i) and _optional(dfinal, _F32, state, i)
+            and _optional(lengths, _I32, u.shape[:1], i)
+            and workspace.is_contiguous() and workspace.get_device() == i):
+        _launch(_lib.mamba2_selective_scan_backward, "selective_scan_backward", i, stream, ref,
+                u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
+                _ptr(z), _ptr(dt_bias), _ptr(init_state), _ptr(lengths), dy.data_ptr(),
+                _ptr(dfinal), du.data_ptr(), ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(),
+                dC.data_ptr(), _ptr(dD), _ptr(dz), _ptr(dbias), dinit.data_ptr(),
+                workspace.data_ptr(), n)
+    else:
+        mamba2_selective_scan_backward(dims, u, dt, A, B, C, D, z, dt_bias, init_state, lengths,
+                                       dy, dfinal, du, ddt, dA, dB, dC, dD, dz, dbias, dinit,
+                                       workspace, n, stream)
+    return {"du": du, "ddt": ddt, "dA": dA, "dB": dB, "dC": dC, "dD": dD, "dz": dz,
+            "ddt_bias": dbias, "dinit": dinit}
 
 
 def selective_scan_step(u, dt, A, B, C, D, z, dt_bias, state, *, softplus=True, stream=None):
     """One token of every sequence: u, dt, z [B,D], B, C [B,G,N]; ``state``[B,D,N] is
     updated in place.  Returns y[B,D]."""
-    where = "selective_scan_step"
-    dims = _scan_dims(where, u, A, B, C, z, softplus, step=True)
+    dims, ref, sshape, ashape, cshape, bc, _, _ = _scan_plan_of(
+        "selective_scan_step", u, A, B, C, z, softplus, True)
     with _owner(stream, u):
-        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
-    mamba2_selective_scan_step(dims, u, dt, A, B, C, D, z, dt_bias, state, y, stream)
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
+    i = u.get_device()
+    if (_plain(state, _F32, sshape, i)
+            and _scan_plain(i, u, dt, A, B, C, D, z, dt_bias, ashape, cshape, bc)):
+        _launch(_lib.mamba2_selective_scan_step, "selective_scan_step", i, stream, ref,
+                u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
+                _ptr(z), _ptr(dt_bias), state.data_ptr(), y.data_ptr())
+    else:
+        mamba2_selective_scan_step(dims, u, dt, A, B, C, D, z, dt_bias, state, y, stream)
     return y
 
 
@@ -481,32 +585,47 @@ def mamba2_norm_backward(dims, x, z, weight, dy, dx, dz, dweight, dbias, workspa
           _ptr(dbias), _ptr(workspace), int(workspace_bytes))
 
 
-def _norm_dims(where, x, z, ngroups, kind, eps):
-    """Dims, and x and z as rows (views: leading axes that are tokens in order)."""
-    if x.dim() < 2:
-        raise Mamba2Error(MAMBA2_ERR_SHAPE, where, f"x {tuple(x.shape)} must be at least 2-d")
-    _dtype_code(where, "x", x)
-    if z is not None and z.shape != x.shape:
+@functools.lru_cache(maxsize=256)
+def _norm_plan(where, shape, strides, zshape, zstrides, ngroups, kind, eps, dtype):
+    """dims, the weight's shape and the backward's workspace of a call with these sizes."""
+    if len(shape) < 2:
+        raise Mamba2Error(MAMBA2_ERR_SHAPE, where, f"x {tuple(shape)} must be at least 2-d")
+    if dtype is not _F32 and dtype is not _BF16:
+        raise Mamba2Error(MAMBA2_ERR_DTYPE, where, f"x is {dtype}, needs float32 or bfloat16")
+    if zshape is not None and zshape != shape:
         raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
-                          f"z has shape {tuple(z.shape)}, needs {tuple(x.shape)}")
-    lead = x.dim() - 1
-    dims = make_norm_dims(x.numel() // max(1, x.shape[-1]), x.shape[-1], ngroups, x.dtype,
-                          kind=kind, eps=eps, x_stride=_stride(where, "x", x, lead),
-                          z_stride=0 if z is None else _stride(where, "z", z, lead))
-    if x.dim() > 2:
-        x = x.view(dims.rows, dims.channels)
-        z = None if z is None else z.view(dims.rows, dims.channels)
-    return dims, x, z
+                          f"z has shape {tuple(zshape)}, needs {tuple(shape)}")
+    lead = len(shape) - 1
+    dims = make_norm_dims(
+        shape[:-1].numel(), shape[-1], ngroups, dtype, kind=kind, eps=eps,
+        x_stride=_stride(where, "x", shape, strides, lead),
+        z_stride=0 if zshape is None else _stride(where, "z", shape, zstrides, lead))
+    return (dims, ctypes.byref(dims), shape[-1:], mamba2_norm_backward_workspace_bytes(dims))
+
+
+def _norm_plan_of(where, x, z, ngroups, kind, eps):
+    return _norm_plan(where, x.shape, x.stride(), None if z is None else z.shape,
+                      None if z is None else z.stride(), ngroups, kind, float(eps), x.dtype)
+
+
+def _rows(t, dims):
+    return None if t is None else t.view(dims.rows, dims.channels)
 
 
 def norm_forward(x, weight, bias=None, z=None, *, ngroups=1, kind="rms", eps=1e-5, stream=None):
     """RMS norm (kind="rms") or layer norm ("layer") of x, or of x * silu(z), over
     ``ngroups`` groups of the last axis; weight and bias [D] float32.  Returns y."""
-    shape = x.shape
-    dims, x, z = _norm_dims("norm_forward", x, z, ngroups, kind, eps)
+    dims, ref, wshape, _ = _norm_plan_of("norm_forward", x, z, ngroups, kind, eps)
     with _owner(stream, x):
-        y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    mamba2_norm_forward(dims, x, z, weight, bias, y.view(dims.rows, dims.channels), stream)
+        y = x.new_empty(x.shape)
+    i = x.get_device()
+    if (i >= 0 and _plain(weight, _F32, wshape, i) and _optional(bias, _F32, wshape, i)
+            and (z is None or (z.dtype is x.dtype and z.get_device() == i))):
+        _launch(_lib.mamba2_norm_forward, "norm_forward", i, stream, ref, x.data_ptr(), _ptr(z),
+                weight.data_ptr(), _ptr(bias), y.data_ptr())
+    else:
+        mamba2_norm_forward(dims, _rows(x, dims), _rows(z, dims), weight, bias, _rows(y, dims),
+                            stream)
     return y
 
 
@@ -514,20 +633,26 @@ def norm_backward(x, weight, bias, z, dy, *, ngroups=1, kind="rms", eps=1e-5, wo
                   stream=None):
     """Gradients of norm_forward: a dict with dx, dweight, dbias (None without bias)
     and dz (None without z)."""
-    where = "norm_backward"
-    shape = x.shape
-    dims, x, z = _norm_dims(where, x, z, ngroups, kind, eps)
-    if dy.shape != shape or not dy.is_contiguous():
-        raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
-                          f"dy {tuple(dy.shape)} must be contiguous and of x's shape {tuple(shape)}")
-    rows = (dims.rows, dims.channels)
+    dims, ref, wshape, need = _norm_plan_of("norm_backward", x, z, ngroups, kind, eps)
+    if dy.shape != x.shape or not dy.is_contiguous():
+        raise Mamba2Error(MAMBA2_ERR_SHAPE, "norm_backward",
+                          f"dy {tuple(dy.shape)} must be contiguous and of x's shape "
+                          f"{tuple(x.shape)}")
     with _owner(stream, x):
-        workspace, n = _workspace(mamba2_norm_backward_workspace_bytes(dims), workspace, x)
-        g = {"dx": torch.empty(shape, dtype=x.dtype, device=x.device),
-             "dweight": torch.empty_like(weight),
+        workspace, n = _workspace(need, workspace, x)
+        g = {"dx": x.new_empty(x.shape), "dweight": torch.empty_like(weight),
              "dbias": None if bias is None else torch.empty_like(bias),
-             "dz": None if z is None else torch.empty(shape, dtype=x.dtype, device=x.device)}
-    mamba2_norm_backward(dims, x, z, weight, dy.view(rows), g["dx"].view(rows),
-                         None if z is None else g["dz"].view(rows), g["dweight"], g["dbias"],
-                         workspace, n, stream)
+             "dz": None if z is None else x.new_empty(x.shape)}
+    i = x.get_device()
+    if (i >= 0 and n >= need > 0 and _plain(weight, _F32, wshape, i)
+            and _optional(bias, _F32, wshape, i) and dy.dtype is x.dtype and dy.get_device() == i
+            and (z is None or (z.dtype is x.dtype and z.get_device() == i))
+            and workspace.is_contiguous() and workspace.get_device() == i):
+        _launch(_lib.mamba2_norm_backward, "norm_backward", i, stream, ref, x.data_ptr(), _ptr(z),
+                weight.data_ptr(), dy.data_ptr(), g["dx"].data_ptr(), _ptr(g["dz"]),
+                g["dweight"].data_ptr(), _ptr(g["dbias"]), workspace.data_ptr(), n)
+    else:
+        mamba2_norm_backward(dims, _rows(x, dims), _rows(z, dims), weight, _rows(dy, dims),
+                             _rows(g["dx"], dims), _rows(g["dz"], dims), g["dweight"], g["dbias"],
+                             workspace, n, stream)
     return g
