@@ -33,6 +33,15 @@ inline int64_t scan_channel_tiles(const ScanDims& d) {
   return d.G * ((d.D / d.G + 63) / 64);
 }
 
+// The kernels that carry states over the chunks: wavefronts of a workgroup, and
+// chunks whose loads a wavefront has in flight together.
+constexpr int kCarryWaves = 16;
+constexpr int kCarryLoads = 16;
+inline unsigned carry_waves(int64_t chunks) {
+  const int64_t w = (chunks + 7) / 8;
+  return (unsigned)(w < kCarryWaves ? w : kCarryWaves);
+}
+
 struct ScanArgs {
   const void *u, *dt, *B, *C, *z;
   const float *A, *D, *dt_bias, *init;

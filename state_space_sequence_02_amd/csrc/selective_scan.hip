@@ -212,33 +212,57 @@ __global__ void __launch_bounds__(64 * WV) scan_fwd_kernel(ScanArgs a, T* __rest
   }
 }
 
-// hs: the states the chunks reach from zero -> the states they start from.
-// One thread per (batch, channel, padded state); the loads of 16 chunks are in
-// flight together.
-__global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs a, int NP, int64_t total,
-                                                         float* __restrict__ hs,
-                                                         const float* __restrict__ sum_d) {
-  constexpr int LOADS = 16;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= total) return;
-  const int n = (int)(id % NP);
-  const int64_t c = id / NP % a.Dm, b = id / NP / a.Dm;
+// hs: the states the chunks reach from zero -> the states they start from.  A
+// workgroup takes 64 columns of (channel, padded state); each of its
+// wavefronts composes its share of the chunks into one (decay, state reached),
+// the shares are carried through LDS, and each wavefront walks its share
+// again, from registers where it is at most kCarryLoads chunks (up to 16
+// wavefronts: 256 chunks).
+__global__ void __launch_bounds__(64 * kCarryWaves) scan_carry_kernel(
+    ScanArgs a, int NP, float* __restrict__ hs, const float* __restrict__ sum_d) {
+  __shared__ float sh[kCarryWaves][64], sp[kCarryWaves][64];
+  const int lane = lane_id(), wave = wave_id(), waves = blockDim.x >> 6;
+  const int64_t cols = a.Dm * NP, col = (int64_t)blockIdx.x * 64 + lane, b = blockIdx.y;
+  const bool live = col < cols;
+  const int n = (int)(col % NP);
+  const int64_t c = live ? col / NP : 0;
   const float A2 = n < a.N ? a.A[c * a.N + n] * kLog2e : 0.f;
-  float run = a.init && n < a.N ? a.init[(b * a.Dm + c) * a.N + n] : 0.f;
-  float* hp = hs + (b * a.chunks * a.Dm + c) * NP + n;
-  const float* sp = sum_d + b * a.chunks * a.Dm + c;
-  for (int64_t q = 0; q < a.chunks; q += LOADS) {
-    float reached[LOADS], d[LOADS];
+  const int64_t share = (a.chunks + waves - 1) / waves;
+  const int64_t c0 = wave * share, c1 = c0 + share < a.chunks ? c0 + share : a.chunks;
+  float* hp = hs + b * a.chunks * cols + (live ? col : 0);
+  const float* dp = sum_d + b * a.chunks * a.Dm + c;
+  float reached[kCarryLoads], d[kCarryLoads];
+  auto load = [&](int64_t q) {
 #pragma unroll
-    for (int k = 0; k < LOADS; ++k) {
-      const int64_t i = q + k < a.chunks ? q + k : a.chunks - 1;
-      reached[k] = hp[i * a.Dm * NP];
-      d[k] = sp[i * a.Dm];
+    for (int k = 0; k < kCarryLoads; ++k) {
+      const int64_t i = q + k < c1 ? q + k : c1 - 1;
+      reached[k] = hp[i * cols];
+      d[k] = dp[i * a.Dm];
     }
+  };
+  float h = 0.f, total = 0.f;
+  for (int64_t q = c0; q < c1; q += kCarryLoads) {
+    load(q);
 #pragma unroll
-    for (int k = 0; k < LOADS; ++k) {
-      if (q + k < a.chunks) {
-        hp[(q + k) * a.Dm * NP] = run;
+    for (int k = 0; k < kCarryLoads; ++k) {
+      if (q + k < c1) {
+        h = __builtin_fmaf(fast_exp2(A2 * d[k]), h, reached[k]);
+        total += d[k];
+      }
+    }
+  }
+  sh[wave][lane] = h;
+  sp[wave][lane] = fast_exp2(A2 * total);
+  __syncthreads();
+  if (!live) return;
+  float run = a.init && n < a.N ? a.init[(b * a.Dm + c) * a.N + n] : 0.f;
+  for (int w = 0; w < wave; ++w) run = __builtin_fmaf(sp[w][lane], run, sh[w][lane]);
+  for (int64_t q = c0; q < c1; q += kCarryLoads) {
+    if (share > kCarryLoads) load(q);
+#pragma unroll
+    for (int k = 0; k < kCarryLoads; ++k) {
+      if (q + k < c1) {
+        hp[(q + k) * cols] = run;
         run = __builtin_fmaf(fast_exp2(A2 * d[k]), run, reached[k]);
       }
     }
@@ -349,9 +373,8 @@ hipError_t forward_t(const ScanDims& d, const ScanSplit& p, const ScanArgs& a, v
   const dim3 grid((unsigned)(p.chunks * scan_channel_tiles(d)), (unsigned)d.B);
   if (p.chunks > 1) {
     scan_fwd_kernel<T, WV, false, false><<<grid, 64 * WV, 0, s>>>(a, nullptr, hs, sum_d, nullptr);
-    const int64_t total = d.B * d.D * kScanK * WV;
-    scan_carry_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, kScanK * WV, total, hs,
-                                                                      sum_d);
+    const dim3 cols((unsigned)((d.D * kScanK * WV + 63) / 64), (unsigned)d.B);
+    scan_carry_kernel<<<cols, 64 * carry_waves(p.chunks), 0, s>>>(a, kScanK * WV, hs, sum_d);
   }
   if (a.z)
     scan_fwd_kernel<T, WV, true, true><<<grid, 64 * WV, 0, s>>>(a, (T*)y, hs, nullptr, final_state);

@@ -260,44 +260,40 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_ends_kernel(
 }
 
 // Over the chunks, per (batch, channel, state): hs from "reached from zero" to
-// "starts from", ge from "sent to its start" to "arrives at its end".  A
-// workgroup takes 64 columns; each of its 16 wavefronts composes its share of
-// the chunks, the shares are carried through LDS, and each wavefront walks
-// its share again.
-constexpr int kCarryWaves = 16;
-constexpr int kCarryLoads = 8;  // chunks whose loads are in flight together
-
+// "starts from", ge from "sent to its start" to "arrives at its end".  Shares
+// of the chunks as in the forward's carry.
 __global__ void __launch_bounds__(64 * kCarryWaves) scan_bwd_carry_kernel(
     ScanArgs a, int NP, float* __restrict__ hs, const float* __restrict__ decay,
     float* __restrict__ ge, const float* __restrict__ dfinal) {
   __shared__ float sh[kCarryWaves][64], sg[kCarryWaves][64], sp[kCarryWaves][64];
-  const int lane = lane_id(), wave = wave_id();
-  const int64_t col = (int64_t)blockIdx.x * 64 + lane, cols = a.Dm * NP, b = blockIdx.y;
+  const int lane = lane_id(), wave = wave_id(), waves = blockDim.x >> 6;
+  const int64_t cols = a.Dm * NP, col = (int64_t)blockIdx.x * 64 + lane, b = blockIdx.y;
   const bool live = col < cols;
   const int n = (int)(col % NP);
-  const int64_t c = col / NP;
-  const int64_t share = (a.chunks + kCarryWaves - 1) / kCarryWaves;
+  const int64_t c = live ? col / NP : 0;
+  const int64_t share = (a.chunks + waves - 1) / waves;
   const int64_t c0 = wave * share, c1 = c0 + share < a.chunks ? c0 + share : a.chunks;
-  const int64_t base = b * a.chunks * cols + col;
+  const int64_t base = b * a.chunks * cols + (live ? col : 0);
+  float x[kCarryLoads], hl[kCarryLoads], el[kCarryLoads];
+  auto load = [&](int64_t q) {
+#pragma unroll
+    for (int k = 0; k < kCarryLoads; ++k) {
+      const int64_t i = base + (q + k < c1 ? q + k : c1 - 1) * cols;
+      x[k] = decay[i];
+      hl[k] = hs[i];
+      el[k] = ge[i];
+    }
+  };
   // this share as one chunk: state reached, decay, gradient sent to its start
   float h = 0.f, P = 1.f, e = 0.f;
-  if (live) {
-    for (int64_t q = c0; q < c1; q += kCarryLoads) {
-      float x[kCarryLoads], hl[kCarryLoads], el[kCarryLoads];
+  for (int64_t q = c0; q < c1; q += kCarryLoads) {
+    load(q);
 #pragma unroll
-      for (int k = 0; k < kCarryLoads; ++k) {
-        const int64_t i = base + (q + k < c1 ? q + k : c1 - 1) * cols;
-        x[k] = decay[i];
-        hl[k] = hs[i];
-        el[k] = ge[i];
-      }
-#pragma unroll
-      for (int k = 0; k < kCarryLoads; ++k) {
-        if (q + k < c1) {
-          e = __builtin_fmaf(P, el[k], e);
-          h = __builtin_fmaf(x[k], h, hl[k]);
-          P *= x[k];
-        }
+    for (int k = 0; k < kCarryLoads; ++k) {
+      if (q + k < c1) {
+        e = __builtin_fmaf(P, el[k], e);
+        h = __builtin_fmaf(x[k], h, hl[k]);
+        P *= x[k];
       }
     }
   }
@@ -310,16 +306,10 @@ __global__ void __launch_bounds__(64 * kCarryWaves) scan_bwd_carry_kernel(
   float run = a.init && n < a.N ? a.init[st] : 0.f;
   for (int w = 0; w < wave; ++w) run = __builtin_fmaf(sp[w][lane], run, sh[w][lane]);
   float back = dfinal && n < a.N ? dfinal[st] : 0.f;
-  for (int w = kCarryWaves - 1; w > wave; --w)
-    back = __builtin_fmaf(sp[w][lane], back, sg[w][lane]);
+  for (int w = waves - 1; w > wave; --w) back = __builtin_fmaf(sp[w][lane], back, sg[w][lane]);
+  const bool again = share > kCarryLoads;  // else the share is still in registers
   for (int64_t q = c0; q < c1; q += kCarryLoads) {
-    float x[kCarryLoads], hl[kCarryLoads];
-#pragma unroll
-    for (int k = 0; k < kCarryLoads; ++k) {
-      const int64_t i = base + (q + k < c1 ? q + k : c1 - 1) * cols;
-      x[k] = decay[i];
-      hl[k] = hs[i];
-    }
+    if (again) load(q);
 #pragma unroll
     for (int k = 0; k < kCarryLoads; ++k) {
       if (q + k < c1) {
@@ -328,18 +318,13 @@ __global__ void __launch_bounds__(64 * kCarryWaves) scan_bwd_carry_kernel(
       }
     }
   }
-  for (int64_t q = c1 - 1; q >= c0; q -= kCarryLoads) {
-    float x[kCarryLoads], el[kCarryLoads];
+  const int64_t last = c0 < c1 ? c0 + (c1 - 1 - c0) / kCarryLoads * kCarryLoads : c0 - 1;
+  for (int64_t q = last; q >= c0; q -= kCarryLoads) {
+    if (again) load(q);
 #pragma unroll
-    for (int k = 0; k < kCarryLoads; ++k) {
-      const int64_t i = base + (q - k > c0 ? q - k : c0) * cols;
-      x[k] = decay[i];
-      el[k] = ge[i];
-    }
-#pragma unroll
-    for (int k = 0; k < kCarryLoads; ++k) {
-      if (q - k >= c0) {
-        ge[base + (q - k) * cols] = back;
+    for (int k = kCarryLoads - 1; k >= 0; --k) {
+      if (q + k < c1) {
+        ge[base + (q + k) * cols] = back;
         back = __builtin_fmaf(x[k], back, el[k]);
       }
     }
@@ -613,7 +598,7 @@ hipError_t backward_t(const ScanDims& d, const ScanSplit& p, const ScanArgs& a, 
   if (p.chunks > 1) {
     scan_bwd_ends_kernel<T, K><<<grid, threads, 0, s>>>(a, (const T*)dy, hs, decay, ge);
     const dim3 cols((unsigned)((d.D * NP + 63) / 64), (unsigned)d.B);
-    scan_bwd_carry_kernel<<<cols, 64 * kCarryWaves, 0, s>>>(a, NP, hs, decay, ge, dfinal);
+    scan_bwd_carry_kernel<<<cols, 64 * carry_waves(p.chunks), 0, s>>>(a, NP, hs, decay, ge, dfinal);
   }
   if (a.z)
     scan_bwd_main_kernel<T, K, true><<<grid, threads, 0, s>>>(
