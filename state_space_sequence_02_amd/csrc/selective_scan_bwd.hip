@@ -62,6 +62,14 @@ __device__ __forceinline__ float quad_sum(float v) {
   v += dpp<0x4E>(v);  // lanes 2 3 0 1
   return v;
 }
+// Lane j of the quad gets the sum over the quad of v[j]: nine operations for
+// four sums.
+__device__ __forceinline__ float quad_sums(const float (&v)[4], int j) {
+  const bool hi2 = j & 2, hi1 = j & 1;
+  const float a = (hi2 ? v[2] : v[0]) + dpp<0x4E>(hi2 ? v[0] : v[2]);
+  const float b = (hi2 ? v[3] : v[1]) + dpp<0x4E>(hi2 ? v[1] : v[3]);
+  return (hi1 ? b : a) + dpp<0xB1>(hi1 ? a : b);
+}
 // The value of the lane 8 and 4 lanes away (exclusive or) in a row of 16: a
 // rotation by 8; the mirror of 8 lanes after that of each quad.
 __device__ __forceinline__ float from_xor8(float v) { return dpp<0x128>(v); }
@@ -147,54 +155,110 @@ struct States {
 __device__ __forceinline__ ScanPlace quad_place(const ScanArgs& a) {
   ScanPlace p = scan_place(a);
   const int64_t dg = a.Dm / a.G;
-  const int64_t in = (int64_t)(blockIdx.x % (unsigned)(a.G * a.tiles) % (unsigned)a.tiles) * 64 +
-                     wave_id() * 16 + (lane_id() >> 2);
-  p.live = in < dg;
-  p.c = (int64_t)p.g * dg + (p.live ? in : 0);
+  const unsigned in = (unsigned)(wave_id() * 16 + (lane_id() >> 2));
+  p.live = p.c0 - (int64_t)p.g * dg + in < dg;
+  p.at = p.live ? in : 0u;
+  p.c = p.c0 + p.at;
   return p;
 }
 
 // B and C of a chunk into LDS as float32, zero past N and past the sequence.
 template <typename T, int NP, int Q>
-__device__ __forceinline__ void stage_bc(const ScanArgs& a, const ScanPlace& p, int64_t end,
+__device__ __forceinline__ void stage_bc(const ScanArgs& a, const ScanPlace& p, int valid,
                                          float (*sB)[NP], float (*sC)[NP]) {
-  const T* Bb = (const T*)a.B + p.b * a.L * a.bs + (int64_t)p.g * a.N;
-  const T* Cb = (const T*)a.C + p.b * a.L * a.cs + (int64_t)p.g * a.N;
+  const int64_t row0 = p.b * a.L + p.t0;
+  const T* Bb = (const T*)a.B + row0 * a.bs + (int64_t)p.g * a.N;
+  const T* Cb = (const T*)a.C + row0 * a.cs + (int64_t)p.g * a.N;
 #pragma unroll
   for (int i = threadIdx.x; i < Q * NP; i += 64 * kQuadWaves) {
     const int t = i / NP, n = i % NP;
-    const int64_t q = p.t0 + t;
-    const bool in = n < a.N && q < end;
-    sB[t][n] = in ? to_f32(Bb[q * a.bs + n]) : 0.f;
-    sC[t][n] = in ? to_f32(Cb[q * a.cs + n]) : 0.f;
+    const bool in = n < a.N && t < valid;
+    sB[t][n] = in ? to_f32(Bb[t * a.bs + n]) : 0.f;
+    sC[t][n] = in ? to_f32(Cb[t * a.cs + n]) : 0.f;
   }
 }
 
-// What a lane loads of its tokens of a tile, and what comes of it.
-template <typename T, int TT>
+// A lane's rows of a chunk: scalar addresses of the chunk's first token, this
+// lane's offsets in bytes from the first token of a group of four, and the
+// counts of tokens (those of the chunk; those that are no padding).
+template <typename T>
+struct Rows {
+  const T *u, *dt, *dy, *z;
+  unsigned off, zoff;
+  int n, valid, j;
+  bool whole;  // every lane of the workgroup has a channel
+  __device__ __forceinline__ Rows(const ScanArgs& a, const ScanPlace& p, const T* dyp, int jj) {
+    const int64_t row0 = p.b * a.L + p.t0;
+    u = (const T*)a.u + row0 * a.Dm + p.c0;
+    dt = (const T*)a.dt + row0 * a.Dm + p.c0;
+    dy = dyp + row0 * a.Dm + p.c0;
+    z = (const T*)a.z + row0 * a.zs + p.c0;  // not read where there is none
+    j = jj;
+    off = ((unsigned)j * (unsigned)a.Dm + p.at) * (unsigned)sizeof(T);
+    zoff = ((unsigned)j * (unsigned)a.zs + p.at) * (unsigned)sizeof(T);
+    n = (int)(p.t1 - p.t0);
+    const int64_t left = p.len - p.t0;
+    valid = left <= 0 ? 0 : left < n ? (int)left : n;
+    whole = p.c0 + 64 <= (int64_t)(p.g + 1) * (a.Dm / a.G);
+  }
+};
+
+// What a lane loads of its tokens of a tile (token 4 i + j of it).
+template <typename T, int TT, bool GATE>
 struct Tokens {
   static constexpr int OWN = TT / 4;
   T u[OWN], dt[OWN], dy[OWN], z[OWN];
-  __device__ __forceinline__ void load(const ScanArgs& a, const ScanPlace& p, const T* dyp,
-                                       int64_t t, int64_t end, int j, bool grad) {
+  template <bool GRAD>
+  __device__ __forceinline__ void load(const ScanArgs& a, const ScanPlace& p, const Rows<T>& r,
+                                       int t) {
+    auto one = [&](int i) {
+      const int64_t at = (int64_t)(t + 4 * i) * a.Dm;
+      u[i] = lane_at(r.u + at, r.off);
+      dt[i] = lane_at(r.dt + at, r.off);
+      if constexpr (GRAD) {
+        dy[i] = lane_at(r.dy + at, r.off);
+        if constexpr (GATE) z[i] = lane_at(r.z + (int64_t)(t + 4 * i) * a.zs, r.zoff);
+      }
+    };
+    if (r.whole && t + TT <= r.valid) {
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) one(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) {
+        u[i] = dt[i] = dy[i] = z[i] = (T)0.f;
+        if (p.live && t + 4 * i + r.j < r.valid) one(i);
+      }
+    }
+  }
+  // the time steps, zero where there is no token
+  __device__ __forceinline__ void steps(const ScanArgs& a, const Rows<T>& r, int t, float bias,
+                                        float (&raw)[OWN], float (&d)[OWN]) const {
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) d[i] = raw[i] = to_f32(dt[i]) + bias;
+    if (a.softplus) {
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) d[i] = softplus_f32(raw[i]);
+    }
+    if (t + TT > r.valid) {
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) d[i] = t + 4 * i + r.j < r.valid ? d[i] : 0.f;
+    }
+  }
+  // dy, times silu(z) with a gate
+  __device__ __forceinline__ void grads(float (&q)[OWN]) const {
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
-      const int64_t q = t + 4 * i + j;
-      u[i] = dt[i] = dy[i] = z[i] = (T)0.f;
-      if (q < end && p.live) {
-        const int64_t at = (p.b * a.L + q) * a.Dm + p.c;
-        u[i] = ((const T*)a.u)[at];
-        dt[i] = ((const T*)a.dt)[at];
-        if (grad) {
-          dy[i] = dyp[at];
-          if (a.z) z[i] = ((const T*)a.z)[(p.b * a.L + q) * a.zs + p.c];
-        }
+      q[i] = to_f32(dy[i]);
+      if constexpr (GATE) {
+        const float zv = to_f32(z[i]);
+        q[i] *= zv * sigmoid_f32(zv);
       }
     }
   }
 };
 
-template <typename T, int K>
+template <typename T, int K, bool GATE>
 __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_ends_kernel(
     ScanArgs a, const T* __restrict__ dy, float* __restrict__ hs, float* __restrict__ decay,
     float* __restrict__ ge) {
@@ -202,8 +266,8 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_ends_kernel(
   __shared__ __align__(16) float sB[Q][NP], sC[Q][NP];
   const int j = lane_id() & 3;
   const ScanPlace p = quad_place(a);
-  const int64_t end = p.t1 < p.len ? p.t1 : p.len;
-  stage_bc<T, NP, Q>(a, p, end, sB, sC);
+  const Rows<T> r(a, p, dy, j);
+  stage_bc<T, NP, Q>(a, p, r.valid, sB, sC);
   const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
   States<K> A2, h, P, e;
   A2.load_n(a.A + p.c * a.N, K * j, a.N, kLog2e);
@@ -212,29 +276,20 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_ends_kernel(
     h.v[k] = e.v[k] = 0.f;
     P.v[k] = 1.f;
   }
-  Tokens<T, TT> cur, nxt;
-  cur.load(a, p, dy, p.t0, end, j, true);
+  Tokens<T, TT, GATE> cur, nxt;
+  cur.template load<true>(a, p, r, 0);
   __syncthreads();
-  for (int64_t t = p.t0; t < end; t += TT) {
-    if (t + TT < end) nxt.load(a, p, dy, t + TT, end, j, true);
-    float d[OWN], w[OWN], q[OWN];
+  for (int t = 0; t < r.valid; t += TT) {
+    if (t + TT < r.valid) nxt.template load<true>(a, p, r, t + TT);
+    float raw[OWN], d[OWN], w[OWN], q[OWN];
+    cur.steps(a, r, t, bias, raw, d);
+    cur.grads(q);
 #pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      d[i] = to_f32(cur.dt[i]) + bias;
-      if (a.softplus) d[i] = softplus_f32(d[i]);
-      if (t + 4 * i + j >= end) d[i] = 0.f;
-      w[i] = d[i] * to_f32(cur.u[i]);
-      q[i] = to_f32(cur.dy[i]);
-      if (a.z) {
-        const float zv = to_f32(cur.z[i]);
-        q[i] *= zv * sigmoid_f32(zv);
-      }
-    }
-    const int r0 = (int)(t - p.t0);
+    for (int i = 0; i < OWN; ++i) w[i] = d[i] * to_f32(cur.u[i]);
     auto token = [&](int i, float dv, float wv, float qv) {
       States<K> B, C;
-      B.load(&sB[r0 + i][K * j]);
-      C.load(&sC[r0 + i][K * j]);
+      B.load(&sB[t + i][K * j]);
+      C.load(&sC[t + i][K * j]);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const float x = fast_exp2(dv * A2.v[k]);
@@ -347,8 +402,8 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
   __shared__ __align__(16) float slot[kQuadWaves][NT][64 * K];
   const int lane = lane_id(), wave = wave_id(), j = lane & 3;
   const ScanPlace p = quad_place(a);
-  const int64_t end = p.t1 < p.len ? p.t1 : p.len;
-  stage_bc<T, NP, Q>(a, p, end, sB, sC);
+  const Rows<T> rows(a, p, dy, j);
+  stage_bc<T, NP, Q>(a, p, rows.valid, sB, sC);
   const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
   const float Dv = a.D ? a.D[p.c] : 0.f;
   const int64_t srow = (p.b * a.Dm + p.c) * a.N;
@@ -364,25 +419,21 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
     if (a.init) h.load_n(a.init + srow, K * j, a.N);
     if (dfinal) ag.load_n(dfinal + srow, K * j, a.N);
   }
-  const int tiles = (int)((p.t1 - p.t0 + TT - 1) / TT);
-  Tokens<T, TT> cur, nxt;
-  cur.load(a, p, dy, p.t0, end, j, tiles == 1);
+  const int tiles = (rows.n + TT - 1) / TT;
+  Tokens<T, TT, GATE> cur, nxt;
+  cur.template load<false>(a, p, rows, 0);
   __syncthreads();
 
   // states at the start of every tile
   for (int i = 0; i < tiles; ++i) {
     h.store(&slot[wave][i][lane * K]);
     if (i + 1 == tiles) break;
-    const int64_t t = p.t0 + (int64_t)i * TT;
-    nxt.load(a, p, dy, t + TT, end, j, i + 2 == tiles);
-    float d[OWN], w[OWN];
+    const int t = i * TT;
+    nxt.template load<false>(a, p, rows, t + TT);
+    float raw[OWN], d[OWN], w[OWN];
+    cur.steps(a, rows, t, bias, raw, d);
 #pragma unroll
-    for (int o = 0; o < OWN; ++o) {
-      d[o] = to_f32(cur.dt[o]) + bias;
-      if (a.softplus) d[o] = softplus_f32(d[o]);
-      if (t + 4 * o + j >= end) d[o] = 0.f;
-      w[o] = d[o] * to_f32(cur.u[o]);
-    }
+    for (int o = 0; o < OWN; ++o) w[o] = d[o] * to_f32(cur.u[o]);
     auto token = [&](int r, float dv, float wv) {
       States<K> B;
       B.load(&sB[i * TT + r][K * j]);
@@ -401,23 +452,19 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
   }
 
   float dDs = 0.f, dbs = 0.f;
+  cur.template load<true>(a, p, rows, (tiles - 1) * TT);
+  T* dub = du + (p.b * a.L + p.t0) * a.Dm + p.c0;
+  T* ddtb = ddt + (p.b * a.L + p.t0) * a.Dm + p.c0;
+  T* dzb = GATE ? dz + (p.b * a.L + p.t0) * dzs + p.c0 : nullptr;
+  const unsigned dzoff = ((unsigned)j * (unsigned)dzs + p.at) * (unsigned)sizeof(T);
   for (int i = tiles - 1; i >= 0; --i) {
-    const int64_t t = p.t0 + (int64_t)i * TT;
-    if (i > 0) nxt.load(a, p, dy, t - TT, end, j, true);
+    const int t = i * TT;
+    if (i > 0) nxt.template load<true>(a, p, rows, t - TT);
     float d[OWN], w[OWN], q[OWN], raw[OWN], s1[OWN], s2[OWN], s3[OWN];
+    cur.steps(a, rows, t, bias, raw, d);
+    cur.grads(q);
 #pragma unroll
-    for (int o = 0; o < OWN; ++o) {
-      raw[o] = to_f32(cur.dt[o]) + bias;
-      d[o] = a.softplus ? softplus_f32(raw[o]) : raw[o];
-      if (t + 4 * o + j >= end) d[o] = 0.f;
-      w[o] = d[o] * to_f32(cur.u[o]);
-      q[o] = to_f32(cur.dy[o]);
-      if constexpr (GATE) {
-        const float zv = to_f32(cur.z[o]);
-        q[o] *= zv * sigmoid_f32(zv);
-      }
-      s1[o] = s2[o] = s3[o] = 0.f;
-    }
+    for (int o = 0; o < OWN; ++o) w[o] = d[o] * to_f32(cur.u[o]);
     float x[TT][K], hh[TT][K];
     States<K> h0;
     h0.load(&slot[wave][i][lane * K]);
@@ -438,7 +485,8 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
       forward(4 * o + 3, of_lane<3>(d[o]), of_lane<3>(w[o]));
     }
     float vB[M], vC[M];
-    auto reverse = [&](int r, int o, float dv, float wv, float qv) {
+    float gBs[4], gAs[4], ys[4];
+    auto reverse = [&](int r, float dv, float wv, float qv) {
       States<K> B, C;
       B.load(&sB[i * TT + r][K * j]);
       C.load(&sC[i * TT + r][K * j]);
@@ -455,21 +503,19 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
         dA.v[k] = __builtin_fmaf(dv, m, dA.v[k]);
         if constexpr (GATE) y = __builtin_fmaf(C.v[k], hh[r][k], y);
       }
-      gB = quad_sum(gB);
-      gA = quad_sum(gA);
-      if constexpr (GATE) y = quad_sum(y);
-      if ((r & 3) == j) {
-        s1[o] = gB;
-        s2[o] = gA;
-        s3[o] = y;
-      }
+      gBs[r & 3] = gB;
+      gAs[r & 3] = gA;
+      ys[r & 3] = y;
     };
 #pragma unroll
     for (int o = OWN - 1; o >= 0; --o) {
-      reverse(4 * o + 3, o, of_lane<3>(d[o]), of_lane<3>(w[o]), of_lane<3>(q[o]));
-      reverse(4 * o + 2, o, of_lane<2>(d[o]), of_lane<2>(w[o]), of_lane<2>(q[o]));
-      reverse(4 * o + 1, o, of_lane<1>(d[o]), of_lane<1>(w[o]), of_lane<1>(q[o]));
-      reverse(4 * o, o, of_lane<0>(d[o]), of_lane<0>(w[o]), of_lane<0>(q[o]));
+      reverse(4 * o + 3, of_lane<3>(d[o]), of_lane<3>(w[o]), of_lane<3>(q[o]));
+      reverse(4 * o + 2, of_lane<2>(d[o]), of_lane<2>(w[o]), of_lane<2>(q[o]));
+      reverse(4 * o + 1, of_lane<1>(d[o]), of_lane<1>(w[o]), of_lane<1>(q[o]));
+      reverse(4 * o, of_lane<0>(d[o]), of_lane<0>(w[o]), of_lane<0>(q[o]));
+      s1[o] = quad_sums(gBs, j);
+      s2[o] = quad_sums(gAs, j);
+      s3[o] = GATE ? quad_sums(ys, j) : 0.f;
     }
     sum_channels<M>(vB, lane);
     sum_channels<M>(vC, lane);
@@ -484,26 +530,33 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
         o[TT * NP + at] = vC[r];
       }
     }
+    const bool full = rows.whole && t + TT <= rows.valid;
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
-      const int64_t tq = t + 4 * o + j;
+      const int tq = t + 4 * o + j;
       const float u = to_f32(cur.u[o]);
-      const bool in = tq < end;
-      const float dd = in ? __builtin_fmaf(s1[o], u, s2[o] * (1.f / kLog2e)) : 0.f;
-      const float dr = a.softplus ? dd * sigmoid_f32(raw[o]) : dd;
+      float dd = __builtin_fmaf(s1[o], u, s2[o] * (1.f / kLog2e));
+      if (a.softplus) dd *= sigmoid_f32(raw[o]);
+      float dzv = 0.f;
+      if constexpr (GATE) {
+        const float zv = to_f32(cur.z[o]), sg = sigmoid_f32(zv);
+        dzv = to_f32(cur.dy[o]) * __builtin_fmaf(Dv, u, s3[o]) *
+              (sg * __builtin_fmaf(zv, 1.f - sg, 1.f));
+      }
       const float duv = __builtin_fmaf(s1[o], d[o], Dv * q[o]);
       dDs = __builtin_fmaf(q[o], u, dDs);
-      if (p.live) dbs += dr;
-      if (p.live && tq < p.t1) {
-        const int64_t at = (p.b * a.L + tq) * a.Dm + p.c;
-        du[at] = from_f32<T>(duv);
-        ddt[at] = from_f32<T>(dr);
-        if constexpr (GATE) {
-          const float zv = to_f32(cur.z[o]), sg = sigmoid_f32(zv);
-          const float y = __builtin_fmaf(Dv, u, s3[o]);
-          dz[(p.b * a.L + tq) * dzs + p.c] =
-              from_f32<T>(to_f32(cur.dy[o]) * y * (sg * __builtin_fmaf(zv, 1.f - sg, 1.f)));
-        }
+      const int64_t at = (int64_t)(t + 4 * o) * a.Dm, zat = (int64_t)(t + 4 * o) * dzs;
+      if (full) {
+        dbs += dd;
+        lane_at(dub + at, rows.off) = from_f32<T>(duv);
+        lane_at(ddtb + at, rows.off) = from_f32<T>(dd);
+        if constexpr (GATE) lane_at(dzb + zat, dzoff) = from_f32<T>(dzv);
+      } else if (p.live && tq < rows.n) {
+        if (tq >= rows.valid) dd = 0.f;
+        dbs += dd;
+        lane_at(dub + at, rows.off) = from_f32<T>(duv);
+        lane_at(ddtb + at, rows.off) = from_f32<T>(dd);
+        if constexpr (GATE) lane_at(dzb + zat, dzoff) = from_f32<T>(dzv);
       }
     }
     cur = nxt;
@@ -596,7 +649,10 @@ hipError_t backward_t(const ScanDims& d, const ScanSplit& p, const ScanArgs& a, 
   float* sums = (float*)(ws + 3 * w.states + w.bc);
   const dim3 grid((unsigned)(p.chunks * scan_channel_tiles(d)), (unsigned)d.B);
   if (p.chunks > 1) {
-    scan_bwd_ends_kernel<T, K><<<grid, threads, 0, s>>>(a, (const T*)dy, hs, decay, ge);
+    if (a.z)
+      scan_bwd_ends_kernel<T, K, true><<<grid, threads, 0, s>>>(a, (const T*)dy, hs, decay, ge);
+    else
+      scan_bwd_ends_kernel<T, K, false><<<grid, threads, 0, s>>>(a, (const T*)dy, hs, decay, ge);
     const dim3 cols((unsigned)((d.D * NP + 63) / 64), (unsigned)d.B);
     scan_bwd_carry_kernel<<<cols, 64 * carry_waves(p.chunks), 0, s>>>(a, NP, hs, decay, ge, dfinal);
   }
