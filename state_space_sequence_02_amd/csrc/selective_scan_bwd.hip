@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kQuadWaves = 4;
 
-// Tokens of a tile whose states and decays stay in registers, and tokens of a
+// Tokens of a tile whose states and decays stay in registers, and the longest
 // chunk: the workgroup's tile-start states take at most 64 KB of LDS.
 constexpr int bwd_tile(int K) { return K <= 4 ? 8 : 4; }
 constexpr int bwd_chunk(int K) { return K <= 4 ? 64 : K == 8 ? 32 : 16; }
@@ -113,6 +113,17 @@ __device__ __forceinline__ void sum_channels(float (&v)[M], int lane) {
   } else {
     v[0] += from_xor4(v[0]);
   }
+}
+
+// Stores what sum_channels left: v[m] is state m % K of this lane's quarter,
+// token m / K of rows of 4 K states.
+template <int M, int K>
+__device__ __forceinline__ void store_sums(float* rows, const float (&v)[M], int lane) {
+  const int m = (lane >> 5) * (M / 2) + (lane >> 4 & 1) * (M / 4) + (lane >> 3 & 1) * (M / 8) +
+                (M >= 16 ? (lane >> 2 & 1) * (M / 16) : 0);
+#pragma unroll
+  for (int r = 0; r < (M >= 16 ? M / 16 : 1); ++r)
+    rows[(m + r) / K * (4 * K) + K * (lane & 3) + (m + r) % K] = v[r];
 }
 
 template <int K>
@@ -396,7 +407,7 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
     T* __restrict__ ddt, T* __restrict__ dz, int64_t dzs, float* __restrict__ dinit,
     float* __restrict__ part_bc, float* __restrict__ part_a) {
   constexpr int NP = 4 * K, Q = bwd_chunk(K), TT = bwd_tile(K), OWN = TT / 4, NT = Q / TT;
-  constexpr int M = TT * K;
+  constexpr int GT = K == 1 ? 8 : 4, M = GT * K;  // tokens and values summed over channels at once
   __shared__ __align__(16) float sB[Q][NP], sC[Q][NP];
   // per wavefront and tile: the states at its start, then its dB and dC
   __shared__ __align__(16) float slot[kQuadWaves][NT][64 * K];
@@ -425,9 +436,8 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
   __syncthreads();
 
   // states at the start of every tile
-  for (int i = 0; i < tiles; ++i) {
+  for (int i = 0; i + 1 < tiles; ++i) {
     h.store(&slot[wave][i][lane * K]);
-    if (i + 1 == tiles) break;
     const int t = i * TT;
     nxt.template load<false>(a, p, rows, t + TT);
     float raw[OWN], d[OWN], w[OWN];
@@ -450,6 +460,7 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
     }
     cur = nxt;
   }
+  h.store(&slot[wave][tiles - 1][lane * K]);
 
   float dDs = 0.f, dbs = 0.f;
   cur.template load<true>(a, p, rows, (tiles - 1) * TT);
@@ -465,47 +476,59 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
     cur.grads(q);
 #pragma unroll
     for (int o = 0; o < OWN; ++o) w[o] = d[o] * to_f32(cur.u[o]);
-    float x[TT][K], hh[TT][K];
+    // forward: states and decays of the tile, dC and the gate's sum C h
+    float x[TT][K], hh[TT][K], v[M];
     States<K> h0;
     h0.load(&slot[wave][i][lane * K]);
-    auto forward = [&](int r, float dv, float wv) {
-      States<K> B;
-      B.load(&sB[i * TT + r][K * j]);
+    float* res = &slot[wave][i][0];  // dB and dC take the place of the states just read
+    float part[4];
+    auto forward = [&](int r, float dv, float wv, float qv) {
+      States<K> B, C;
+      B.load(&sB[t + r][K * j]);
+      C.load(&sC[t + r][K * j]);
+      float y = 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         x[r][k] = fast_exp2(dv * A2.v[k]);
         hh[r][k] = __builtin_fmaf(x[r][k], r ? hh[r ? r - 1 : 0][k] : h0.v[k], wv * B.v[k]);
+        v[r % GT * K + k] = qv * hh[r][k];
+        if constexpr (GATE) y = __builtin_fmaf(C.v[k], hh[r][k], y);
       }
+      part[r & 3] = y;
     };
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
-      forward(4 * o, of_lane<0>(d[o]), of_lane<0>(w[o]));
-      forward(4 * o + 1, of_lane<1>(d[o]), of_lane<1>(w[o]));
-      forward(4 * o + 2, of_lane<2>(d[o]), of_lane<2>(w[o]));
-      forward(4 * o + 3, of_lane<3>(d[o]), of_lane<3>(w[o]));
+      forward(4 * o, of_lane<0>(d[o]), of_lane<0>(w[o]), of_lane<0>(q[o]));
+      forward(4 * o + 1, of_lane<1>(d[o]), of_lane<1>(w[o]), of_lane<1>(q[o]));
+      forward(4 * o + 2, of_lane<2>(d[o]), of_lane<2>(w[o]), of_lane<2>(q[o]));
+      forward(4 * o + 3, of_lane<3>(d[o]), of_lane<3>(w[o]), of_lane<3>(q[o]));
+      s3[o] = GATE ? quad_sums(part, j) : 0.f;
+      if ((4 * o + 4) % GT == 0) {
+        sum_channels<M>(v, lane);
+        store_sums<M, K>(res + (TT + 4 * o + 4 - GT) * NP, v, lane);
+      }
+      // keep the next tokens' LDS reads behind: hoisted, they cost registers that spill
+      __builtin_amdgcn_sched_barrier(0);
     }
-    float vB[M], vC[M];
-    float gBs[4], gAs[4], ys[4];
+    // reverse: the gradients of the states
+    float gAs[4];
     auto reverse = [&](int r, float dv, float wv, float qv) {
       States<K> B, C;
-      B.load(&sB[i * TT + r][K * j]);
-      C.load(&sC[i * TT + r][K * j]);
-      float gB = 0.f, gA = 0.f, y = 0.f;
+      B.load(&sB[t + r][K * j]);
+      C.load(&sC[t + r][K * j]);
+      float gB = 0.f, gA = 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const float g = __builtin_fmaf(qv, C.v[k], ag.v[k]);
-        vC[r * K + k] = qv * hh[r][k];
-        vB[r * K + k] = g * wv;
+        v[r % GT * K + k] = g * wv;
         gB = __builtin_fmaf(g, B.v[k], gB);
         ag.v[k] = x[r][k] * g;
         const float m = ag.v[k] * (r ? hh[r ? r - 1 : 0][k] : h0.v[k]);
         gA = __builtin_fmaf(A2.v[k], m, gA);
         dA.v[k] = __builtin_fmaf(dv, m, dA.v[k]);
-        if constexpr (GATE) y = __builtin_fmaf(C.v[k], hh[r][k], y);
       }
-      gBs[r & 3] = gB;
+      part[r & 3] = gB;
       gAs[r & 3] = gA;
-      ys[r & 3] = y;
     };
 #pragma unroll
     for (int o = OWN - 1; o >= 0; --o) {
@@ -513,22 +536,13 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
       reverse(4 * o + 2, of_lane<2>(d[o]), of_lane<2>(w[o]), of_lane<2>(q[o]));
       reverse(4 * o + 1, of_lane<1>(d[o]), of_lane<1>(w[o]), of_lane<1>(q[o]));
       reverse(4 * o, of_lane<0>(d[o]), of_lane<0>(w[o]), of_lane<0>(q[o]));
-      s1[o] = quad_sums(gBs, j);
+      s1[o] = quad_sums(part, j);
       s2[o] = quad_sums(gAs, j);
-      s3[o] = GATE ? quad_sums(ys, j) : 0.f;
-    }
-    sum_channels<M>(vB, lane);
-    sum_channels<M>(vC, lane);
-    {
-      const int m = (lane >> 5) * (M / 2) + (lane >> 4 & 1) * (M / 4) + (lane >> 3 & 1) * (M / 8) +
-                    (M >= 16 ? (lane >> 2 & 1) * (M / 16) : 0);
-      float* o = &slot[wave][i][0];
-#pragma unroll
-      for (int r = 0; r < (M >= 16 ? M / 16 : 1); ++r) {
-        const int at = (m + r) / K * NP + K * j + (m + r) % K;  // [token][state]
-        o[at] = vB[r];
-        o[TT * NP + at] = vC[r];
+      if (4 * o % GT == 0) {
+        sum_channels<M>(v, lane);
+        store_sums<M, K>(res + 4 * o * NP, v, lane);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
     const bool full = rows.whole && t + TT <= rows.valid;
 #pragma unroll
@@ -612,9 +626,14 @@ __global__ void __launch_bounds__(256) scan_bwd_bc_kernel(const float* __restric
   (arr ? dC : dB)[i / NP * N + n] = from_f32<T>(s);
 }
 
+// Chunks: as long as the tile-start states fit in LDS (a chunk's states are
+// written and read five times), shorter, down to 16 tokens, where that leaves
+// fewer than two workgroups for each CU.
 ScanSplit backward_split(const ScanDims& d) {
   ScanSplit p;
   p.len = bwd_chunk(bwd_k(d.N));
+  const int64_t per = d.B * scan_channel_tiles(d);
+  while (p.len > 16 && per * ((d.L + p.len - 1) / p.len) < 512) p.len /= 2;
   p.chunks = (d.L + p.len - 1) / p.len;
   return p;
 }
