@@ -30,9 +30,7 @@ template <int TEAM, int N>
 __device__ __forceinline__ void team_sum(float (&s)[N], float (*red)[N]) {
   constexpr int LANES = TEAM < 64 ? TEAM : 64;
 #pragma unroll
-  for (int off = LANES / 2; off >= 1; off >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] += __shfl_xor(s[i], off, 64);
+  for (int i = 0; i < N; ++i) s[i] = lanes_sum<LANES>(s[i]);
   if constexpr (TEAM > 64) {
     const int wave = wave_id();
     if (lane_id() == 0) {
@@ -176,13 +174,19 @@ __global__ void __launch_bounds__(block_of(TEAM)) norm_bwd_kernel(
     rx.load(x + r * xs + g0, lane, TEAM, live ? Dg : 0);
     rg.load(dy + r * D + g0, lane, TEAM, live ? Dg : 0);
     if constexpr (GATE) rz.load(z + r * zs + g0, lane, TEAM, live ? Dg : 0);
-    float v[NV][V];
+    // the gate's sigmoid is used twice: kept where there are registers for it
+    constexpr bool KEEP = GATE && NV * V <= 8;
+    float v[NV][V], sg[KEEP ? NV : 1][KEEP ? V : 1];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         v[k][e] = rx.at(k, e);
-        if constexpr (GATE) v[k][e] *= rz.at(k, e) * sigmoid_f32(rz.at(k, e));
+        if constexpr (GATE) {
+          const float q = sigmoid_f32(rz.at(k, e));
+          v[k][e] *= rz.at(k, e) * q;
+          if constexpr (KEEP) sg[k][e] = q;
+        }
       }
     if (layer) {
       float s[1] = {0.f};
@@ -222,7 +226,12 @@ __global__ void __launch_bounds__(block_of(TEAM)) norm_bwd_kernel(
         db[k][e] += g;
         const float dv = rstd * (__builtin_fmaf(g, wv[k][e], -md) - xh * mx);
         if constexpr (GATE) {
-          const float zv = rz.at(k, e), q = sigmoid_f32(zv);
+          const float zv = rz.at(k, e);
+          float q;
+          if constexpr (KEEP)
+            q = sg[k][e];
+          else
+            q = sigmoid_f32(zv);
           gx[k][e] = dv * (zv * q);
           gz[k][e] = dv * rx.at(k, e) * (q * __builtin_fmaf(zv, 1.f - q, 1.f));
         } else {

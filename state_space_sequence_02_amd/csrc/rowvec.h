@@ -30,6 +30,41 @@ struct RowVec<T, 1> {
   typedef T type;
 };
 
+// Lanes of a row of 16 rotated by CTRL - 0x120, or another DPP control.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// v + the same of the lane whose number differs in bit 5 (4): the two halves
+// of a register pair that is exchanged with itself.
+__device__ __forceinline__ float add_xor32(float v) {
+  const unsigned u = __builtin_bit_cast(unsigned, v);
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned x = s[0], y = s[1];  // a bit cast of s[1] itself reads s[0]
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ float add_xor16(float v) {
+  const unsigned u = __builtin_bit_cast(unsigned, v);
+  const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned x = s[0], y = s[1];
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// Sum over LANES = 32 or 64 neighbouring lanes, in each of them: rotations
+// inside the rows of 16, then the exchanges between rows.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += dpp<0x121>(v);
+  v += dpp<0x122>(v);
+  v += dpp<0x124>(v);
+  v += dpp<0x128>(v);
+  v = add_xor16(v);
+  if constexpr (LANES == 64) v = add_xor32(v);
+  return v;
+}
+
 // Element of a row whose address is the same for the wavefront, at this lane's
 // offset in bytes: one instruction with a scalar address and a 32-bit offset.
 template <typename T>

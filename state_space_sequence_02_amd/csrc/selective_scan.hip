@@ -19,6 +19,8 @@
 // from their start states.  That computes the exponentials twice.
 #include "selective_scan.h"
 
+#include <type_traits>
+
 namespace m2 {
 
 namespace {
@@ -269,52 +271,63 @@ __global__ void __launch_bounds__(64 * kCarryWaves) scan_carry_kernel(
   }
 }
 
-// One token.  State rows of 4 LPR states: LPR lanes of 16 bytes each.
-template <typename T, int LPR>
-__global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a, int64_t rows, float* state,
+// One token.  State rows of 4 LPR states: LPR lanes of 16 bytes each.  A thread
+// takes its channel's row of SEQS sequences: their states are all requested
+// before the first is used, and the channel's parameters are read once.
+template <typename T, int LPR, int SEQS>
+__global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a, int B, float* state,
                                                         T* __restrict__ y, int wide) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = id / LPR;
-  if (row >= rows) return;  // the lanes of a row leave together
-  const int n0 = (int)(id % LPR) * 4;
-  const int64_t b = row / a.Dm, c = row % a.Dm;
-  const int64_t g = c / (a.Dm / a.G);
-  float* sp = state + row * a.N + n0;
-  f32x4 h = *(const f32x4*)sp;
-  const f32x4 A4 = *(const f32x4*)(a.A + c * a.N + n0);
-  const T* Bp = (const T*)a.B + b * a.bs + g * a.N + n0;
-  const T* Cp = (const T*)a.C + b * a.cs + g * a.N + n0;
-  float Bv[4], Cv[4];
-  if (wide) {
-    load_row<T, 4>(Bp, Bv);
-    load_row<T, 4>(Cp, Cv);
-  } else {
+  const int n0 = (int)(threadIdx.x % LPR) * 4;
+  const unsigned c = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  if (c >= (unsigned)a.Dm) return;  // the lanes of a row leave together
+  const unsigned g = a.G == 1 ? 0u : c / (unsigned)(a.Dm / a.G);
+  const int b0 = (int)blockIdx.y * SEQS;
+  f32x4 h[SEQS];
+#pragma unroll
+  for (int i = 0; i < SEQS; ++i) {
+    h[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (b0 + i < B) h[i] = *(const f32x4*)(state + ((int64_t)(b0 + i) * a.Dm + c) * a.N + n0);
+  }
+  const f32x4 A2 = *(const f32x4*)(a.A + (int64_t)c * a.N + n0) * kLog2e;
+  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, Dv = a.D ? a.D[c] : 0.f;
+#pragma unroll
+  for (int i = 0; i < SEQS; ++i) {
+    const int64_t b = b0 + i, row = b * a.Dm + c;
+    if (b >= B) return;
+    const T* Bp = (const T*)a.B + b * a.bs + (int64_t)g * a.N + n0;
+    const T* Cp = (const T*)a.C + b * a.cs + (int64_t)g * a.N + n0;
+    float Bv[4], Cv[4];
+    if (wide) {
+      load_row<T, 4>(Bp, Bv);
+      load_row<T, 4>(Cp, Cv);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        Bv[k] = to_f32(Bp[k]);
+        Cv[k] = to_f32(Cp[k]);
+      }
+    }
+    const float u = to_f32(((const T*)a.u)[row]);
+    float d = to_f32(((const T*)a.dt)[row]) + bias;
+    if (a.softplus) d = softplus_f32(d);
+    const float w = d * u;
+    float s = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      Bv[k] = to_f32(Bp[k]);
-      Cv[k] = to_f32(Cp[k]);
+      h[i][k] = __builtin_fmaf(fast_exp2(d * A2[k]), h[i][k], w * Bv[k]);
+      s = __builtin_fmaf(h[i][k], Cv[k], s);
     }
-  }
-  const float u = to_f32(((const T*)a.u)[row]);
-  float d = to_f32(((const T*)a.dt)[row]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
-  if (a.softplus) d = softplus_f32(d);
-  const float w = d * u, d2 = d * kLog2e;
-  float s = 0.f;
+    *(f32x4*)(state + row * a.N + n0) = h[i];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    h[k] = __builtin_fmaf(fast_exp2(d2 * A4[k]), h[k], w * Bv[k]);
-    s = __builtin_fmaf(h[k], Cv[k], s);
-  }
-  *(f32x4*)sp = h;
-#pragma unroll
-  for (int off = 1; off < LPR; off <<= 1) s += __shfl_xor(s, off, 64);
-  if (n0 == 0) {
-    if (a.D) s = __builtin_fmaf(a.D[c], u, s);
-    if (a.z) {
-      const float zv = to_f32(((const T*)a.z)[b * a.zs + c]);
-      s *= zv * sigmoid_f32(zv);
+    for (int off = 1; off < LPR; off <<= 1) s += __shfl_xor(s, off, 64);
+    if (n0 == 0) {
+      s = __builtin_fmaf(Dv, u, s);
+      if (a.z) {
+        const float zv = to_f32(((const T*)a.z)[b * a.zs + c]);
+        s *= zv * sigmoid_f32(zv);
+      }
+      y[row] = from_f32<T>(s);
     }
-    y[row] = from_f32<T>(s);
   }
 }
 
@@ -400,18 +413,32 @@ size_t states_bytes(const ScanDims& d, const ScanSplit& p) {
   return (size_t)(d.B * p.chunks * d.D * kScanK * scan_waves(d.N)) * sizeof(float);
 }
 
+constexpr int kStepSeqs = 2;
+constexpr int64_t kStepThreads = 1 << 19;
+
 template <typename T>
 hipError_t step_t(const ScanDims& d, const ScanArgs& a, float* state, void* y, hipStream_t s) {
   const int64_t rows = d.B * d.D;
   const int wide = d.bs % 4 == 0 && d.cs % 4 == 0;
-  auto grid = [&](int lanes) { return (unsigned)((rows * lanes + 255) / 256); };
+  auto vec = [&](auto lanes) {
+    constexpr int LPR = decltype(lanes)::value, SEQS = kStepSeqs;
+    const unsigned x = (unsigned)((d.D + 256 / LPR - 1) / (256 / LPR));
+    if (rows * LPR >= kStepThreads)
+      scan_step_kernel<T, LPR, SEQS><<<dim3(x, (unsigned)((d.B + SEQS - 1) / SEQS)), 256, 0, s>>>(
+          a, (int)d.B, state, (T*)y, wide);
+    else
+      scan_step_kernel<T, LPR, 1>
+          <<<dim3(x, (unsigned)d.B), 256, 0, s>>>(a, (int)d.B, state, (T*)y, wide);
+  };
   switch (d.N) {
-    case 4: scan_step_kernel<T, 1><<<grid(1), 256, 0, s>>>(a, rows, state, (T*)y, wide); break;
-    case 8: scan_step_kernel<T, 2><<<grid(2), 256, 0, s>>>(a, rows, state, (T*)y, wide); break;
-    case 16: scan_step_kernel<T, 4><<<grid(4), 256, 0, s>>>(a, rows, state, (T*)y, wide); break;
-    case 32: scan_step_kernel<T, 8><<<grid(8), 256, 0, s>>>(a, rows, state, (T*)y, wide); break;
-    case 64: scan_step_kernel<T, 16><<<grid(16), 256, 0, s>>>(a, rows, state, (T*)y, wide); break;
-    default: scan_step_any_kernel<T><<<grid(16), 256, 0, s>>>(a, rows, state, (T*)y); break;
+    case 4: vec(std::integral_constant<int, 1>()); break;
+    case 8: vec(std::integral_constant<int, 2>()); break;
+    case 16: vec(std::integral_constant<int, 4>()); break;
+    case 32: vec(std::integral_constant<int, 8>()); break;
+    case 64: vec(std::integral_constant<int, 16>()); break;
+    default:
+      scan_step_any_kernel<T><<<(unsigned)((rows * 16 + 255) / 256), 256, 0, s>>>(a, rows, state,
+                                                                                  (T*)y);
   }
   return hipGetLastError();
 }

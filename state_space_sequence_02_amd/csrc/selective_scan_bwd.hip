@@ -49,11 +49,6 @@ inline int bwd_k(int64_t N) {
   return k;
 }
 
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __builtin_bit_cast(
-      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
 // The value of lane J of this lane's quad.
 template <int J>
 __device__ __forceinline__ float of_lane(float v) { return dpp<J * 0x55>(v); }
