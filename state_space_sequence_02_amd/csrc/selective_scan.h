@@ -1,13 +1,16 @@
 // What the forward and the backward pass of the selective scan share: how a
-// workgroup divides channels and states, its tile of tokens, and the loads
-// that turn a tile of the inputs into float32 values in LDS.
+// workgroup divides channels and states, and the loads of a tile of tokens.
 //
-// A workgroup takes 64 neighbouring channels of one group (lane = channel)
-// and every state of them: wavefront w of WV holds states 4 w .. 4 w + 3 of
-// its lane's channel in registers.  B and C are then the same for all lanes
-// and come from LDS as broadcast reads of 16 bytes; the recurrence runs down
-// the tokens with no exchange between lanes, and only the sum over a
-// channel's states crosses wavefronts, through LDS, once per token.
+// A lane holds K of a channel's 4 K states, four lanes (a quad) a channel, a
+// wavefront 16 channels, a workgroup 64 neighbouring channels of one group.
+// Each lane of a quad loads every fourth token of its channel and hands the
+// values to the other three through the quad permutation that an
+// instruction's operand can carry; sums over a channel's states cross the
+// quad the same way.  B and C are the same for all channels and come from LDS
+// as float32.  So the recurrence runs down the tokens with no exchange between
+// wavefronts.  The vector ALU bounds these kernels: what is the same for a
+// wavefront stays off it (scalar row addresses with constant 32-bit lane
+// offsets, 32-bit token counts), and tiles inside a sequence skip the masks.
 #pragma once
 
 #include "launch.h"
@@ -15,18 +18,15 @@
 
 namespace m2 {
 
-constexpr int kScanK = 4;           // states of one channel in one lane
-constexpr int kScanMaxState = 64;   // 16 wavefronts
+constexpr int kScanMaxState = 64;  // K = 16
+constexpr int kQuadWaves = 4;
 
-// Wavefronts of a workgroup for N states: 1, 2, 4, 8 or 16.
-inline int scan_waves(int64_t N) {
-  int w = 1;
-  while (w * kScanK < N) w *= 2;
-  return w;
+// States per lane for N states of a channel: 1, 2, 4, 8 or 16.
+inline int scan_k(int64_t N) {
+  int k = 1;
+  while (4 * k < N) k *= 2;
+  return k;
 }
-
-// Tokens of a tile: what 64 KB of LDS hold twice over.
-constexpr int scan_tile(int wv) { return wv <= 4 ? 16 : wv == 8 ? 8 : 4; }
 
 // Workgroups along the channels: tiles never straddle two groups.
 inline int64_t scan_channel_tiles(const ScanDims& d) {
@@ -81,8 +81,8 @@ inline ScanArgs scan_args(const ScanDims& d, const ScanSplit& p, const void* u, 
   return a;
 }
 
-// Where this workgroup is: blockIdx.x = chunk * (G * tiles) + group * tiles +
-// tile, blockIdx.y = batch.
+// Where this workgroup is (blockIdx.x = chunk * (G * tiles) + group * tiles +
+// tile, blockIdx.y = batch) and this lane's channel.
 struct ScanPlace {
   int64_t b, chunk, c;  // c: this lane's channel, c0 + at
   int64_t c0;           // the tile's first channel
@@ -101,9 +101,10 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a) {
   p.g = (int)(r / (unsigned)a.tiles);
   const int64_t dg = a.Dm / a.G;
   const int64_t first = (int64_t)(r % (unsigned)a.tiles) * 64;
-  p.live = first + lane_id() < dg;
+  const unsigned in = (unsigned)(wave_id() * 16 + (lane_id() >> 2));
+  p.live = first + in < dg;
   p.c0 = (int64_t)p.g * dg + first;
-  p.at = p.live ? (unsigned)lane_id() : 0u;
+  p.at = p.live ? in : 0u;
   p.c = p.c0 + p.at;
   p.t0 = p.chunk * a.chunk;
   p.t1 = p.t0 + a.chunk < a.L ? p.t0 + a.chunk : a.L;
@@ -115,24 +116,145 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a) {
   return p;
 }
 
-// A state array of the caller's, [.., N] float32: four states of one channel,
-// zero past N.
-__device__ __forceinline__ f32x4 load_states(const float* p, int n0, int N) {
-  f32x4 v;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = n0 + k < N ? p[n0 + k] : 0.f;
+// The value of lane J of this lane's quad.
+template <int J>
+__device__ __forceinline__ float of_lane(float v) { return dpp<J * 0x55>(v); }
+__device__ __forceinline__ float quad_sum(float v) {
+  v += dpp<0xB1>(v);  // lanes 1 0 3 2
+  v += dpp<0x4E>(v);  // lanes 2 3 0 1
   return v;
 }
-__device__ __forceinline__ void store_states(float* p, int n0, int N, const f32x4& v) {
+// Lane j of the quad gets the sum over the quad of v[j]: nine operations for
+// four sums.
+__device__ __forceinline__ float quad_sums(const float (&v)[4], int j) {
+  const bool hi2 = j & 2, hi1 = j & 1;
+  const float a = (hi2 ? v[2] : v[0]) + dpp<0x4E>(hi2 ? v[0] : v[2]);
+  const float b = (hi2 ? v[3] : v[1]) + dpp<0x4E>(hi2 ? v[1] : v[3]);
+  return (hi1 ? b : a) + dpp<0xB1>(hi1 ? a : b);
+}
+// K states of one channel.  load / store: rows padded to 4 K states, 16-byte
+// aligned; load_n / store_n: the caller's rows of N, zero past them.
+template <int K>
+struct States {
+  float v[K];
+  __device__ __forceinline__ void load(const float* p) {
+    if constexpr (K >= 4) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (n0 + k < N) p[n0 + k] = v[k];
+      for (int k = 0; k < K; k += 4) {
+        const f32x4 q = *(const f32x4*)(p + k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k + e] = q[e];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] = p[k];
+    }
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    if constexpr (K >= 4) {
+#pragma unroll
+      for (int k = 0; k < K; k += 4) *(f32x4*)(p + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) p[k] = v[k];
+    }
+  }
+  __device__ __forceinline__ void load_n(const float* p, int n0, int N, float by = 1.f) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = n0 + k < N ? by * p[n0 + k] : 0.f;
+  }
+  __device__ __forceinline__ void store_n(float* p, int n0, int N) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (n0 + k < N) p[n0 + k] = v[k];
+  }
+};
+
+// A lane's rows of a chunk: scalar addresses of the chunk's first token, this
+// lane's offsets in bytes from the first token of a group of four, and the
+// counts of tokens (those of the chunk; those that are no padding).
+template <typename T>
+struct Rows {
+  const T *u, *dt, *dy, *z;
+  unsigned off, zoff;
+  int n, valid, j;
+  bool whole;  // every lane of the workgroup has a channel
+  __device__ __forceinline__ Rows(const ScanArgs& a, const ScanPlace& p, const T* dyp, int jj) {
+    const int64_t row0 = p.b * a.L + p.t0;
+    u = (const T*)a.u + row0 * a.Dm + p.c0;
+    dt = (const T*)a.dt + row0 * a.Dm + p.c0;
+    dy = dyp + row0 * a.Dm + p.c0;
+    z = (const T*)a.z + row0 * a.zs + p.c0;  // not read where there is none
+    j = jj;
+    off = ((unsigned)j * (unsigned)a.Dm + p.at) * (unsigned)sizeof(T);
+    zoff = ((unsigned)j * (unsigned)a.zs + p.at) * (unsigned)sizeof(T);
+    n = (int)(p.t1 - p.t0);
+    const int64_t left = p.len - p.t0;
+    valid = left <= 0 ? 0 : left < n ? (int)left : n;
+    whole = p.c0 + 64 <= (int64_t)(p.g + 1) * (a.Dm / a.G);
+  }
+};
+
+// A token count that the compiler takes as new: addresses formed from it stay
+// scalar.  Else it turns every row's address of a loop into a 64-bit pointer
+// in vector registers, advanced by vector instructions.
+__device__ __forceinline__ int fresh(int t) {
+  asm("" : "+s"(t));
+  return t;
 }
 
-// A[c, n] log2(e) of this lane's four states (0 past N: such a state stays
-// what it is, zero).
-__device__ __forceinline__ f32x4 load_A2(const ScanArgs& a, int64_t c, int n0) {
-  return load_states(a.A + c * a.N, n0, a.N) * kLog2e;
-}
+// What a lane loads of its tokens of a tile (token 4 i + j of it).
+template <typename T, int TT, bool GATE>
+struct Tokens {
+  static constexpr int OWN = TT / 4;
+  T u[OWN], dt[OWN], dy[OWN], z[OWN];
+  template <bool DY, bool Z>
+  __device__ __forceinline__ void load(const ScanArgs& a, const ScanPlace& p, const Rows<T>& r,
+                                       int t0) {
+    const int t = fresh(t0);
+    auto one = [&](int i) {
+      const int64_t at = (int64_t)(t + 4 * i) * a.Dm;
+      u[i] = lane_at(r.u + at, r.off);
+      dt[i] = lane_at(r.dt + at, r.off);
+      if constexpr (DY) dy[i] = lane_at(r.dy + at, r.off);
+      if constexpr (Z && GATE) z[i] = lane_at(r.z + (int64_t)(t + 4 * i) * a.zs, r.zoff);
+    };
+    if (r.whole && t + TT <= r.valid) {
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) one(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) {
+        u[i] = dt[i] = dy[i] = z[i] = (T)0.f;
+        if (p.live && t + 4 * i + r.j < r.valid) one(i);
+      }
+    }
+  }
+  // the time steps, zero where there is no token
+  __device__ __forceinline__ void steps(const ScanArgs& a, const Rows<T>& r, int t, float bias,
+                                        float (&raw)[OWN], float (&d)[OWN]) const {
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) d[i] = raw[i] = to_f32(dt[i]) + bias;
+    if (a.softplus) {
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) d[i] = softplus_f32(raw[i]);
+    }
+    if (t + TT > r.valid) {
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) d[i] = t + 4 * i + r.j < r.valid ? d[i] : 0.f;
+    }
+  }
+  // dy, times silu(z) with a gate
+  __device__ __forceinline__ void grads(float (&q)[OWN]) const {
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      q[i] = to_f32(dy[i]);
+      if constexpr (GATE) {
+        const float zv = to_f32(z[i]);
+        q[i] *= zv * sigmoid_f32(zv);
+      }
+    }
+  }
+};
 
 }  // namespace m2

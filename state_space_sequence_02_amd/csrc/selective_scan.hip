@@ -6,10 +6,11 @@
 //
 // The decays of a token differ by state, so no matrix product forms the
 // interaction of two tokens as in the SSD; what is left is one step per
-// (token, channel, state): an exponential and four float32 operations, eight
-// issue slots on the vector ALU (the exponential takes four), against 6-8
-// bytes of HBM traffic per (token, channel).  At 16 states it is bound by
-// the vector ALU.
+// (token, channel, state): an exponential and four float32 operations.  The
+// counters put a wavefront's exponential at two issue slots of the vector ALU
+// and the others at one: six slots, against 6-8 bytes of HBM traffic per
+// (token, channel).  At 16 states the vector ALU bounds it; a token's own work
+// (softplus, gate, loads, the sum over states) adds 2.5 slots per state.
 //
 // Where batch * channels fill the device, one pass walks all tokens.  Where
 // they do not (a long prompt, a small batch) the sequence is cut into
@@ -25,191 +26,140 @@ namespace m2 {
 
 namespace {
 
-// Tokens of a tile that one thread loads: raw values of u, dt and z, and one
-// element of B and of C.
-template <typename T, int ROWS>
-struct Held {
-  T u[ROWS], dt[ROWS], z[ROWS], b, c;
-};
+constexpr int kStageTokens = 32;  // tokens whose B and C are in LDS at once (twice)
+constexpr int fwd_tile(int K) { return K <= 8 ? 16 : 8; }
 
-// The vector ALU bounds this kernel, so what is the same for a wavefront stays
-// off it: a row's address is scalar and lanes add a constant 32-bit offset;
-// token counts are 32-bit and scalar; tiles inside the sequence skip the
-// masks; two tiles per round alternate the registers of the tile in hand and
-// of the one being loaded.
-template <typename T, int WV, bool GATE, bool OUT>
-__global__ void __launch_bounds__(64 * WV) scan_fwd_kernel(ScanArgs a, T* __restrict__ y,
-                                                           float* __restrict__ hs,
-                                                           float* __restrict__ sum_d,
-                                                           float* final_state) {
-  constexpr int TT = scan_tile(WV);
-  constexpr int ROWS = TT > WV ? TT / WV : 1;
-  constexpr int NP = kScanK * WV;  // states, padded
-  constexpr int LOADERS = TT / ROWS;  // wavefronts that load rows
-  __shared__ float sd[2][TT][64], su[2][TT][64];
-  __shared__ __align__(16) float sB[2][TT][NP], sC[2][OUT ? TT : 1][NP];
-  __shared__ float sy[2][OUT ? WV : 1][OUT ? TT : 1][64];
-  const int lane = lane_id(), wave = wave_id();
+// OUT: the outputs, from the chunks' start states; else the states that the
+// chunks reach from zero and their sums of d.
+template <typename T, int K, bool GATE, bool OUT>
+__global__ void __launch_bounds__(64 * kQuadWaves) scan_fwd_kernel(
+    ScanArgs a, T* __restrict__ y, float* __restrict__ hs, float* __restrict__ sum_d,
+    float* final_state) {
+  constexpr int NP = 4 * K, TT = fwd_tile(K), OWN = TT / 4, S = kStageTokens;
+  constexpr int THREADS = 64 * kQuadWaves, EACH = S * NP > THREADS ? S * NP / THREADS : 1;
+  __shared__ __align__(16) float sB[2][S][NP], sC[2][OUT ? S : 1][NP];
+  const int j = lane_id() & 3;
   const ScanPlace p = scan_place(a);
-  const int n = (int)(p.t1 - p.t0);  // tokens of this chunk, and those that are no padding
-  const int64_t left = p.len - p.t0;
-  const int valid = left <= 0 ? 0 : left < n ? (int)left : n;
-  const int64_t row0 = p.b * a.L + p.t0;
-  const T* ub = (const T*)a.u + row0 * a.Dm + p.c0;
-  const T* db = (const T*)a.dt + row0 * a.Dm + p.c0;
-  const T* zb = GATE ? (const T*)a.z + row0 * a.zs + p.c0 : nullptr;
-  T* yb = OUT ? y + row0 * a.Dm + p.c0 : nullptr;
-  const unsigned off = p.at * (unsigned)sizeof(T);
-  const int bt = threadIdx.x / NP, bn = threadIdx.x % NP;  // the element of B and C it loads
-  const bool bc = bt < TT && bn < a.N;
-  const T* Bb = (const T*)a.B + row0 * a.bs + (int64_t)p.g * a.N;
-  const T* Cb = (const T*)a.C + row0 * a.cs + (int64_t)p.g * a.N;
-  const unsigned boff = bc ? (unsigned)(bt * (int)a.bs + bn) * (unsigned)sizeof(T) : 0u;
-  const unsigned coff = bc ? (unsigned)(bt * (int)a.cs + bn) * (unsigned)sizeof(T) : 0u;
+  const Rows<T> r(a, p, (const T*)a.u, j);
   const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
   const float Dv = OUT && a.D ? a.D[p.c] : 0.f;
-  const int n0 = kScanK * wave;
-  const f32x4 A2 = load_A2(a, p.c, n0);
-
-  f32x4 h = {0.f, 0.f, 0.f, 0.f};
-  const int64_t hrow = ((p.b * a.chunks + p.chunk) * a.Dm + p.c) * NP + n0;
+  States<K> A2, h;
+  A2.load_n(a.A + p.c * a.N, K * j, a.N, kLog2e);
+#pragma unroll
+  for (int k = 0; k < K; ++k) h.v[k] = 0.f;
+  const int64_t hrow = ((p.b * a.chunks + p.chunk) * a.Dm + p.c) * NP + K * j;
+  const int64_t srow = (p.b * a.Dm + p.c) * a.N;
   if constexpr (OUT) {
     if (a.chunks > 1)
-      h = *(const f32x4*)(hs + hrow);
+      h.load(hs + hrow);
     else if (a.init)
-      h = load_states(a.init + (p.b * a.Dm + p.c) * a.N, n0, a.N);
+      h.load_n(a.init + srow, K * j, a.N);
   }
+  T* yb = OUT ? y + (p.b * a.L + p.t0) * a.Dm + p.c0 : nullptr;
 
-  auto load = [&](Held<T, ROWS>& r, int t) {
-    const int first = t + wave * ROWS;
-    if (t + TT <= valid) {
-      if (wave < LOADERS) {
+  // B and C: thread -> state bn of tokens bt, bt + THREADS / NP, ..
+  const int bt = threadIdx.x / NP, bn = threadIdx.x % NP;
+  const T* Bb = (const T*)a.B + (p.b * a.L + p.t0) * a.bs + (int64_t)p.g * a.N;
+  const T* Cb = (const T*)a.C + (p.b * a.L + p.t0) * a.cs + (int64_t)p.g * a.N;
+  const bool state = bn < a.N && bt < S;
+  const unsigned boff = state ? ((unsigned)bt * (unsigned)a.bs + bn) * (unsigned)sizeof(T) : 0u;
+  const unsigned coff = state ? ((unsigned)bt * (unsigned)a.cs + bn) * (unsigned)sizeof(T) : 0u;
+  T hb[EACH], hc[EACH];
+  auto load_bc = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          r.u[i] = lane_at(ub + (int64_t)(first + i) * a.Dm, off);
-          r.dt[i] = lane_at(db + (int64_t)(first + i) * a.Dm, off);
-          if constexpr (GATE && OUT) r.z[i] = lane_at(zb + (int64_t)(first + i) * a.zs, off);
-        }
-      }
-      if (bc) {
-        r.b = lane_at(Bb + (int64_t)t * a.bs, boff);
-        if constexpr (OUT) r.c = lane_at(Cb + (int64_t)t * a.cs, coff);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        r.u[i] = r.dt[i] = r.z[i] = (T)0.f;
-        if (wave < LOADERS && first + i < valid) {
-          r.u[i] = lane_at(ub + (int64_t)(first + i) * a.Dm, off);
-          r.dt[i] = lane_at(db + (int64_t)(first + i) * a.Dm, off);
-          if constexpr (GATE && OUT) r.z[i] = lane_at(zb + (int64_t)(first + i) * a.zs, off);
-        }
-      }
-      r.b = r.c = (T)0.f;
-      if (bc && t + bt < valid) {
-        r.b = lane_at(Bb + (int64_t)t * a.bs, boff);
-        if constexpr (OUT) r.c = lane_at(Cb + (int64_t)t * a.cs, coff);
+    for (int i = 0; i < EACH; ++i) {
+      const int q = t + i * (THREADS / NP);
+      hb[i] = hc[i] = (T)0.f;
+      if (state && q + bt < r.valid) {
+        hb[i] = lane_at(Bb + (int64_t)q * a.bs, boff);
+        if constexpr (OUT) hc[i] = lane_at(Cb + (int64_t)q * a.cs, coff);
       }
     }
   };
-  float total = 0.f;  // sum of d over the chunk's tokens that this thread loaded
-  auto stage = [&](const Held<T, ROWS>& r, int t, int buf) {
-    if (wave < LOADERS) {
-      float d[ROWS];
+  auto stage_bc = [&](int buf) {
+    if (bt < S) {
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) d[i] = to_f32(r.dt[i]) + bias;
-      if (a.softplus) {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) d[i] = softplus_f32(d[i]);
+      for (int i = 0; i < EACH; ++i) {
+        sB[buf][bt + i * (THREADS / NP)][bn] = to_f32(hb[i]);
+        if constexpr (OUT) sC[buf][bt + i * (THREADS / NP)][bn] = to_f32(hc[i]);
       }
-      if (t + TT > valid) {
+    }
+  };
+
+  Tokens<T, TT, GATE> cur, nxt;
+  float total = 0.f;
+  load_bc(0);
+  cur.template load<false, OUT>(a, p, r, 0);
+  stage_bc(0);
+  __syncthreads();
+  int buf = 0;
+  for (int s0 = 0; s0 < r.n; s0 += S, buf ^= 1) {
+    if (s0 + S < r.n) load_bc(s0 + S);
+    const int s1 = s0 + S < r.n ? s0 + S : r.n;
+    for (int t = s0; t < s1; t += TT) {
+      if (t + TT < r.n) nxt.template load<false, OUT>(a, p, r, t + TT);
+      float raw[OWN], d[OWN], w[OWN], part[4];
+      cur.steps(a, r, t, bias, raw, d);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) d[i] = t + wave * ROWS + i < valid ? d[i] : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        sd[buf][wave * ROWS + i][lane] = d[i];
-        su[buf][wave * ROWS + i][lane] = d[i] * to_f32(r.u[i]);
+      for (int i = 0; i < OWN; ++i) {
+        w[i] = d[i] * to_f32(cur.u[i]);
         if constexpr (!OUT) total += d[i];
       }
-    }
-    if (bt < TT) {
-      sB[buf][bt][bn] = bc ? to_f32(r.b) : 0.f;
-      if constexpr (OUT) sC[buf][bt][bn] = bc ? to_f32(r.c) : 0.f;
-    }
-  };
-  // One tile: `cur` is staged in buffer `buf`, the next tile is loaded into
-  // `nxt` meanwhile and staged in the other buffer.
-  auto tile = [&](const Held<T, ROWS>& cur, Held<T, ROWS>& nxt, int t, int buf) {
-    const bool more = t + TT < n;
-    if (more) load(nxt, t + TT);
+      auto token = [&](int i, float dv, float wv) {
+        States<K> B, C;
+        B.load(&sB[buf][t - s0 + i][K * j]);
+        if constexpr (OUT) C.load(&sC[buf][t - s0 + i][K * j]);
+        float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const float d = sd[buf][i][lane], w = su[buf][i][lane];
-      const f32x4 Bv = *(const f32x4*)&sB[buf][i][n0];
-      f32x4 Cv;
-      if constexpr (OUT) Cv = *(const f32x4*)&sC[buf][i][n0];
-      float s = 0.f;
+        for (int k = 0; k < K; ++k) {
+          h.v[k] = __builtin_fmaf(fast_exp2(dv * A2.v[k]), h.v[k], wv * B.v[k]);
+          if constexpr (OUT) s = __builtin_fmaf(h.v[k], C.v[k], s);
+        }
+        part[i & 3] = s;
+      };
+      float out[OWN];
 #pragma unroll
-      for (int k = 0; k < kScanK; ++k) {
-        h[k] = __builtin_fmaf(fast_exp2(d * A2[k]), h[k], w * Bv[k]);
-        if constexpr (OUT) s = __builtin_fmaf(h[k], Cv[k], s);
-      }
-      if constexpr (OUT) sy[buf][wave][i][lane] = s;
-    }
-    if (more) stage(nxt, t + TT, buf ^ 1);
-    __syncthreads();
-    if constexpr (OUT) {
-      if (wave < LOADERS && p.live) {
-        float s[ROWS];
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          s[i] = Dv * to_f32(cur.u[i]);
-#pragma unroll
-          for (int w = 0; w < WV; ++w) s[i] += sy[buf][w][wave * ROWS + i][lane];
+      for (int i = 0; i < OWN; ++i) {
+        token(4 * i, of_lane<0>(d[i]), of_lane<0>(w[i]));
+        token(4 * i + 1, of_lane<1>(d[i]), of_lane<1>(w[i]));
+        token(4 * i + 2, of_lane<2>(d[i]), of_lane<2>(w[i]));
+        token(4 * i + 3, of_lane<3>(d[i]), of_lane<3>(w[i]));
+        if constexpr (OUT) {
+          out[i] = __builtin_fmaf(Dv, to_f32(cur.u[i]), quad_sums(part, j));
           if constexpr (GATE) {
             const float zv = to_f32(cur.z[i]);
-            s[i] *= zv * sigmoid_f32(zv);
+            out[i] *= zv * sigmoid_f32(zv);
           }
         }
-        const int first = t + wave * ROWS;
-        if (t + TT <= valid) {
+      }
+      if constexpr (OUT) {
+        const int ty = fresh(t);
+        if (r.whole && t + TT <= r.valid) {
 #pragma unroll
-          for (int i = 0; i < ROWS; ++i)
-            lane_at(yb + (int64_t)(first + i) * a.Dm, off) = from_f32<T>(s[i]);
-        } else {
+          for (int i = 0; i < OWN; ++i)
+            lane_at(yb + (int64_t)(ty + 4 * i) * a.Dm, r.off) = from_f32<T>(out[i]);
+        } else if (p.live) {
 #pragma unroll
-          for (int i = 0; i < ROWS; ++i)
-            if (first + i < n)
-              lane_at(yb + (int64_t)(first + i) * a.Dm, off) =
-                  from_f32<T>(first + i < valid ? s[i] : 0.f);
+          for (int i = 0; i < OWN; ++i)
+            if (t + 4 * i + j < r.n)
+              lane_at(yb + (int64_t)(ty + 4 * i) * a.Dm, r.off) =
+                  from_f32<T>(t + 4 * i + j < r.valid ? out[i] : 0.f);
         }
       }
+      cur = nxt;
     }
-  };
-
-  Held<T, ROWS> r0, r1;
-  load(r0, 0);
-  stage(r0, 0, 0);
-  __syncthreads();
-  for (int t = 0; t < n; t += 2 * TT) {
-    tile(r0, r1, t, 0);
-    if (t + TT < n) tile(r1, r0, t + TT, 1);
+    if (s0 + S < r.n) stage_bc(buf ^ 1);
+    __syncthreads();
   }
 
   if constexpr (OUT) {
     if (final_state && p.live && p.chunk == a.chunks - 1)
-      store_states(final_state + (p.b * a.Dm + p.c) * a.N, n0, a.N, h);
+      h.store_n(final_state + srow, K * j, a.N);
   } else {
-    if (p.live) *(f32x4*)(hs + hrow) = h;
-    // the sums of the loading wavefronts, through LDS that no wavefront reads any more
-    if (wave < LOADERS) sd[0][wave][lane] = total;
-    __syncthreads();
-    if (wave == 0 && p.live) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < LOADERS; ++w) s += sd[0][w][lane];
-      sum_d[(p.b * a.chunks + p.chunk) * a.Dm + p.c] = s;
+    total = quad_sum(total);
+    if (p.live) {
+      h.store(hs + hrow);
+      if (j == 0) sum_d[(p.b * a.chunks + p.chunk) * a.Dm + p.c] = total;
     }
   }
 }
@@ -365,52 +315,55 @@ __global__ void __launch_bounds__(256) scan_step_any_kernel(ScanArgs a, int64_t 
   }
 }
 
-// Chunks of the forward: one where the channel tiles alone keep the device
-// busy, else enough for about 6 workgroups per CU, of at least 64 tokens.
+// Chunks of the forward.  One pass over whole sequences where the channel
+// tiles nearly fill the device (2048 tokens x 2048 channels x 16 states:
+// batch 16, 512 workgroups, 385 us in one pass and 460 in chunks; batch 12,
+// 384 workgroups, 380 and 356), or where there is little to divide; else
+// chunks of 64 tokens (1 x 512 x 2048: 25 us, 37 with 128) and, from 4096
+// workgroups on, longer ones.
 ScanSplit forward_split(const ScanDims& d) {
-  const int64_t tile = scan_tile(scan_waves(d.N));
   const int64_t blocks = d.B * scan_channel_tiles(d);
-  int64_t chunks = 1;
-  if (blocks < 512) chunks = 1536 / blocks;
-  const int64_t most = (d.L + 63) / 64;
-  if (chunks > most) chunks = most;
   ScanSplit p;
-  p.len = ((d.L + chunks - 1) / chunks + tile - 1) / tile * tile;
+  if (d.L <= 128 || blocks >= 448) {
+    p.len = (d.L + 15) / 16 * 16;
+  } else {
+    p.len = 64;
+    while (blocks * ((d.L + p.len - 1) / p.len) > 4096) p.len *= 2;
+  }
   p.chunks = (d.L + p.len - 1) / p.len;
   return p;
 }
 
-template <typename T, int WV>
+template <typename T, int K>
 hipError_t forward_t(const ScanDims& d, const ScanSplit& p, const ScanArgs& a, void* y,
                      float* final_state, float* hs, float* sum_d, hipStream_t s) {
+  constexpr int threads = 64 * kQuadWaves;
   const dim3 grid((unsigned)(p.chunks * scan_channel_tiles(d)), (unsigned)d.B);
   if (p.chunks > 1) {
-    scan_fwd_kernel<T, WV, false, false><<<grid, 64 * WV, 0, s>>>(a, nullptr, hs, sum_d, nullptr);
-    const dim3 cols((unsigned)((d.D * kScanK * WV + 63) / 64), (unsigned)d.B);
-    scan_carry_kernel<<<cols, 64 * carry_waves(p.chunks), 0, s>>>(a, kScanK * WV, hs, sum_d);
+    scan_fwd_kernel<T, K, false, false><<<grid, threads, 0, s>>>(a, nullptr, hs, sum_d, nullptr);
+    const dim3 cols((unsigned)((d.D * 4 * K + 63) / 64), (unsigned)d.B);
+    scan_carry_kernel<<<cols, 64 * carry_waves(p.chunks), 0, s>>>(a, 4 * K, hs, sum_d);
   }
   if (a.z)
-    scan_fwd_kernel<T, WV, true, true><<<grid, 64 * WV, 0, s>>>(a, (T*)y, hs, nullptr, final_state);
+    scan_fwd_kernel<T, K, true, true><<<grid, threads, 0, s>>>(a, (T*)y, hs, nullptr, final_state);
   else
-    scan_fwd_kernel<T, WV, false, true><<<grid, 64 * WV, 0, s>>>(a, (T*)y, hs, nullptr,
-                                                                 final_state);
+    scan_fwd_kernel<T, K, false, true><<<grid, threads, 0, s>>>(a, (T*)y, hs, nullptr, final_state);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t forward_by_waves(const ScanDims& d, const ScanSplit& p, const ScanArgs& a, void* y,
-                            float* final_state, float* hs, float* sum_d, hipStream_t s) {
-  switch (scan_waves(d.N)) {
-    case 1: return forward_t<T, 1>(d, p, a, y, final_state, hs, sum_d, s);
-    case 2: return forward_t<T, 2>(d, p, a, y, final_state, hs, sum_d, s);
-    case 4: return forward_t<T, 4>(d, p, a, y, final_state, hs, sum_d, s);
-    case 8: return forward_t<T, 8>(d, p, a, y, final_state, hs, sum_d, s);
-    default: return forward_t<T, 16>(d, p, a, y, final_state, hs, sum_d, s);
+template <typename T, typename... R>
+hipError_t forward_by_k(const ScanDims& d, R... r) {
+  switch (scan_k(d.N)) {
+    case 1: return forward_t<T, 1>(d, r...);
+    case 2: return forward_t<T, 2>(d, r...);
+    case 4: return forward_t<T, 4>(d, r...);
+    case 8: return forward_t<T, 8>(d, r...);
+    default: return forward_t<T, 16>(d, r...);
   }
 }
 
 size_t states_bytes(const ScanDims& d, const ScanSplit& p) {
-  return (size_t)(d.B * p.chunks * d.D * kScanK * scan_waves(d.N)) * sizeof(float);
+  return (size_t)(d.B * p.chunks * d.D * 4 * scan_k(d.N)) * sizeof(float);
 }
 
 constexpr int kStepSeqs = 2;
@@ -461,8 +414,8 @@ hipError_t launch_selective_scan(const ScanDims& d, const void* u, const void* d
   const ScanArgs a = scan_args(d, p, u, dt, A, B, C, D, z, dt_bias, init, lengths);
   float* hs = (float*)ws;
   float* sum_d = p.chunks > 1 ? (float*)((char*)ws + states_bytes(d, p)) : nullptr;
-  return d.bf16 ? forward_by_waves<bf16>(d, p, a, y, final_state, hs, sum_d, s)
-                : forward_by_waves<float>(d, p, a, y, final_state, hs, sum_d, s);
+  return d.bf16 ? forward_by_k<bf16>(d, p, a, y, final_state, hs, sum_d, s)
+                : forward_by_k<float>(d, p, a, y, final_state, hs, sum_d, s);
 }
 
 hipError_t launch_selective_scan_step(const ScanDims& d, const void* u, const void* dt,

@@ -11,10 +11,10 @@
 //
 // The states are recomputed.  The sequence is cut into short chunks (64
 // tokens at 16 states) that run at once:
-//   1. scan_bwd_ends: per chunk the state reached from zero, the decay over
-//      the chunk, and the gradient its tokens send to its start.  All three
-//      go forward in time, from one exponential per (token, channel, state):
-//      the last is sum_t (a[0] .. a[t]) q[t] C[t].
+//   1. scan_bwd_ends: per chunk the state reached from zero, the sum of d (the
+//      decay over the chunk is exp(A sum d)), and the gradient its tokens send
+//      to its start.  All go forward in time, from one exponential per (token,
+//      channel, state): the last is sum_t (a[0] .. a[t]) q[t] C[t].
 //   2. scan_bwd_carry: start states forward over the chunks, end gradients
 //      backward over them.
 //   3. scan_bwd_main: per chunk the states at the start of each tile of
@@ -36,35 +36,11 @@ namespace m2 {
 
 namespace {
 
-constexpr int kQuadWaves = 4;
-
 // Tokens of a tile whose states and decays stay in registers, and the longest
 // chunk: the workgroup's tile-start states take at most 64 KB of LDS.
 constexpr int bwd_tile(int K) { return K <= 4 ? 8 : 4; }
 constexpr int bwd_chunk(int K) { return K <= 4 ? 64 : K == 8 ? 32 : 16; }
 
-inline int bwd_k(int64_t N) {
-  int k = 1;
-  while (4 * k < N) k *= 2;
-  return k;
-}
-
-// The value of lane J of this lane's quad.
-template <int J>
-__device__ __forceinline__ float of_lane(float v) { return dpp<J * 0x55>(v); }
-__device__ __forceinline__ float quad_sum(float v) {
-  v += dpp<0xB1>(v);  // lanes 1 0 3 2
-  v += dpp<0x4E>(v);  // lanes 2 3 0 1
-  return v;
-}
-// Lane j of the quad gets the sum over the quad of v[j]: nine operations for
-// four sums.
-__device__ __forceinline__ float quad_sums(const float (&v)[4], int j) {
-  const bool hi2 = j & 2, hi1 = j & 1;
-  const float a = (hi2 ? v[2] : v[0]) + dpp<0x4E>(hi2 ? v[0] : v[2]);
-  const float b = (hi2 ? v[3] : v[1]) + dpp<0x4E>(hi2 ? v[1] : v[3]);
-  return (hi1 ? b : a) + dpp<0xB1>(hi1 ? a : b);
-}
 // The value of the lane 8 and 4 lanes away (exclusive or) in a row of 16: a
 // rotation by 8; the mirror of 8 lanes after that of each quad.
 __device__ __forceinline__ float from_xor8(float v) { return dpp<0x128>(v); }
@@ -121,53 +97,6 @@ __device__ __forceinline__ void store_sums(float* rows, const float (&v)[M], int
     rows[(m + r) / K * (4 * K) + K * (lane & 3) + (m + r) % K] = v[r];
 }
 
-template <int K>
-struct States {
-  float v[K];
-  __device__ __forceinline__ void load(const float* p) {
-    if constexpr (K >= 4) {
-#pragma unroll
-      for (int k = 0; k < K; k += 4) {
-        const f32x4 q = *(const f32x4*)(p + k);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[k + e] = q[e];
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] = p[k];
-    }
-  }
-  __device__ __forceinline__ void store(float* p) const {
-    if constexpr (K >= 4) {
-#pragma unroll
-      for (int k = 0; k < K; k += 4) *(f32x4*)(p + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
-    } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k) p[k] = v[k];
-    }
-  }
-  __device__ __forceinline__ void load_n(const float* p, int n0, int N, float by = 1.f) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = n0 + k < N ? by * p[n0 + k] : 0.f;
-  }
-  __device__ __forceinline__ void store_n(float* p, int n0, int N) const {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (n0 + k < N) p[n0 + k] = v[k];
-  }
-};
-
-// As scan_place, with this lane's channel: four lanes to each.
-__device__ __forceinline__ ScanPlace quad_place(const ScanArgs& a) {
-  ScanPlace p = scan_place(a);
-  const int64_t dg = a.Dm / a.G;
-  const unsigned in = (unsigned)(wave_id() * 16 + (lane_id() >> 2));
-  p.live = p.c0 - (int64_t)p.g * dg + in < dg;
-  p.at = p.live ? in : 0u;
-  p.c = p.c0 + p.at;
-  return p;
-}
-
 // B and C of a chunk into LDS as float32, zero past N and past the sequence.
 template <typename T, int NP, int Q>
 __device__ __forceinline__ void stage_bc(const ScanArgs& a, const ScanPlace& p, int valid,
@@ -184,94 +113,14 @@ __device__ __forceinline__ void stage_bc(const ScanArgs& a, const ScanPlace& p, 
   }
 }
 
-// A lane's rows of a chunk: scalar addresses of the chunk's first token, this
-// lane's offsets in bytes from the first token of a group of four, and the
-// counts of tokens (those of the chunk; those that are no padding).
-template <typename T>
-struct Rows {
-  const T *u, *dt, *dy, *z;
-  unsigned off, zoff;
-  int n, valid, j;
-  bool whole;  // every lane of the workgroup has a channel
-  __device__ __forceinline__ Rows(const ScanArgs& a, const ScanPlace& p, const T* dyp, int jj) {
-    const int64_t row0 = p.b * a.L + p.t0;
-    u = (const T*)a.u + row0 * a.Dm + p.c0;
-    dt = (const T*)a.dt + row0 * a.Dm + p.c0;
-    dy = dyp + row0 * a.Dm + p.c0;
-    z = (const T*)a.z + row0 * a.zs + p.c0;  // not read where there is none
-    j = jj;
-    off = ((unsigned)j * (unsigned)a.Dm + p.at) * (unsigned)sizeof(T);
-    zoff = ((unsigned)j * (unsigned)a.zs + p.at) * (unsigned)sizeof(T);
-    n = (int)(p.t1 - p.t0);
-    const int64_t left = p.len - p.t0;
-    valid = left <= 0 ? 0 : left < n ? (int)left : n;
-    whole = p.c0 + 64 <= (int64_t)(p.g + 1) * (a.Dm / a.G);
-  }
-};
-
-// What a lane loads of its tokens of a tile (token 4 i + j of it).
-template <typename T, int TT, bool GATE>
-struct Tokens {
-  static constexpr int OWN = TT / 4;
-  T u[OWN], dt[OWN], dy[OWN], z[OWN];
-  template <bool GRAD>
-  __device__ __forceinline__ void load(const ScanArgs& a, const ScanPlace& p, const Rows<T>& r,
-                                       int t) {
-    auto one = [&](int i) {
-      const int64_t at = (int64_t)(t + 4 * i) * a.Dm;
-      u[i] = lane_at(r.u + at, r.off);
-      dt[i] = lane_at(r.dt + at, r.off);
-      if constexpr (GRAD) {
-        dy[i] = lane_at(r.dy + at, r.off);
-        if constexpr (GATE) z[i] = lane_at(r.z + (int64_t)(t + 4 * i) * a.zs, r.zoff);
-      }
-    };
-    if (r.whole && t + TT <= r.valid) {
-#pragma unroll
-      for (int i = 0; i < OWN; ++i) one(i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < OWN; ++i) {
-        u[i] = dt[i] = dy[i] = z[i] = (T)0.f;
-        if (p.live && t + 4 * i + r.j < r.valid) one(i);
-      }
-    }
-  }
-  // the time steps, zero where there is no token
-  __device__ __forceinline__ void steps(const ScanArgs& a, const Rows<T>& r, int t, float bias,
-                                        float (&raw)[OWN], float (&d)[OWN]) const {
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) d[i] = raw[i] = to_f32(dt[i]) + bias;
-    if (a.softplus) {
-#pragma unroll
-      for (int i = 0; i < OWN; ++i) d[i] = softplus_f32(raw[i]);
-    }
-    if (t + TT > r.valid) {
-#pragma unroll
-      for (int i = 0; i < OWN; ++i) d[i] = t + 4 * i + r.j < r.valid ? d[i] : 0.f;
-    }
-  }
-  // dy, times silu(z) with a gate
-  __device__ __forceinline__ void grads(float (&q)[OWN]) const {
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      q[i] = to_f32(dy[i]);
-      if constexpr (GATE) {
-        const float zv = to_f32(z[i]);
-        q[i] *= zv * sigmoid_f32(zv);
-      }
-    }
-  }
-};
-
 template <typename T, int K, bool GATE>
 __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_ends_kernel(
-    ScanArgs a, const T* __restrict__ dy, float* __restrict__ hs, float* __restrict__ decay,
+    ScanArgs a, const T* __restrict__ dy, float* __restrict__ hs, float* __restrict__ sum_d,
     float* __restrict__ ge) {
   constexpr int NP = 4 * K, Q = bwd_chunk(K), TT = Q < 16 ? Q : 16, OWN = TT / 4;
   __shared__ __align__(16) float sB[Q][NP], sC[Q][NP];
   const int j = lane_id() & 3;
-  const ScanPlace p = quad_place(a);
+  const ScanPlace p = scan_place(a);
   const Rows<T> r(a, p, dy, j);
   stage_bc<T, NP, Q>(a, p, r.valid, sB, sC);
   const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
@@ -282,16 +131,20 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_ends_kernel(
     h.v[k] = e.v[k] = 0.f;
     P.v[k] = 1.f;
   }
+  float total = 0.f;
   Tokens<T, TT, GATE> cur, nxt;
-  cur.template load<true>(a, p, r, 0);
+  cur.template load<true, true>(a, p, r, 0);
   __syncthreads();
   for (int t = 0; t < r.valid; t += TT) {
-    if (t + TT < r.valid) nxt.template load<true>(a, p, r, t + TT);
+    if (t + TT < r.valid) nxt.template load<true, true>(a, p, r, t + TT);
     float raw[OWN], d[OWN], w[OWN], q[OWN];
     cur.steps(a, r, t, bias, raw, d);
     cur.grads(q);
 #pragma unroll
-    for (int i = 0; i < OWN; ++i) w[i] = d[i] * to_f32(cur.u[i]);
+    for (int i = 0; i < OWN; ++i) {
+      w[i] = d[i] * to_f32(cur.u[i]);
+      total += d[i];
+    }
     auto token = [&](int i, float dv, float wv, float qv) {
       States<K> B, C;
       B.load(&sB[t + i][K * j]);
@@ -313,18 +166,19 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_ends_kernel(
     }
     cur = nxt;
   }
+  total = quad_sum(total);
   if (!p.live) return;
-  const int64_t row = ((p.b * a.chunks + p.chunk) * a.Dm + p.c) * NP + K * j;
-  h.store(hs + row);
-  P.store(decay + row);
-  e.store(ge + row);
+  const int64_t col = (p.b * a.chunks + p.chunk) * a.Dm + p.c;
+  h.store(hs + col * NP + K * j);
+  e.store(ge + col * NP + K * j);
+  if (j == 0) sum_d[col] = total;
 }
 
 // Over the chunks, per (batch, channel, state): hs from "reached from zero" to
 // "starts from", ge from "sent to its start" to "arrives at its end".  Shares
 // of the chunks as in the forward's carry.
 __global__ void __launch_bounds__(64 * kCarryWaves) scan_bwd_carry_kernel(
-    ScanArgs a, int NP, float* __restrict__ hs, const float* __restrict__ decay,
+    ScanArgs a, int NP, float* __restrict__ hs, const float* __restrict__ sum_d,
     float* __restrict__ ge, const float* __restrict__ dfinal) {
   __shared__ float sh[kCarryWaves][64], sg[kCarryWaves][64], sp[kCarryWaves][64];
   const int lane = lane_id(), wave = wave_id(), waves = blockDim.x >> 6;
@@ -335,15 +189,19 @@ __global__ void __launch_bounds__(64 * kCarryWaves) scan_bwd_carry_kernel(
   const int64_t share = (a.chunks + waves - 1) / waves;
   const int64_t c0 = wave * share, c1 = c0 + share < a.chunks ? c0 + share : a.chunks;
   const int64_t base = b * a.chunks * cols + (live ? col : 0);
+  const float A2 = n < a.N ? a.A[c * a.N + n] * kLog2e : 0.f;
+  const float* dp = sum_d + b * a.chunks * a.Dm + c;
   float x[kCarryLoads], hl[kCarryLoads], el[kCarryLoads];
   auto load = [&](int64_t q) {
 #pragma unroll
     for (int k = 0; k < kCarryLoads; ++k) {
-      const int64_t i = base + (q + k < c1 ? q + k : c1 - 1) * cols;
-      x[k] = decay[i];
-      hl[k] = hs[i];
-      el[k] = ge[i];
+      const int64_t i = q + k < c1 ? q + k : c1 - 1;
+      x[k] = dp[i * a.Dm];
+      hl[k] = hs[base + i * cols];
+      el[k] = ge[base + i * cols];
     }
+#pragma unroll
+    for (int k = 0; k < kCarryLoads; ++k) x[k] = fast_exp2(A2 * x[k]);
   };
   // this share as one chunk: state reached, decay, gradient sent to its start
   float h = 0.f, P = 1.f, e = 0.f;
@@ -407,7 +265,7 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
   // per wavefront and tile: the states at its start, then its dB and dC
   __shared__ __align__(16) float slot[kQuadWaves][NT][64 * K];
   const int lane = lane_id(), wave = wave_id(), j = lane & 3;
-  const ScanPlace p = quad_place(a);
+  const ScanPlace p = scan_place(a);
   const Rows<T> rows(a, p, dy, j);
   stage_bc<T, NP, Q>(a, p, rows.valid, sB, sC);
   const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
@@ -427,14 +285,14 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
   }
   const int tiles = (rows.n + TT - 1) / TT;
   Tokens<T, TT, GATE> cur, nxt;
-  cur.template load<false>(a, p, rows, 0);
+  cur.template load<false, false>(a, p, rows, 0);
   __syncthreads();
 
   // states at the start of every tile
   for (int i = 0; i + 1 < tiles; ++i) {
     h.store(&slot[wave][i][lane * K]);
     const int t = i * TT;
-    nxt.template load<false>(a, p, rows, t + TT);
+    nxt.template load<false, false>(a, p, rows, t + TT);
     float raw[OWN], d[OWN], w[OWN];
     cur.steps(a, rows, t, bias, raw, d);
 #pragma unroll
@@ -458,14 +316,14 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
   h.store(&slot[wave][tiles - 1][lane * K]);
 
   float dDs = 0.f, dbs = 0.f;
-  cur.template load<true>(a, p, rows, (tiles - 1) * TT);
+  cur.template load<true, true>(a, p, rows, (tiles - 1) * TT);
   T* dub = du + (p.b * a.L + p.t0) * a.Dm + p.c0;
   T* ddtb = ddt + (p.b * a.L + p.t0) * a.Dm + p.c0;
   T* dzb = GATE ? dz + (p.b * a.L + p.t0) * dzs + p.c0 : nullptr;
   const unsigned dzoff = ((unsigned)j * (unsigned)dzs + p.at) * (unsigned)sizeof(T);
   for (int i = tiles - 1; i >= 0; --i) {
     const int t = i * TT;
-    if (i > 0) nxt.template load<true>(a, p, rows, t - TT);
+    if (i > 0) nxt.template load<true, true>(a, p, rows, t - TT);
     float d[OWN], w[OWN], q[OWN], raw[OWN], s1[OWN], s2[OWN], s3[OWN];
     cur.steps(a, rows, t, bias, raw, d);
     cur.grads(q);
@@ -502,8 +360,6 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
         sum_channels<M>(v, lane);
         store_sums<M, K>(res + (TT + 4 * o + 4 - GT) * NP, v, lane);
       }
-      // keep the next tokens' LDS reads behind: hoisted, they cost registers that spill
-      __builtin_amdgcn_sched_barrier(0);
     }
     // reverse: the gradients of the states
     float gAs[4];
@@ -537,9 +393,9 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
         sum_channels<M>(v, lane);
         store_sums<M, K>(res + 4 * o * NP, v, lane);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
     const bool full = rows.whole && t + TT <= rows.valid;
+    const int ty = fresh(t);
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
       const int tq = t + 4 * o + j;
@@ -554,7 +410,7 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
       }
       const float duv = __builtin_fmaf(s1[o], d[o], Dv * q[o]);
       dDs = __builtin_fmaf(q[o], u, dDs);
-      const int64_t at = (int64_t)(t + 4 * o) * a.Dm, zat = (int64_t)(t + 4 * o) * dzs;
+      const int64_t at = (int64_t)(ty + 4 * o) * a.Dm, zat = (int64_t)(ty + 4 * o) * dzs;
       if (full) {
         dbs += dd;
         lane_at(dub + at, rows.off) = from_f32<T>(duv);
@@ -626,7 +482,7 @@ __global__ void __launch_bounds__(256) scan_bwd_bc_kernel(const float* __restric
 // fewer than two workgroups for each CU.
 ScanSplit backward_split(const ScanDims& d) {
   ScanSplit p;
-  p.len = bwd_chunk(bwd_k(d.N));
+  p.len = bwd_chunk(scan_k(d.N));
   const int64_t per = d.B * scan_channel_tiles(d);
   while (p.len > 16 && per * ((d.L + p.len - 1) / p.len) < 512) p.len /= 2;
   p.chunks = (d.L + p.len - 1) / p.len;
@@ -634,18 +490,19 @@ ScanSplit backward_split(const ScanDims& d) {
 }
 
 struct BwdParts {
-  size_t states, bc, sums, total;  // bytes; states: each of hs, decay, ge
+  size_t states, steps, bc, sums, total;  // bytes; states: each of hs and ge; steps: sum_d
 };
 
 BwdParts backward_parts(const ScanDims& d) {
   const ScanSplit p = backward_split(d);
-  const int64_t NP = 4 * bwd_k(d.N), tiles = (d.D / d.G + 63) / 64;
+  const int64_t NP = 4 * scan_k(d.N), tiles = (d.D / d.G + 63) / 64;
   auto round = [](int64_t n) { return ((size_t)n * sizeof(float) + 255) & ~(size_t)255; };
   BwdParts w;
   w.states = p.chunks > 1 ? round(d.B * p.chunks * d.D * NP) : 0;
+  w.steps = p.chunks > 1 ? round(d.B * p.chunks * d.D) : 0;
   w.bc = round(2 * tiles * d.B * d.L * d.G * NP);
   w.sums = round(d.B * p.chunks * d.D * (d.N + 2));
-  w.total = 3 * w.states + w.bc + w.sums;
+  w.total = 2 * w.states + w.steps + w.bc + w.sums;
   return w;
 }
 
@@ -657,18 +514,18 @@ hipError_t backward_t(const ScanDims& d, const ScanSplit& p, const ScanArgs& a, 
   constexpr int NP = 4 * K, threads = 64 * kQuadWaves;
   const BwdParts w = backward_parts(d);
   float* hs = (float*)ws;
-  float* decay = (float*)(ws + w.states);
-  float* ge = (float*)(ws + 2 * w.states);
-  float* bc = (float*)(ws + 3 * w.states);
-  float* sums = (float*)(ws + 3 * w.states + w.bc);
+  float* ge = (float*)(ws + w.states);
+  float* sum_d = (float*)(ws + 2 * w.states);
+  float* bc = (float*)(ws + 2 * w.states + w.steps);
+  float* sums = (float*)(ws + 2 * w.states + w.steps + w.bc);
   const dim3 grid((unsigned)(p.chunks * scan_channel_tiles(d)), (unsigned)d.B);
   if (p.chunks > 1) {
     if (a.z)
-      scan_bwd_ends_kernel<T, K, true><<<grid, threads, 0, s>>>(a, (const T*)dy, hs, decay, ge);
+      scan_bwd_ends_kernel<T, K, true><<<grid, threads, 0, s>>>(a, (const T*)dy, hs, sum_d, ge);
     else
-      scan_bwd_ends_kernel<T, K, false><<<grid, threads, 0, s>>>(a, (const T*)dy, hs, decay, ge);
+      scan_bwd_ends_kernel<T, K, false><<<grid, threads, 0, s>>>(a, (const T*)dy, hs, sum_d, ge);
     const dim3 cols((unsigned)((d.D * NP + 63) / 64), (unsigned)d.B);
-    scan_bwd_carry_kernel<<<cols, 64 * carry_waves(p.chunks), 0, s>>>(a, NP, hs, decay, ge, dfinal);
+    scan_bwd_carry_kernel<<<cols, 64 * carry_waves(p.chunks), 0, s>>>(a, NP, hs, sum_d, ge, dfinal);
   }
   if (a.z)
     scan_bwd_main_kernel<T, K, true><<<grid, threads, 0, s>>>(
@@ -688,7 +545,7 @@ hipError_t backward_t(const ScanDims& d, const ScanSplit& p, const ScanArgs& a, 
 
 template <typename T, typename... R>
 hipError_t backward_by_k(const ScanDims& d, R... r) {
-  switch (bwd_k(d.N)) {
+  switch (scan_k(d.N)) {
     case 1: return backward_t<T, 1>(d, r...);
     case 2: return backward_t<T, 2>(d, r...);
     case 4: return backward_t<T, 4>(d, r...);
