@@ -23,7 +23,6 @@ namespace m2 {
 namespace {
 
 constexpr int kLoads = 8;         // rows in flight per thread
-constexpr int kBwdTile = 32;      // tokens per wavefront of the backward
 constexpr int kBwdWaves = 4;      // wavefronts (token tiles) per workgroup of the backward
 
 struct Parts {
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(256) conv1d_fwd_kernel(
   }
 }
 
-// Backward: a wavefront walks kBwdTile tokens and the W-1 after them (whose g
+// Backward: a wavefront walks a tile of tokens and the W-1 after them (whose g
 // it recomputes for its last dx rows).  The workgroup's kBwdWaves tiles are
 // summed in LDS into one row of weight-gradient parts [C * W | C]; the rows
 // are summed by partial_sums.
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves) conv1d_bwd_kernel(
     const T* __restrict__ init, const int32_t* __restrict__ lengths, Parts dy,
     const T* __restrict__ dfinal, T* __restrict__ dx, T* __restrict__ dinit,
     float* __restrict__ part, int64_t L, int64_t C, int64_t xs, int64_t dxs, unsigned ncb,
-    int silu) {
+    int tile_len, int silu) {
   constexpr int NS = (W + 1) * V;
   __shared__ float red[kBwdWaves - 1][NS][64];
   const int lane = lane_id(), wave = wave_id();
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves) conv1d_bwd_kernel(
   const unsigned tile = blockIdx.x / ncb;
   const int64_t c = ((int64_t)(blockIdx.x % ncb) * 64 + lane) * V;
   const int64_t b = blockIdx.y;
-  const int64_t t0 = ((int64_t)tile * kBwdWaves + wave) * kBwdTile;
+  const int64_t t0 = ((int64_t)tile * kBwdWaves + wave) * tile_len;
   const bool live = c < C;
   const int64_t len = length_of(lengths, b, L);
 
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves) conv1d_bwd_kernel(
         for (int e = 0; e < V; ++e) xw[j + 1][e] = elem<T, V>(q, e);
       }
     }
-    const int64_t own = t0 + kBwdTile < L ? t0 + kBwdTile : L;
+    const int64_t own = t0 + tile_len < L ? t0 + tile_len : L;
     const int64_t end = own + W - 1;
     constexpr int U = 4;
     for (int64_t t = t0; t < end; t += U) {
@@ -284,18 +283,18 @@ __global__ void __launch_bounds__(64 * kBwdWaves) conv1d_bwd_kernel(
   __syncthreads();
   if (wave || !live) return;
   float* row = part + ((int64_t)b * (gridDim.x / ncb) + tile) * C * (W + 1);
+  auto sum = [&](int k, int e) {
+    float s = acc[k][e];
 #pragma unroll
-  for (int k = 0; k <= W; ++k)
+    for (int o = 0; o < kBwdWaves - 1; ++o) s += red[o][k * V + e][lane];
+    return s;
+  };
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float s = acc[k][e];
+  for (int e = 0; e < V; ++e)
 #pragma unroll
-      for (int o = 0; o < kBwdWaves - 1; ++o) s += red[o][k * V + e][lane];
-      if (k < W)
-        row[(c + e) * W + k] = s;
-      else
-        row[C * W + c + e] = s;
-    }
+    for (int k = 0; k < W; ++k) row[(c + e) * W + k] = sum(k, e);
+#pragma unroll
+  for (int e = 0; e < V; ++e) row[C * W + c + e] = sum(W, e);
 }
 
 template <typename T, int V, int W>
@@ -362,8 +361,21 @@ hipError_t dispatch(const ConvDims& d, bool back, F&& f) {
                                            : by_width<float, 1>(d, f);
 }
 
+// Tokens of a backward tile: 32, or 16 or 8 where that leaves less than one
+// wavefront for each SIMD (5 x 306 x 1920 bf16: 33 us with 32, 18 with 8; 2 x
+// 2048 x 2560: 37 with 32, 31 with 16).  By the sizes alone, so that the
+// workspace is known before the pointers.
+int bwd_tile(const ConvDims& d) {
+  const int64_t lanes = d.C / (vectors(d, d.bf16 ? 8 : 4, true) ? (d.bf16 ? 8 : 4) : 1);
+  const int64_t per = (lanes + 63) / 64 * d.B;
+  for (int n = 32; n > 8; n /= 2)
+    if (per * ((d.L + n - 1) / n) >= 1024) return n;
+  return 8;
+}
+
 int64_t bwd_tiles(const ConvDims& d) {
-  return (d.L + kBwdTile * kBwdWaves - 1) / (kBwdTile * kBwdWaves);
+  const int n = bwd_tile(d) * kBwdWaves;
+  return (d.L + n - 1) / n;
 }
 
 }  // namespace
@@ -402,7 +414,7 @@ hipError_t launch_conv1d_backward(const ConvDims& d, const void* x, const float*
     const dim3 grid((unsigned)(ncb * bwd_tiles(d)), (unsigned)d.B);
     conv1d_bwd_kernel<T, V, W><<<grid, 64 * kBwdWaves, 0, s>>>(
         (const T*)x, w, bias, (const T*)init, lengths, parts_of(d, dy), (const T*)dfinal, (T*)dx,
-        (T*)dinit, part, d.L, d.C, d.xs, d.dxs, ncb, d.silu);
+        (T*)dinit, part, d.L, d.C, d.xs, d.dxs, ncb, bwd_tile(d), d.silu);
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;

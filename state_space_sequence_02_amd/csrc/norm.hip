@@ -72,17 +72,29 @@ __device__ __forceinline__ void store(T* p, int lane, int team, int64_t n,
   }
 }
 
-// Float parameters of this lane's columns (0 past the group).
+// Float parameters of this lane's columns (0 past the group).  With vectors
+// the columns start at a multiple of 16 bytes.
 template <int V, int NV>
 __device__ __forceinline__ void params(const float* p, int lane, int team, int64_t n,
                                        float (&v)[NV][V]) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
+  for (int k = 0; k < NV; ++k) {
+    const int64_t c = (int64_t)(k * team + lane) * V;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int64_t c = (int64_t)(k * team + lane) * V + e;
-      v[k][e] = p && c < n ? p[c] : 0.f;
+    for (int e = 0; e < V; ++e) v[k][e] = 0.f;
+    if (p && c < n) {
+      if constexpr (V == 1) {
+        v[k][0] = p[c];
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+          const f32x4 q = *(const f32x4*)(p + c + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[k][e + i] = q[i];
+        }
+      }
     }
+  }
 }
 
 constexpr int block_of(int team) { return team < 256 ? 256 : team; }
@@ -258,6 +270,7 @@ __global__ void __launch_bounds__(block_of(TEAM)) norm_bwd_kernel(
       __syncthreads();
     }
     if (team == 0) {
+      float out[NV][V];
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -267,9 +280,22 @@ __global__ void __launch_bounds__(block_of(TEAM)) norm_bwd_kernel(
 #pragma unroll
             for (int q = 0; q < TEAMS - 1; ++q) s += cols[q][k * V + e][lane];
           }
-          const int64_t c = (int64_t)(k * TEAM + lane) * V + e;
-          if (c < Dg) row[c] = s;
+          out[k][e] = s;
         }
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int64_t c = (int64_t)(k * TEAM + lane) * V;
+        if (c < Dg) {
+          if constexpr (V == 1) {
+            row[c] = out[k][0];
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 4)
+              *(f32x4*)(row + c + e) =
+                  f32x4{out[k][e], out[k][e + 1], out[k][e + 2], out[k][e + 3]};
+          }
+        }
+      }
     }
   }
 }
@@ -303,7 +329,7 @@ Shape shape_of(const NormDims& d, bool back) {
     s.nv = n <= 64 ? 1 : n <= 64 * (most / 2) ? most / 2 : most;
   } else if (n <= 256 * most) {
     s.team = 256;
-    s.nv = most;
+    s.nv = n <= 256 * (most / 2) ? most / 2 : most;
   } else {
     s.team = 1024;
     s.nv = 8 / s.v;
@@ -312,12 +338,14 @@ Shape shape_of(const NormDims& d, bool back) {
 }
 
 // Workgroups along the rows.  Forward: enough teams to fill the device
-// several times over; backward: each workgroup leaves a row of parts that is
-// read again, so about two resident sets of them.
+// several times over.  Backward: each workgroup leaves a row of parts that is
+// read again, so about two resident sets of them, and four rows per team where
+// that leaves a workgroup for each CU (1000 x 4096 bf16: 20 us, 38 with one).
 int64_t row_blocks(const NormDims& d, int team, bool back) {
   const int64_t teams = block_of(team) / team;
   const int64_t most = (back ? 1024 : 4096) * 256 / block_of(team) / d.G;
-  const int64_t want = (d.R + teams - 1) / teams;
+  int64_t want = (d.R + teams - 1) / teams;
+  if (back && want > 256) want = (want + 3) / 4 < 256 ? 256 : (want + 3) / 4;
   return want < most ? want : most < 1 ? 1 : most;
 }
 
@@ -334,7 +362,9 @@ hipError_t by_shape(const Shape& s, F&& f) {
   if (s.team == 64)
     return s.nv == 1 ? call<T, V, 1, 64>(f)
                      : s.nv == MOST / 2 ? call<T, V, MOST / 2, 64>(f) : call<T, V, MOST, 64>(f);
-  return s.team == 256 ? call<T, V, MOST, 256>(f) : call<T, V, 8 / V, 1024>(f);
+  if (s.team == 256)
+    return s.nv == MOST / 2 ? call<T, V, MOST / 2, 256>(f) : call<T, V, MOST, 256>(f);
+  return call<T, V, 8 / V, 1024>(f);
 }
 
 template <bool BACK, typename F>

@@ -4,7 +4,7 @@
 // a gradient has the same bits each time (no atomics).  Columns go to up to
 // three outputs: [0, end0) to the first, [end0, end1) to the second and
 // [end1, end2) to the third; an output that is NULL is not written.  A
-// workgroup sums 64 columns, each of its 8 wavefronts every eighth row.
+// workgroup sums 64 columns, each of its 16 wavefronts every sixteenth row.
 #include "common.h"
 #include "launch.h"
 
@@ -12,7 +12,8 @@ namespace m2 {
 
 namespace {
 
-constexpr int kSumWaves = 8;
+constexpr int kSumWaves = 16;
+constexpr int kSumLoads = 8;  // rows in flight per wavefront
 
 struct Outs {
   float* p[3];
@@ -24,21 +25,25 @@ __global__ void __launch_bounds__(64 * kSumWaves) partial_sums_kernel(
   __shared__ float red[kSumWaves][64];
   const int lane = lane_id(), wave = wave_id();
   const int64_t m = (int64_t)blockIdx.x * 64 + lane;
-  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  float s = 0.f;
   if (m < M) {
     int64_t p = wave;
-    for (; p + 3 * kSumWaves < P; p += 4 * kSumWaves) {
-      s0 += part[p * M + m];
-      s1 += part[(p + kSumWaves) * M + m];
-      s2 += part[(p + 2 * kSumWaves) * M + m];
-      s3 += part[(p + 3 * kSumWaves) * M + m];
+    for (; p + (kSumLoads - 1) * kSumWaves < P; p += kSumLoads * kSumWaves) {
+      float v[kSumLoads];
+#pragma unroll
+      for (int i = 0; i < kSumLoads; ++i) v[i] = part[(p + i * kSumWaves) * M + m];
+#pragma unroll
+      for (int n = kSumLoads / 2; n >= 1; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] += v[i + n];
+      s += v[0];
     }
-    for (; p < P; p += kSumWaves) s0 += part[p * M + m];
+    for (; p < P; p += kSumWaves) s += part[p * M + m];
   }
-  red[wave][lane] = (s0 + s1) + (s2 + s3);
+  red[wave][lane] = s;
   __syncthreads();
   if (wave || m >= M) return;
-  float s = red[0][lane];
+  s = red[0][lane];
 #pragma unroll
   for (int o = 1; o < kSumWaves; ++o) s += red[o][lane];
   const int i = m < out.end[0] ? 0 : m < out.end[1] ? 1 : 2;
