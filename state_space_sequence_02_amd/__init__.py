@@ -10,6 +10,9 @@ current torch stream into a ``hipStream_t``.  The functions keep the C names:
     mamba2_ssd_forward, mamba2_ssd_forward_profile, mamba2_status_string,
     mamba2_last_error
 
+and, in ``layer.py``, the operators around the SSD (``conv1d_*``,
+``selective_scan_*``, ``norm_*`` and their ``mamba2_*`` forms);
+
 plus ``make_dims`` and ``ssd_forward`` (allocates outputs and workspace with
 torch, then calls ``mamba2_ssd_forward``).  Importing fails loudly when the
 library has not been built; there is no fallback implementation.
