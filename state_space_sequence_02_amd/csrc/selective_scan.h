@@ -18,7 +18,6 @@
 
 namespace m2 {
 
-constexpr int kScanMaxState = 64;  // K = 16
 constexpr int kQuadWaves = 4;
 
 // States per lane for N states of a channel: 1, 2, 4, 8 or 16.

@@ -135,12 +135,16 @@ def _plain(t, dtype, shape, index):
             and t.get_device() == index)
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _owner(stream, t):
     """Allocations inside belong to ``stream``."""
     if stream is None or not t.is_cuda:
-        return contextlib.nullcontext()
+        return _CURRENT
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, t.device)
+        stream = (torch.cuda.ExternalStream(stream, t.device) if stream
+                  else torch.cuda.default_stream(t.device))
     return torch.cuda.stream(stream)
 
 

@@ -312,6 +312,10 @@ def test_other_streams(m2):
             got2 = other()
         got3 = calls(stream=s2.cuda_stream)
         torch.cuda.synchronize()
+        with torch.cuda.stream(s2):
+            got4 = calls(stream=0)  # the default stream, from another current one
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want, got4))
         assert all(torch.equal(p, q) for p, q in zip(want, got1))
         assert all(torch.equal(p, q) for p, q in zip(wother, got2))
         assert all(torch.equal(p, q) for p, q in zip(want, got3))
