@@ -20,7 +20,8 @@
 //   3. scan_bwd_main: per chunk the states at the start of each tile of
 //      tokens (kept in LDS), then the tiles in reverse, each with its states
 //      and decays in registers.
-//   4. the sums over channels (dB, dC) and over chunks (dA, dD, ddt_bias).
+//   4. scan_bwd_sums: the sums over channel tiles (dB, dC) and over chunks
+//      (dA, dD, ddt_bias).
 //
 // A lane holds K of a channel's 4 K states, four lanes (a quad) a channel, a
 // wavefront 16 channels, a workgroup 64 of one group.  Each lane of a quad
@@ -30,6 +31,7 @@
 // inside a chunk.  Sums over the channels of a wavefront (dB, dC) exchange
 // halves of the values while they add: the count of values halves with the
 // count of lanes, two operations per value instead of eight.
+#include "partial_sums.h"
 #include "selective_scan.h"
 
 namespace m2 {
@@ -459,13 +461,20 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
   }
 }
 
-// dB and dC [B, L, G, N] from the channel tiles' parts.
+// The last sums in one launch: the first `first` workgroups add dB and dC
+// [B, L, G, N] from the channel tiles' parts, the others dA, dD and ddt_bias
+// from the chunks'.
 template <typename T>
-__global__ void __launch_bounds__(256) scan_bwd_bc_kernel(const float* __restrict__ part,
-                                                          int64_t tiles, int64_t count, int NP,
-                                                          int N, T* __restrict__ dB,
-                                                          T* __restrict__ dC) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(64 * kSumWaves) scan_bwd_sums_kernel(
+    const float* __restrict__ part, int64_t tiles, int64_t count, int NP, int N,
+    T* __restrict__ dB, T* __restrict__ dC, unsigned first, const float* __restrict__ sums,
+    int64_t P, int64_t M, SumOuts out) {
+  __shared__ float red[kSumWaves][64];
+  if (blockIdx.x >= first) {
+    sum_columns(sums, P, M, out, blockIdx.x - first, red);
+    return;
+  }
+  const int64_t id = (int64_t)blockIdx.x * (64 * kSumWaves) + threadIdx.x;
   if (id >= 2 * count) return;
   const int64_t arr = id / count, i = id % count;
   const int n = (int)(i % NP);
@@ -533,14 +542,14 @@ hipError_t backward_t(const ScanDims& d, const ScanSplit& p, const ScanArgs& a, 
   else
     scan_bwd_main_kernel<T, K, false><<<grid, threads, 0, s>>>(
         a, (const T*)dy, dfinal, hs, ge, (T*)du, (T*)ddt, nullptr, 0, dinit, bc, sums);
-  const int64_t count = d.B * d.L * d.G * NP;
-  scan_bwd_bc_kernel<T><<<(unsigned)((2 * count + 255) / 256), 256, 0, s>>>(
-      bc, a.tiles, count, NP, a.N, (T*)dB, (T*)dC);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int64_t ends[3] = {d.D * d.N, d.D * (d.N + 1), d.D * (d.N + 2)};
+  const int64_t count = d.B * d.L * d.G * NP, M = d.D * (d.N + 2);
+  const int64_t ends[3] = {d.D * d.N, d.D * (d.N + 1), M};
   float* const outs[3] = {dA, dD, ddt_bias};
-  return launch_partial_sums(sums, d.B * p.chunks, d.D * (d.N + 2), ends, outs, s);
+  const unsigned first = (unsigned)((2 * count + 64 * kSumWaves - 1) / (64 * kSumWaves));
+  scan_bwd_sums_kernel<T><<<first + (unsigned)((M + 63) / 64), 64 * kSumWaves, 0, s>>>(
+      bc, a.tiles, count, NP, a.N, (T*)dB, (T*)dC, first, sums, d.B * p.chunks, M,
+      sum_outs(ends, outs));
+  return hipGetLastError();
 }
 
 template <typename T, typename... R>
