@@ -9,10 +9,13 @@
 //     dw[k] = sum_t g[t] x[t - (W-1) + k]              dbias = sum_t g[t]
 //
 // About 2 W + 6 operations for every element read and written: all three are
-// bound by HBM.  A thread owns 16 bytes of channels and walks the tokens of a
-// tile with the last W-1 rows in registers, so each row is read once but for
-// the W-1 rows before a tile; neighbouring lanes own neighbouring channels,
-// so every access of a wavefront is 1 KB of one row (or of two).
+// bound by HBM.  A thread owns four channels and walks the tokens of a tile
+// with the last W-1 rows in registers, so each row is read once but for the
+// W-1 rows before a tile; neighbouring lanes own neighbouring channels, so
+// every access of a wavefront is 512 bytes (bfloat16) or 1 KB of one row or of
+// two.  Eight bfloat16 channels per thread make 16-byte accesses and are
+// slower (65536 x 2560: 147 us, 137 with four; backward 2 x 8192 x 1792: 51
+// and 48): their weights, rows and gradient sums leave two wavefronts per SIMD.
 #include <type_traits>
 
 #include "launch.h"
@@ -22,6 +25,7 @@ namespace m2 {
 
 namespace {
 
+constexpr int kVec = 4;           // channels of a thread (1 where rows or parts are no multiple)
 constexpr int kLoads = 8;         // rows in flight per thread
 constexpr int kBwdWaves = 4;      // wavefronts (token tiles) per workgroup of the backward
 
@@ -328,9 +332,9 @@ __global__ void __launch_bounds__(256) conv1d_step_kernel(
   for (int j = 0; j < W - 1; ++j) *(raw_t<T, V>*)(sb + j * C) = r[j + 1];
 }
 
-bool vectors(const ConvDims& d, int v, bool back) {
-  return d.C % v == 0 && d.part[0] % v == 0 && d.part[1] % v == 0 && d.part[2] % v == 0 &&
-         d.xs % v == 0 && (!back || d.dxs % v == 0);
+bool vectors(const ConvDims& d, bool back) {
+  return d.C % kVec == 0 && d.part[0] % kVec == 0 && d.part[1] % kVec == 0 &&
+         d.part[2] % kVec == 0 && d.xs % kVec == 0 && (!back || d.dxs % kVec == 0);
 }
 
 Parts parts_of(const ConvDims& d, void* const* p) {
@@ -354,22 +358,20 @@ hipError_t by_width(const ConvDims& d, F&& f) {
 
 template <typename F>
 hipError_t dispatch(const ConvDims& d, bool back, F&& f) {
-  if (d.bf16)
-    return vectors(d, vec_of<bf16>(), back) ? by_width<bf16, vec_of<bf16>()>(d, f)
-                                            : by_width<bf16, 1>(d, f);
-  return vectors(d, vec_of<float>(), back) ? by_width<float, vec_of<float>()>(d, f)
-                                           : by_width<float, 1>(d, f);
+  const bool vec = vectors(d, back);
+  if (d.bf16) return vec ? by_width<bf16, kVec>(d, f) : by_width<bf16, 1>(d, f);
+  return vec ? by_width<float, kVec>(d, f) : by_width<float, 1>(d, f);
 }
 
-// Tokens of a backward tile: 32, or 16 or 8 where that leaves less than one
-// wavefront for each SIMD (5 x 306 x 1920 bf16: 33 us with 32, 18 with 8; 2 x
-// 2048 x 2560: 37 with 32, 31 with 16).  By the sizes alone, so that the
-// workspace is known before the pointers.
+// Tokens of a backward tile: 32, or 16 or 8 where that leaves less than two
+// wavefronts for each SIMD (2 x 2048 x 2560 bf16: 32 tokens 30 us, 16 tokens
+// 25; 1 x 38 x 2560: 8 tokens 11 us, 32 tokens 30).  By the sizes alone, so
+// that the workspace is known before the pointers.
 int bwd_tile(const ConvDims& d) {
-  const int64_t lanes = d.C / (vectors(d, d.bf16 ? 8 : 4, true) ? (d.bf16 ? 8 : 4) : 1);
+  const int64_t lanes = d.C / (vectors(d, true) ? kVec : 1);
   const int64_t per = (lanes + 63) / 64 * d.B;
   for (int n = 32; n > 8; n /= 2)
-    if (per * ((d.L + n - 1) / n) >= 1024) return n;
+    if (per * ((d.L + n - 1) / n) >= 2048) return n;
   return 8;
 }
 
@@ -391,9 +393,9 @@ hipError_t launch_conv1d(const ConvDims& d, const void* x, const float* w, const
     typedef std::remove_pointer_t<decltype(tp)> T;
     constexpr int V = decltype(v)::value, W = decltype(wd)::value;
     // long tiles read fewer rows and weights again, short ones fill the device
-    // (65536 x 2560 bf16: 147 us with 64 rows, 149 with 32, 162 with 16, 170 with 128)
+    // (65536 x 2560 bf16: 137 us with 32 rows, 141 with 64, 157 with 128)
     const int64_t per = d.C / V * d.B;
-    const int tile = per * ((d.L + 63) / 64) >= (1 << 16) ? 64 : 8;
+    const int tile = per * ((d.L + 31) / 32) >= (1 << 17) ? 32 : 8;
     const int64_t ntiles = (d.L + tile - 1) / tile;
     const unsigned grid = (unsigned)((per * ntiles + 255) / 256);
     conv1d_fwd_kernel<T, V, W><<<grid, 256, 0, s>>>((const T*)x, w, bias, (const T*)init, lengths,
