@@ -77,6 +77,8 @@ CONV = [
     ("bf16", 1, 3, (72,), 4, 0, True, True, False, None),
     ("f32", 2, 31, (8,), 4, 0, True, True, True, [-5, 900]),          # clamped to 0 and 31
     ("bf16", 1, 4100, (8,), 4, 0, True, True, True, None),            # many tiles
+    ("bf16", 2, 100, (20, 12, 4), 4, 4, True, True, True, [100, 61]),  # rows of 8-byte steps
+    ("bf16", 3, 700, (260, 64, 64), 2, 0, True, True, False, None),
 ]
 
 
@@ -228,6 +230,9 @@ SCAN = [
     ("f32", 1, 1, 1, 1, 1, False, False, False, False, None, False, 0),
     ("f32", 2, 50, 64, 16, 1, True, True, True, True, None, False, 0),
     ("f32", 4, 2100, 8, 16, 1, False, True, True, True, [2100, 64, 65, 1999], True, 0),
+    ("bf16", 2, 1100, 160, 24, 1, True, True, True, True, None, True, 40),
+    ("f32", 1, 129, 64, 64, 1, True, True, True, True, None, True, 0),
+    ("bf16", 66, 140, 500, 4, 1, True, True, True, True, None, True, 0),   # one pass, long enough to cut
 ]
 
 
