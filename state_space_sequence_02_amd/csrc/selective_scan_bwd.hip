@@ -39,9 +39,10 @@ namespace m2 {
 namespace {
 
 // Tokens of a tile whose states and decays stay in registers, and the longest
-// chunk: the workgroup's tile-start states take at most 64 KB of LDS.
+// chunk: the workgroup's tile-start states take 32 KB of LDS at 16 states, 64
+// at 32, 128 at 64 (2 x 2048 x 1536 x 64: 758 us, 949 with half the chunk).
 constexpr int bwd_tile(int K) { return K <= 4 ? 8 : 4; }
-constexpr int bwd_chunk(int K) { return K <= 4 ? 64 : K == 8 ? 32 : 16; }
+constexpr int bwd_chunk(int K) { return K <= 4 ? 64 : 32; }
 
 // The value of the lane 8 and 4 lanes away (exclusive or) in a row of 16: a
 // rotation by 8; the mirror of 8 lanes after that of each quad.
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(64 * kCarryWaves) scan_bwd_carry_kernel(
 }
 
 // part_bc: [2][tiles][B][L][G][NP] parts of dB and dC, one for each channel
-// tile of a group.  part_a: [B * chunks][D * NP + 2 D] parts of dA, dD and
+// tile of a group.  part_a: [B * chunks][D (N + 2)] parts of dA, dD and
 // ddt_bias.
 template <typename T, int K, bool GATE>
 __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
     T* __restrict__ ddt, T* __restrict__ dz, int64_t dzs, float* __restrict__ dinit,
     float* __restrict__ part_bc, float* __restrict__ part_a) {
   constexpr int NP = 4 * K, Q = bwd_chunk(K), TT = bwd_tile(K), OWN = TT / 4, NT = Q / TT;
-  constexpr int GT = K == 1 ? 8 : 4, M = GT * K;  // tokens and values summed over channels at once
+  constexpr int GT = K == 1 ? 8 : 16 / K, M = GT * K;  // tokens and values summed over channels at once
   __shared__ __align__(16) float sB[Q][NP], sC[Q][NP];
   // per wavefront and tile: the states at its start, then its dB and dC
   __shared__ __align__(16) float slot[kQuadWaves][NT][64 * K];
@@ -350,6 +351,10 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
         if constexpr (GATE) y = __builtin_fmaf(C.v[k], hh[r][k], y);
       }
       part[r & 3] = y;
+      if ((r + 1) % GT == 0) {
+        sum_channels<M>(v, lane);
+        store_sums<M, K>(res + (TT + r + 1 - GT) * NP, v, lane);
+      }
     };
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
@@ -358,10 +363,6 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
       forward(4 * o + 2, of_lane<2>(d[o]), of_lane<2>(w[o]), of_lane<2>(q[o]));
       forward(4 * o + 3, of_lane<3>(d[o]), of_lane<3>(w[o]), of_lane<3>(q[o]));
       s3[o] = GATE ? quad_sums(part, j) : 0.f;
-      if ((4 * o + 4) % GT == 0) {
-        sum_channels<M>(v, lane);
-        store_sums<M, K>(res + (TT + 4 * o + 4 - GT) * NP, v, lane);
-      }
     }
     // reverse: the gradients of the states
     float gAs[4];
@@ -382,6 +383,10 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
       }
       part[r & 3] = gB;
       gAs[r & 3] = gA;
+      if (r % GT == 0) {
+        sum_channels<M>(v, lane);
+        store_sums<M, K>(res + r * NP, v, lane);
+      }
     };
 #pragma unroll
     for (int o = OWN - 1; o >= 0; --o) {
@@ -391,10 +396,6 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
       reverse(4 * o, of_lane<0>(d[o]), of_lane<0>(w[o]), of_lane<0>(q[o]));
       s1[o] = quad_sums(part, j);
       s2[o] = quad_sums(gAs, j);
-      if (4 * o % GT == 0) {
-        sum_channels<M>(v, lane);
-        store_sums<M, K>(res + 4 * o * NP, v, lane);
-      }
     }
     const bool full = rows.whole && t + TT <= rows.valid;
     const int ty = fresh(t);
