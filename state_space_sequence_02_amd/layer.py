@@ -135,6 +135,12 @@ def _plain(t, dtype, shape, index):
             and t.get_device() == index)
 
 
+def _missing(where, **tensors):
+    """The error for a None among what a short function looks into before the call."""
+    name = next(name for name, t in tensors.items() if t is None)
+    return Mamba2Error(MAMBA2_ERR_NULL, where, f"{name} is None")
+
+
 _CURRENT = contextlib.nullcontext()
 
 
@@ -267,6 +273,8 @@ def conv1d_forward(x, weight, bias=None, init_state=None, *, parts=None, activat
     counts that add up to C; the output then comes as that many contiguous tensors,
     e.g. (H*P, G*N, G*N) for the x, B and C of an SSD call.  ``activation``: "silu"
     or "none".  Returns (y or tuple of parts, final_state[B,W-1,C])."""
+    if x is None or weight is None:
+        raise _missing("conv1d_forward", x=x, weight=weight)
     dims, ref, state, shapes, wshape, bshape, _ = _conv_plan(
         "conv1d_forward", x.shape, x.stride(), weight.shape, _parts(parts), activation, x.dtype,
         False)
@@ -291,7 +299,11 @@ def conv1d_backward(x, weight, bias, init_state, dys, dfinal=None, *, activation
     """Gradients of conv1d_forward: ``dys`` is the gradient of y, or a tuple of the
     parts' gradients.  Returns a dict with dx, dweight, dbias (None without bias)
     and dinit."""
+    if x is None or weight is None or dys is None:
+        raise _missing("conv1d_backward", x=x, weight=weight, dys=dys)
     dys = (dys,) if isinstance(dys, torch.Tensor) else tuple(dys)
+    if any(d is None for d in dys):
+        raise _missing("conv1d_backward", dys=None)
     dims, ref, state, shapes, wshape, bshape, need = _conv_plan(
         "conv1d_backward", x.shape, x.stride(), weight.shape, tuple(d.shape[-1] for d in dys),
         activation, x.dtype, False)
@@ -320,6 +332,8 @@ def conv1d_backward(x, weight, bias, init_state, dys, dfinal=None, *, activation
 def conv1d_step(x, weight, bias, state, *, parts=None, activation="silu", stream=None):
     """One token of every sequence: x[B,C], ``state``[B,W-1,C] moved on in place.
     Returns y[B,C] or the tuple of its parts."""
+    if x is None or weight is None:
+        raise _missing("conv1d_step", x=x, weight=weight)
     dims, ref, sshape, shapes, wshape, bshape, _ = _conv_plan(
         "conv1d_step", x.shape, x.stride(), weight.shape, _parts(parts), activation, x.dtype, True)
     with _owner(stream, x):
@@ -434,6 +448,8 @@ def _scan_plan(where, shape, ashape, bshape, bstrides, cshape, cstrides, zstride
                           f"{tuple(bshape)} and C {tuple(cshape)} {lead + 2}-d")
     if dtype is not _F32 and dtype is not _BF16:
         raise Mamba2Error(MAMBA2_ERR_DTYPE, where, f"u is {dtype}, needs float32 or bfloat16")
+    if zstrides is not None and len(zstrides) != len(shape):
+        raise Mamba2Error(MAMBA2_ERR_SHAPE, where, f"z is {len(zstrides)}-d, u {len(shape)}-d")
     ch, n, g = shape[-1], ashape[1], bshape[-2]
     dims = make_scan_dims(
         shape[0], 1 if step else shape[1], ch, n, g, dtype, softplus=softplus,
@@ -447,8 +463,8 @@ def _scan_plan(where, shape, ashape, bshape, bstrides, cshape, cstrides, zstride
 
 
 def _scan_plan_of(where, u, A, B, C, z, softplus, step=False):
-    if A is None or B is None or C is None:
-        raise Mamba2Error(MAMBA2_ERR_NULL, where, "A, B and C are required")
+    if u is None or A is None or B is None or C is None:
+        raise _missing(where, u=u, A=A, B=B, C=C)
     return _scan_plan(where, u.shape, A.shape, B.shape, B.stride(), C.shape, C.stride(),
                       None if z is None else z.stride(), u.dtype, bool(softplus), step)
 
@@ -619,6 +635,8 @@ def _rows(t, dims):
 def norm_forward(x, weight, bias=None, z=None, *, ngroups=1, kind="rms", eps=1e-5, stream=None):
     """RMS norm (kind="rms") or layer norm ("layer") of x, or of x * silu(z), over
     ``ngroups`` groups of the last axis; weight and bias [D] float32.  Returns y."""
+    if x is None or weight is None:
+        raise _missing("norm_forward", x=x, weight=weight)
     dims, ref, wshape, _ = _norm_plan_of("norm_forward", x, z, ngroups, kind, eps)
     with _owner(stream, x):
         y = x.new_empty(x.shape)
@@ -637,6 +655,8 @@ def norm_backward(x, weight, bias, z, dy, *, ngroups=1, kind="rms", eps=1e-5, wo
                   stream=None):
     """Gradients of norm_forward: a dict with dx, dweight, dbias (None without bias)
     and dz (None without z)."""
+    if x is None or weight is None or dy is None:
+        raise _missing("norm_backward", x=x, weight=weight, dy=dy)
     dims, ref, wshape, need = _norm_plan_of("norm_backward", x, z, ngroups, kind, eps)
     if dy.shape != x.shape or not dy.is_contiguous():
         raise Mamba2Error(MAMBA2_ERR_SHAPE, "norm_backward",

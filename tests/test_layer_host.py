@@ -311,3 +311,35 @@ def test_norm_tensors():
     _raises(m2.MAMBA2_ERR_SHAPE, "dy", m2.norm_backward, x, w, None, None, _t(96, 10).t())
     _raises(m2.MAMBA2_ERR_DTYPE, "dy", m2.norm_backward, x, w, None, None, x.float())
     _raises(m2.MAMBA2_ERR_SHAPE, "x", n, _t(96), w)
+
+
+def test_short_functions_refuse_what_is_missing():
+    u, A, B, w = torch.zeros(2, 8, 4), torch.zeros(4, 3), torch.zeros(2, 8, 1, 3), torch.zeros(4)
+    calls = [
+        lambda: m2.conv1d_forward(None, torch.zeros(4, 4)),
+        lambda: m2.conv1d_forward(u, None),
+        lambda: m2.conv1d_backward(u, torch.zeros(4, 4), None, None, None),
+        lambda: m2.conv1d_backward(u, torch.zeros(4, 4), None, None, (u, None)),
+        lambda: m2.conv1d_step(u[:, 0], None, None, torch.zeros(2, 3, 4)),
+        lambda: m2.selective_scan_forward(None, u, A, B, B),
+        lambda: m2.selective_scan_forward(u, u, None, B, B),
+        lambda: m2.selective_scan_backward(u, u, A, B, B, None, None, None, None, None),
+        lambda: m2.norm_forward(u, None),
+        lambda: m2.norm_backward(u, None, None, None, u),
+        lambda: m2.norm_backward(u, w, None, None, None),
+    ]
+    for call in calls:
+        with pytest.raises(m2.Mamba2Error) as e:
+            call()
+        assert e.value.status == m2.MAMBA2_ERR_NULL
+
+
+@pytest.mark.parametrize("z", [(4,), (8, 4), (2, 2, 8, 4), (1, 8, 4)])
+def test_gate_of_another_shape(z):
+    u, A, B = torch.zeros(2, 8, 4), torch.zeros(4, 3), torch.zeros(2, 8, 1, 3)
+    for call in (lambda: m2.selective_scan_forward(u, u, A, B, B, z=torch.zeros(z)),
+                 lambda: m2.selective_scan_backward(u, u, A, B, B, None, torch.zeros(z), None,
+                                                    None, u)):
+        with pytest.raises(m2.Mamba2Error) as e:
+            call()
+        assert e.value.status == m2.MAMBA2_ERR_SHAPE
