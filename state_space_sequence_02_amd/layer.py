@@ -41,11 +41,13 @@ def _stride(where, name, shape, st, lead):
             raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
                               f"{name} has gaps inside a token (strides {st})")
         row *= shape[i]
-    step, count = 0, 1  # the innermost token axis that has more than one entry sets the step
+    # the innermost token axis with more than one entry sets the step; a step of 0 is one too
+    # (a row for all tokens, which the kernels would read past)
+    step, count = None, 1
     for i in range(lead - 1, -1, -1):
         if shape[i] == 1:
             continue
-        if step == 0:
+        if step is None:
             step = st[i]
         elif st[i] != step * count:
             raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
