@@ -225,7 +225,9 @@ __global__ void __launch_bounds__(block_of(TEAM)) norm_bwd_kernel(
         s[2] = __builtin_fmaf(d, v[k][e], s[2]);
       }
     team_sum<TEAM, 3>(s, red3);
-    const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], inv, eps));
+    // a team without a row: 0, else eps = 0 makes it infinite and its 0 * xh
+    // a NaN in the weights' gradients
+    const float rstd = live ? __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], inv, eps)) : 0.f;
     const float md = layer ? s[1] * inv : 0.f;
     const float mx = s[2] * inv * rstd;  // mean(d xh)
     float gx[NV][V], gz[NV][V];
