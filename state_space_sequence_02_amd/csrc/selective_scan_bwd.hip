@@ -276,15 +276,20 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
   const int64_t srow = (p.b * a.Dm + p.c) * a.N;
   const int64_t row = ((p.b * a.chunks + p.chunk) * a.Dm + p.c) * NP + K * j;
   States<K> A2, h, ag, dA;
-  A2.load_n(a.A + p.c * a.N, K * j, a.N, kLog2e);
+  // a lane without a channel: decay 1, state and gradient 0.  With the tile's
+  // first channel's instead, a negative bias (its time step, without softplus)
+  // makes them grow, and 0 * infinity is no 0 in the sums over channels
 #pragma unroll
-  for (int k = 0; k < K; ++k) h.v[k] = ag.v[k] = dA.v[k] = 0.f;
-  if (a.chunks > 1) {
-    h.load(hs + row);
-    ag.load(ge + row);
-  } else {
-    if (a.init) h.load_n(a.init + srow, K * j, a.N);
-    if (dfinal) ag.load_n(dfinal + srow, K * j, a.N);
+  for (int k = 0; k < K; ++k) A2.v[k] = h.v[k] = ag.v[k] = dA.v[k] = 0.f;
+  if (p.live) {
+    A2.load_n(a.A + p.c * a.N, K * j, a.N, kLog2e);
+    if (a.chunks > 1) {
+      h.load(hs + row);
+      ag.load(ge + row);
+    } else {
+      if (a.init) h.load_n(a.init + srow, K * j, a.N);
+      if (dfinal) ag.load_n(dfinal + srow, K * j, a.N);
+    }
   }
   const int tiles = (rows.n + TT - 1) / TT;
   Tokens<T, TT, GATE> cur, nxt;
