@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
       if (dfinal) ag.load_n(dfinal + srow, K * j, a.N);
     }
   }
-  const int tiles = (rows.n + TT - 1) / TT;
+  const int tiles = (rows.valid + TT - 1) / TT;  // those that hold a token
   Tokens<T, TT, GATE> cur, nxt;
   cur.template load<false, false>(a, p, rows, 0);
   __syncthreads();
@@ -321,10 +321,11 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
     }
     cur = nxt;
   }
-  h.store(&slot[wave][tiles - 1][lane * K]);
-
   float dDs = 0.f, dbs = 0.f;
-  cur.template load<true, true>(a, p, rows, (tiles - 1) * TT);
+  if (tiles > 0) {
+    h.store(&slot[wave][tiles - 1][lane * K]);
+    cur.template load<true, true>(a, p, rows, (tiles - 1) * TT);
+  }
   T* dub = du + (p.b * a.L + p.t0) * a.Dm + p.c0;
   T* ddtb = ddt + (p.b * a.L + p.t0) * a.Dm + p.c0;
   T* dzb = GATE ? dz + (p.b * a.L + p.t0) * dzs + p.c0 : nullptr;
@@ -368,6 +369,17 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
       forward(4 * o + 2, of_lane<2>(d[o]), of_lane<2>(w[o]), of_lane<2>(q[o]));
       forward(4 * o + 3, of_lane<3>(d[o]), of_lane<3>(w[o]), of_lane<3>(q[o]));
       s3[o] = GATE ? quad_sums(part, j) : 0.f;
+    }
+    // tokens behind the sequence keep its last state and add nothing to dA: the
+    // states before them are taken as 0, or an infinite one would be 0 * infinity
+    if (t + TT > rows.valid) {
+#pragma unroll
+      for (int r = 0; r < TT; ++r) {
+        if (t + r + 1 >= rows.valid) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) hh[r][k] = 0.f;
+        }
+      }
     }
     // reverse: the gradients of the states
     float gAs[4];
@@ -416,7 +428,7 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
         dzv = to_f32(cur.dy[o]) * __builtin_fmaf(Dv, u, s3[o]) *
               (sg * __builtin_fmaf(zv, 1.f - sg, 1.f));
       }
-      const float duv = __builtin_fmaf(s1[o], d[o], Dv * q[o]);
+      float duv = __builtin_fmaf(s1[o], d[o], Dv * q[o]);
       dDs = __builtin_fmaf(q[o], u, dDs);
       const int64_t at = (int64_t)(ty + 4 * o) * a.Dm, zat = (int64_t)(ty + 4 * o) * dzs;
       if (full) {
@@ -425,7 +437,7 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
         lane_at(ddtb + at, rows.off) = from_f32<T>(dd);
         if constexpr (GATE) lane_at(dzb + zat, dzoff) = from_f32<T>(dzv);
       } else if (p.live && tq < rows.n) {
-        if (tq >= rows.valid) dd = 0.f;
+        if (tq >= rows.valid) dd = duv = dzv = 0.f;
         dbs += dd;
         lane_at(dub + at, rows.off) = from_f32<T>(duv);
         lane_at(ddtb + at, rows.off) = from_f32<T>(dd);
@@ -435,7 +447,13 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
     cur = nxt;
   }
 
+  // what is left of the chunk lies behind the sequence
   if (p.live) {
+    for (int t = tiles * TT; t + j < rows.n; t += 4) {
+      lane_at(dub + (int64_t)t * a.Dm, rows.off) = (T)0.f;
+      lane_at(ddtb + (int64_t)t * a.Dm, rows.off) = (T)0.f;
+      if constexpr (GATE) lane_at(dzb + (int64_t)t * dzs, dzoff) = (T)0.f;
+    }
     if (dinit && p.chunk == 0) ag.store_n(dinit + srow, K * j, a.N);
     float* pa = part_a + (p.b * a.chunks + p.chunk) * (a.Dm * (a.N + 2));
     dA.store_n(pa + p.c * a.N, K * j, a.N);
@@ -458,9 +476,11 @@ __global__ void __launch_bounds__(64 * kQuadWaves) scan_bwd_main_kernel(
       const int t = i / NP, n = i % NP;
       if (p.t0 + t < p.t1) {
         float s = 0.f;
+        if (t < rows.valid) {
 #pragma unroll
-        for (int w = 0; w < kQuadWaves; ++w)
-          s += slot[w][t / TT][arr * TT * NP + t % TT * NP + n];
+          for (int w = 0; w < kQuadWaves; ++w)
+            s += slot[w][t / TT][arr * TT * NP + t % TT * NP + n];
+        }
         out[((p.t0 + t) * a.G + p.g) * NP + n] = s;
       }
     }
