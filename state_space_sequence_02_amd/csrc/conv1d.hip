@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves) conv1d_bwd_kernel(
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const bool mine = t + i < own;
+        const bool mine = t + i < own && t + i < len;  // g is 0 behind len, but x may be infinite
         float out[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {

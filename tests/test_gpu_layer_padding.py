@@ -4,6 +4,7 @@ over tokens take nothing from there (0 * infinity is no term of theirs)."""
 import pytest
 import torch
 
+import layer_reference as ref
 from gpu_helpers import say
 from layer_bounds import scan_gradients
 from layer_reference import F, to64, within
@@ -105,3 +106,28 @@ def test_a_state_that_overflows_at_the_last_token(m2, n, m, ch, ns):
         fits = v.abs() < 1e38
         assert fits.any()
         within(name, torch.where(fits, got[name].cpu().to(F), v), v, bound)
+
+
+@pytest.mark.parametrize("n,m,c,w", [(40, 17, 64, 4), (130, 100, 64, 4), (20, 5, 33, 3),
+                                     (9, 1, 8, 2), (40, 32, 64, 4), (40, 31, 7, 4)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=("f32", "bf16"))
+def test_convolution_gradient_with_an_infinite_last_token(m2, n, m, c, w, dtype):
+    """Without an activation an infinite last row meets only the last tap's gradient; the
+    taps before it would meet it in the padding, where g is zero."""
+    r = _gen(n + c)
+    x, dy = r(2, n, c).to(dtype), r(2, n, c).to(dtype)
+    wt, bias = r(c, w), r(c)
+    x[1, m - 1] = INF
+    lens = [n, m]
+    got = m2.conv1d_backward(x.cuda(), wt.cuda(), bias.cuda(), None, dy.cuda(), activation="none",
+                             lengths=torch.tensor(lens, dtype=torch.int32).cuda())
+    a = (to64(x), to64(wt), to64(bias), torch.zeros(2, w - 1, c, dtype=F))
+    want = ref.grads(lambda *v: ref.conv(*v, lens, False), a, (to64(dy), None))
+    assert torch.isfinite(want[1][:, :-1]).all() and torch.isinf(want[1][:, -1]).all()
+    g = got["dweight"].cpu().to(F)
+    # two roundings a product, at most 32 + 4 + the tiles' additions, on the terms' sizes
+    size = torch.where(torch.isinf(a[0]), torch.zeros_like(a[0]), a[0]).abs()
+    big = ref.grads(lambda *v: ref.conv(*v, lens, False), (size,) + a[1:], (to64(dy).abs(), None))
+    within("dweight", g[:, :-1], want[1][:, :-1], (40 + 2 * n) * ref.U * big[1][:, :-1])
+    assert torch.equal(g[:, -1], want[1][:, -1])
+    assert (got["dx"][1, m:] == 0).all() and torch.isfinite(got["dx"]).all()
