@@ -16,16 +16,24 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import operator
+from collections.abc import Iterable
 
 import torch
 
 from . import (MAMBA2_DTYPE_BF16, MAMBA2_DTYPE_F32, MAMBA2_ERR_DTYPE, MAMBA2_ERR_NULL,
-               MAMBA2_ERR_SHAPE, MAMBA2_ERR_UNSUPPORTED, Mamba2ConvDims, Mamba2Error,
-               Mamba2NormDims, Mamba2ScanDims, _check, _lib, _ptr, _req_bytes, _same_device)
+               MAMBA2_ERR_SHAPE, MAMBA2_ERR_UNSUPPORTED, MAMBA2_ERR_WORKSPACE, Mamba2ConvDims,
+               Mamba2Error, Mamba2NormDims, Mamba2ScanDims, _check, _lib, _ptr, _req_bytes,
+               _same_device)
 
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+_Tensor = torch.Tensor
 _ACTIVATIONS = {"none": 0, "silu": 1}
 _KINDS = {"rms": 0, "layer": 1}
+
+
+def _known(name, names):
+    return isinstance(name, str) and name in names
 
 
 def _io(dims):
@@ -133,14 +141,21 @@ def _plain(t, dtype, shape, index):
     """Whether t is a contiguous tensor of this type and shape on device ``index``.  The
     short functions ask this first and launch at once where it holds for all inputs; else
     the mamba2_* function looks closer and says what is wrong."""
-    return (t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == index)
+    return (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == index)
 
 
 def _missing(where, **tensors):
-    """The error for a None among what a short function looks into before the call."""
-    name = next(name for name, t in tensors.items() if t is None)
-    return Mamba2Error(MAMBA2_ERR_NULL, where, f"{name} is None")
+    """The error for what is no tensor among what a short function looks into before the call."""
+    name, t = next((name, t) for name, t in tensors.items() if not isinstance(t, _Tensor))
+    if t is None:
+        return Mamba2Error(MAMBA2_ERR_NULL, where, f"{name} is None")
+    return Mamba2Error(MAMBA2_ERR_SHAPE, where, f"{name} is a {type(t).__name__}, not a tensor")
+
+
+def _like(t):
+    """The gradient's tensor of an optional input (the call refuses what is no tensor)."""
+    return torch.empty_like(t) if isinstance(t, _Tensor) else None
 
 
 _CURRENT = contextlib.nullcontext()
@@ -156,11 +171,14 @@ def _owner(stream, t):
     return torch.cuda.stream(stream)
 
 
-def _workspace(need, workspace, t):
+def _workspace(where, need, workspace, t):
     """The caller's workspace, or one of ``need`` bytes (where the sizes are refused, need
     is 0 and the C call says why), and its size."""
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=t.device)
+    elif not isinstance(workspace, _Tensor):
+        raise Mamba2Error(MAMBA2_ERR_WORKSPACE, where,
+                          f"workspace is a {type(workspace).__name__}, not a tensor")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -173,7 +191,7 @@ def make_conv_dims(batch, seqlen, channels, width, parts, dtype, *, activation="
     parts = (channels,) if parts is None else tuple(parts)
     if not 1 <= len(parts) <= 3:
         raise Mamba2Error(MAMBA2_ERR_SHAPE, "make_conv_dims", f"{len(parts)} parts: 1 to 3 are possible")
-    if activation not in _ACTIVATIONS:
+    if not _known(activation, _ACTIVATIONS):
         raise Mamba2Error(MAMBA2_ERR_UNSUPPORTED, "make_conv_dims", f"unknown activation {activation!r}")
     code = MAMBA2_DTYPE_BF16 if dtype is _BF16 else MAMBA2_DTYPE_F32 if dtype is _F32 else int(dtype)
     d = Mamba2ConvDims(batch, seqlen, channels, width)
@@ -260,8 +278,18 @@ def _conv_plan(where, shape, strides, wshape, parts, activation, dtype, step):
             mamba2_conv1d_backward_workspace_bytes(dims))
 
 
-def _parts(parts):
-    return None if parts is None else tuple(parts)
+def _conv_plan_of(where, x, weight, parts, activation, step=False):
+    if not (isinstance(x, _Tensor) and isinstance(weight, _Tensor)):
+        raise _missing(where, x=x, weight=weight)
+    if parts is not None:
+        try:
+            parts = tuple(map(operator.index, parts))
+        except TypeError:
+            raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
+                              f"parts is {parts!r}, not up to three channel counts") from None
+    if not _known(activation, _ACTIVATIONS):
+        raise Mamba2Error(MAMBA2_ERR_UNSUPPORTED, where, f"unknown activation {activation!r}")
+    return _conv_plan(where, x.shape, x.stride(), weight.shape, parts, activation, x.dtype, step)
 
 
 def _optional(t, dtype, shape, index):
@@ -275,11 +303,8 @@ def conv1d_forward(x, weight, bias=None, init_state=None, *, parts=None, activat
     counts that add up to C; the output then comes as that many contiguous tensors,
     e.g. (H*P, G*N, G*N) for the x, B and C of an SSD call.  ``activation``: "silu"
     or "none".  Returns (y or tuple of parts, final_state[B,W-1,C])."""
-    if x is None or weight is None:
-        raise _missing("conv1d_forward", x=x, weight=weight)
-    dims, ref, state, shapes, wshape, bshape, _ = _conv_plan(
-        "conv1d_forward", x.shape, x.stride(), weight.shape, _parts(parts), activation, x.dtype,
-        False)
+    dims, ref, state, shapes, wshape, bshape, _ = _conv_plan_of(
+        "conv1d_forward", x, weight, parts, activation)
     with _owner(stream, x):
         ys = [x.new_empty(p) for p in shapes]
         final = x.new_empty(state)
@@ -301,19 +326,18 @@ def conv1d_backward(x, weight, bias, init_state, dys, dfinal=None, *, activation
     """Gradients of conv1d_forward: ``dys`` is the gradient of y, or a tuple of the
     parts' gradients.  Returns a dict with dx, dweight, dbias (None without bias)
     and dinit."""
-    if x is None or weight is None or dys is None:
-        raise _missing("conv1d_backward", x=x, weight=weight, dys=dys)
-    dys = (dys,) if isinstance(dys, torch.Tensor) else tuple(dys)
-    if any(d is None for d in dys):
-        raise _missing("conv1d_backward", dys=None)
-    dims, ref, state, shapes, wshape, bshape, need = _conv_plan(
-        "conv1d_backward", x.shape, x.stride(), weight.shape, tuple(d.shape[-1] for d in dys),
-        activation, x.dtype, False)
+    dys = (dys,) if isinstance(dys, _Tensor) or not isinstance(dys, Iterable) else tuple(dys)
+    for i, d in enumerate(dys):
+        if not isinstance(d, _Tensor):
+            raise _missing("conv1d_backward", **{f"dy{i}": d})
+        if not d.dim():
+            raise Mamba2Error(MAMBA2_ERR_SHAPE, "conv1d_backward", f"dy{i} has no channels")
+    dims, ref, state, shapes, wshape, bshape, need = _conv_plan_of(
+        "conv1d_backward", x, weight, tuple(d.shape[-1] for d in dys), activation)
     with _owner(stream, x):
-        workspace, n = _workspace(need, workspace, x)
+        workspace, n = _workspace("conv1d_backward", need, workspace, x)
         g = {"dx": x.new_empty(x.shape), "dweight": torch.empty_like(weight),
-             "dbias": None if bias is None else torch.empty_like(bias),
-             "dinit": x.new_empty(state)}
+             "dbias": _like(bias), "dinit": x.new_empty(state)}
     dy3 = dys + (None,) * (3 - len(dys))
     i = x.get_device()
     if (i >= 0 and n >= need > 0 and _plain(weight, _F32, wshape, i)
@@ -334,10 +358,8 @@ def conv1d_backward(x, weight, bias, init_state, dys, dfinal=None, *, activation
 def conv1d_step(x, weight, bias, state, *, parts=None, activation="silu", stream=None):
     """One token of every sequence: x[B,C], ``state``[B,W-1,C] moved on in place.
     Returns y[B,C] or the tuple of its parts."""
-    if x is None or weight is None:
-        raise _missing("conv1d_step", x=x, weight=weight)
-    dims, ref, sshape, shapes, wshape, bshape, _ = _conv_plan(
-        "conv1d_step", x.shape, x.stride(), weight.shape, _parts(parts), activation, x.dtype, True)
+    dims, ref, sshape, shapes, wshape, bshape, _ = _conv_plan_of(
+        "conv1d_step", x, weight, parts, activation, True)
     with _owner(stream, x):
         ys = [x.new_empty(p) for p in shapes]
     out = ys + [None] * (3 - len(ys))
@@ -465,8 +487,11 @@ def _scan_plan(where, shape, ashape, bshape, bstrides, cshape, cstrides, zstride
 
 
 def _scan_plan_of(where, u, A, B, C, z, softplus, step=False):
-    if u is None or A is None or B is None or C is None:
+    if not (isinstance(u, _Tensor) and isinstance(A, _Tensor) and isinstance(B, _Tensor)
+            and isinstance(C, _Tensor)):
         raise _missing(where, u=u, A=A, B=B, C=C)
+    if z is not None and not isinstance(z, _Tensor):
+        raise _missing(where, z=z)
     return _scan_plan(where, u.shape, A.shape, B.shape, B.stride(), C.shape, C.stride(),
                       None if z is None else z.stride(), u.dtype, bool(softplus), step)
 
@@ -490,7 +515,7 @@ def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, init_st
     dims, ref, state, ashape, cshape, bc, need, _ = _scan_plan_of(
         "selective_scan_forward", u, A, B, C, z, softplus)
     with _owner(stream, u):
-        workspace, n = _workspace(need, workspace, u)
+        workspace, n = _workspace("selective_scan_forward", need, workspace, u)
         y = torch.empty_like(u, memory_format=torch.contiguous_format)
         final = u.new_empty(state, dtype=_F32)
     i = u.get_device()
@@ -514,12 +539,12 @@ def selective_scan_backward(u, dt, A, B, C, D, z, dt_bias, init_state, dy, dfina
     dims, ref, state, ashape, cshape, bc, _, need = _scan_plan_of(
         "selective_scan_backward", u, A, B, C, z, softplus)
     with _owner(stream, u):
-        workspace, n = _workspace(need, workspace, u)
+        workspace, n = _workspace("selective_scan_backward", need, workspace, u)
         du, ddt = u.new_empty(u.shape), u.new_empty(u.shape)
         dA, dB, dC = torch.empty_like(A), u.new_empty(B.shape), u.new_empty(C.shape)
-        dD = None if D is None else torch.empty_like(D)
+        dD = _like(D)
         dz = None if z is None else u.new_empty(u.shape)
-        dbias = None if dt_bias is None else torch.empty_like(dt_bias)
+        dbias = _like(dt_bias)
         dinit = u.new_empty(state, dtype=_F32)
     i = u.get_device()
     if (n >= need > 0 and _scan_plain(i, u, dt, A, B, C, D, z, dt_bias, ashape, cshape, bc)
@@ -564,7 +589,7 @@ def selective_scan_step(u, dt, A, B, C, D, z, dt_bias, state, *, softplus=True, 
 
 def make_norm_dims(rows, channels, ngroups, dtype, *, kind="rms", eps=1e-5, x_stride=0, z_stride=0,
                    dz_stride=0) -> Mamba2NormDims:
-    if kind not in _KINDS:
+    if not _known(kind, _KINDS):
         raise Mamba2Error(MAMBA2_ERR_UNSUPPORTED, "make_norm_dims", f"unknown norm {kind!r}")
     code = MAMBA2_DTYPE_BF16 if dtype is _BF16 else MAMBA2_DTYPE_F32 if dtype is _F32 else int(dtype)
     return Mamba2NormDims(rows, channels, ngroups, x_stride, z_stride, dz_stride, eps, _KINDS[kind],
@@ -625,7 +650,13 @@ def _norm_plan(where, shape, strides, zshape, zstrides, ngroups, kind, eps, dtyp
     return (dims, ctypes.byref(dims), shape[-1:], mamba2_norm_backward_workspace_bytes(dims))
 
 
-def _norm_plan_of(where, x, z, ngroups, kind, eps):
+def _norm_plan_of(where, x, weight, z, ngroups, kind, eps):
+    if not (isinstance(x, _Tensor) and isinstance(weight, _Tensor)):
+        raise _missing(where, x=x, weight=weight)
+    if z is not None and not isinstance(z, _Tensor):
+        raise _missing(where, z=z)
+    if not _known(kind, _KINDS):
+        raise Mamba2Error(MAMBA2_ERR_UNSUPPORTED, where, f"unknown norm {kind!r}")
     return _norm_plan(where, x.shape, x.stride(), None if z is None else z.shape,
                       None if z is None else z.stride(), ngroups, kind, float(eps), x.dtype)
 
@@ -637,9 +668,7 @@ def _rows(t, dims):
 def norm_forward(x, weight, bias=None, z=None, *, ngroups=1, kind="rms", eps=1e-5, stream=None):
     """RMS norm (kind="rms") or layer norm ("layer") of x, or of x * silu(z), over
     ``ngroups`` groups of the last axis; weight and bias [D] float32.  Returns y."""
-    if x is None or weight is None:
-        raise _missing("norm_forward", x=x, weight=weight)
-    dims, ref, wshape, _ = _norm_plan_of("norm_forward", x, z, ngroups, kind, eps)
+    dims, ref, wshape, _ = _norm_plan_of("norm_forward", x, weight, z, ngroups, kind, eps)
     with _owner(stream, x):
         y = x.new_empty(x.shape)
     i = x.get_device()
@@ -657,17 +686,19 @@ def norm_backward(x, weight, bias, z, dy, *, ngroups=1, kind="rms", eps=1e-5, wo
                   stream=None):
     """Gradients of norm_forward: a dict with dx, dweight, dbias (None without bias)
     and dz (None without z)."""
-    if x is None or weight is None or dy is None:
-        raise _missing("norm_backward", x=x, weight=weight, dy=dy)
-    dims, ref, wshape, need = _norm_plan_of("norm_backward", x, z, ngroups, kind, eps)
+    dims, ref, wshape, need = _norm_plan_of("norm_backward", x, weight, z, ngroups, kind, eps)
+    if not isinstance(dy, _Tensor):
+        raise _missing("norm_backward", dy=dy)
+    if bias is not None and not isinstance(bias, _Tensor):
+        raise _missing("norm_backward", bias=bias)
     if dy.shape != x.shape or not dy.is_contiguous():
         raise Mamba2Error(MAMBA2_ERR_SHAPE, "norm_backward",
                           f"dy {tuple(dy.shape)} must be contiguous and of x's shape "
                           f"{tuple(x.shape)}")
     with _owner(stream, x):
-        workspace, n = _workspace(need, workspace, x)
+        workspace, n = _workspace("norm_backward", need, workspace, x)
         g = {"dx": x.new_empty(x.shape), "dweight": torch.empty_like(weight),
-             "dbias": None if bias is None else torch.empty_like(bias),
+             "dbias": _like(bias),
              "dz": None if z is None else x.new_empty(x.shape)}
     i = x.get_device()
     if (i >= 0 and n >= need > 0 and _plain(weight, _F32, wshape, i)
