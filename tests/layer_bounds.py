@@ -7,13 +7,17 @@ or sum as the value it belongs to, so they stay tight over long sequences
 those of layer_reference: the sigmoid is off by a relative (2 |v| + 8) U, the
 time step by (3 |raw| + 10) U with softplus and U without, the decay
 a = exp(d A) by (|d A| (cd + 3) + 3) U with cd the time step's count.  FIRST
-covers the products of two errors.
+covers the products of two errors.  TINY is float32's smallest normal number:
+the exponential gives 0 for results below it, so a decay is also off by TINY,
+and with it what it multiplies by TINY times that (64 states at time steps of
+0.7 reach exp(-90) = 8e-40 in one token).
 """
 import torch
 
 from layer_reference import F, U, conv, grads, half_step, lengths_of, norm, norm_terms, silu, softplus
 
 FIRST = 1 + 2.0 ** -8
+TINY = 2.0 ** -126
 
 
 def _rounded(want, err, dtype):
@@ -52,6 +56,7 @@ def scan_gradients(u, dt, A, B, C, D, z, dt_bias, init, lengths, use_softplus, d
         term = w[:, t, :, None] * Bs[:, t]
         new = a * hs[-1] + term
         e = a * eh[-1] + U * ((dA.abs() * c3 + 3) * (a * hs[-1]).abs() + c3 * term.abs() + new.abs())
+        e = e + TINY * (1 + hs[-1].abs())
         on = live[:, t, :, None]
         hs.append(torch.where(on, new, hs[-1]))
         eh.append(torch.where(on, e, eh[-1]))
@@ -65,7 +70,7 @@ def scan_gradients(u, dt, A, B, C, D, z, dt_bias, init, lengths, use_softplus, d
         g = ag + qC
         eg = ea + U * (rq[:, t, :, None] * qC.abs() + g.abs())
         nag = a * g
-        nea = a * eg + U * (dA.abs() * c3 + 4) * nag.abs()
+        nea = a * eg + U * (dA.abs() * c3 + 4) * nag.abs() + TINY * (1 + g.abs())
         # what a kernel holds: the recurrence's error twice (chunks), and a rounding
         full = lambda e, v: 2 * e + U * v.abs()
         m, hp = nag * hs[t], full(eh[t], hs[t])
@@ -89,10 +94,11 @@ def scan_gradients(u, dt, A, B, C, D, z, dt_bias, init, lengths, use_softplus, d
         dd, edd = keep(dd), keep(edd)
     du = gB * d + Dv * q
     edu = egB * d.abs() + (cd + 2) * U * (gB * d).abs() + (rq + 2) * U * (Dv * q).abs()
-    # an element of a sum over tokens passes a chunk's tokens, then the parts of the
-    # batch's chunks (16 tokens at least); one over channels 16 lanes by halves, four
-    # wavefronts and the channel tiles
-    over_tokens = 64 + 16 + b * -(-n // 16)
+    # an element of a sum over tokens passes a chunk's 64 tokens at most, then the parts of
+    # the batch's chunks (16 tokens at least): eight at a time by a tree, every sixteenth
+    # eight in a row, up to seven single ones, and 16 wavefronts; one over channels 16
+    # lanes by halves, four wavefronts and the channel tiles
+    over_tokens = 64 + 3 + b * -(-n // 16) // 128 + 1 + 7 + 16
     over_channels = 8 + -(-(ch // groups) // 64)
 
     def by_group(v, e):
