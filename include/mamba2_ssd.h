@@ -340,15 +340,21 @@ int mamba2_ssd_backward_profile(const mamba2_dims* dims, const void* x, const vo
  * Strides: where dims has a <name>_stride, token t of batch b of that tensor
  *        starts at element (b * L + t) * <name>_stride of it (row r of a norm
  *        at r * <name>_stride): a tensor may be a column range of a wider
- *        one.  0 means rows without gaps.  The base pointer is 16-byte
- *        aligned; rows need not be (rows and sizes that are multiples of 16
- *        bytes run faster).  Everything else is contiguous.
+ *        one.  0 means rows without gaps; a stride is at least a row (a row
+ *        that stands for several tokens is refused) and at most 2^24.  The
+ *        base pointer is 16-byte aligned; rows need not be (rows and sizes
+ *        that are multiples of 16 bytes run faster).  Everything else is
+ *        contiguous.
+ * Sizes: batch <= 65535; batch * L, and the rows of a norm, <= 2^30; channels
+ *        <= 2^20; each operator's further bounds stand at it.  Beyond them
+ *        a call returns MAMBA2_ERR_UNSUPPORTED.
  * lengths: int32 [B] or NULL (every sequence has L tokens): sequence b has
  *        lengths[b] tokens, values outside 0 .. L are taken as the nearer
  *        bound.  What stands in the inputs behind them is not read; outputs
- *        and gradients there are written as zeros.  A final state is the
- *        state after the sequence's own last token (the initial state where
- *        it has none).
+ *        and gradients there are written as zeros, also where the sequence's
+ *        own are not finite, and sums over tokens take nothing from there.
+ *        A final state is the state after the sequence's own last token (the
+ *        initial state where it has none).
  * Outputs do not overlap inputs, but final_state may be init_state.
  * Gradients that are sums over tokens are formed from per-workgroup float32
  * parts in a fixed order: the same call gives the same bits.
@@ -380,7 +386,7 @@ typedef struct {
  *     init_state    [B, W-1, C] or NULL; final_state the same or NULL (not
  *                   written): the last W-1 rows of [init_state; x]
  * x, y and the states have the type of dims.  Sums are float32.  Supported:
- * batch <= 65535, C <= 2^20, C * B * ceil(L / 8) <= 2^31.
+ * C * B * ceil(L / 8) <= 2^31.
  */
 int mamba2_conv1d_forward(const mamba2_conv_dims* dims, const void* x, const float* weight,
                           const float* bias, const void* init_state, const int32_t* lengths,
@@ -441,8 +447,9 @@ typedef struct {
  *     A             [D, N] float32, <= 0; D, dt_bias [D] float32 or NULL
  *     init_state, final_state [B, D, N] float32 or NULL
  * u, dt, B, C, z and y have the type of dims; the recurrence is float32.
- * Supported: batch <= 65535, B * D <= 2^26, (L / 16) * (D / 64) < 2^24,
- * B * L * G * N <= 2^28 (a problem too large gives MAMBA2_ERR_UNSUPPORTED).
+ * Supported: B * D <= 2^26; ceil(L / 16) * G * ceil(D / G / 64) < 2^24 (the
+ * backward's workgroups: 64 channels of one group each, so many small groups
+ * count in full); B * L * G * N <= 2^29 (N = 1 counts as 2).
  * Workspace at least mamba2_selective_scan_workspace_bytes(dims) (0: dims invalid),
  * 256-byte aligned.
  */

@@ -8,14 +8,19 @@
 //     dx[s] = sum_k w[k] g[s + (W-1) - k]              (+ dfinal at the last W-1 rows)
 //     dw[k] = sum_t g[t] x[t - (W-1) + k]              dbias = sum_t g[t]
 //
-// About 2 W + 6 operations for every element read and written: all three are
-// bound by HBM.  A thread owns four channels and walks the tokens of a tile
-// with the last W-1 rows in registers, so each row is read once but for the
-// W-1 rows before a tile; neighbouring lanes own neighbouring channels, so
-// every access of a wavefront is 512 bytes (bfloat16) or 1 KB of one row or of
-// two.  Eight bfloat16 channels per thread make 16-byte accesses and are
-// slower (65536 x 2560: 147 us, 137 with four; backward 2 x 8192 x 1792: 51
-// and 48): their weights, rows and gradient sums leave two wavefronts per SIMD.
+// About 2 W + 6 operations for every element read and written: the forward is
+// bound by HBM, one token by the launch.  The backward's 6 W + 12 (the
+// convolution again, silu's slope, W products each for dx and dw) keep the
+// vector ALU 79 % busy (2 x 8192 x 1792 bf16: 43 us, 29 for its bytes).  A
+// thread owns four channels and walks the tokens of a tile with the last W-1
+// rows in registers, so each row is read once but for the W-1 rows before a
+// tile; neighbouring lanes own neighbouring channels, so every access of a
+// wavefront is 512 bytes (bfloat16) or 1 KB of one row or of two.  Eight
+// bfloat16 channels per thread make 16-byte accesses and are slower (65536 x
+// 2560: 147 us, 137 with four; backward 2 x 8192 x 1792: 51 and 48): their
+// weights, rows and gradient sums leave two wavefronts per SIMD.  Where a row,
+// part or stride is no multiple of four, a thread owns one channel (16384 x
+// 2048 bf16: 30 us, 55 with rows of 2049; backward 44 and 77).
 #include <type_traits>
 
 #include "launch.h"

@@ -40,7 +40,7 @@ namespace {
 
 // Tokens of a tile whose states and decays stay in registers, and the longest
 // chunk: the workgroup's tile-start states take 32 KB of LDS at 16 states, 64
-// at 32, 128 at 64 (2 x 2048 x 1536 x 64: 758 us, 949 with half the chunk).
+// at 32, 128 at 64 (2 x 2048 x 1536 x 64: 749 us, 949 with half the chunk).
 constexpr int bwd_tile(int K) { return K <= 4 ? 8 : 4; }
 constexpr int bwd_chunk(int K) { return K <= 4 ? 64 : 32; }
 
