@@ -16,8 +16,6 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
-import operator
-from collections.abc import Iterable
 
 import torch
 
@@ -141,16 +139,22 @@ def _plain(t, dtype, shape, index):
     """Whether t is a contiguous tensor of this type and shape on device ``index``.  The
     short functions ask this first and launch at once where it holds for all inputs; else
     the mamba2_* function looks closer and says what is wrong."""
-    return (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous() and t.get_device() == index)
+    try:
+        return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == index)
+    except AttributeError:
+        return False
 
 
-def _missing(where, **tensors):
-    """The error for what is no tensor among what a short function looks into before the call."""
-    name, t = next((name, t) for name, t in tensors.items() if not isinstance(t, _Tensor))
-    if t is None:
-        return Mamba2Error(MAMBA2_ERR_NULL, where, f"{name} is None")
-    return Mamba2Error(MAMBA2_ERR_SHAPE, where, f"{name} is a {type(t).__name__}, not a tensor")
+def _tensors(where, **tensors):
+    """Raises the error for what is no tensor among what a short function looks into before
+    the call."""
+    for name, t in tensors.items():
+        if t is None:
+            raise Mamba2Error(MAMBA2_ERR_NULL, where, f"{name} is None")
+        if not isinstance(t, _Tensor):
+            raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
+                              f"{name} is a {type(t).__name__}, not a tensor")
 
 
 def _like(t):
@@ -279,17 +283,20 @@ def _conv_plan(where, shape, strides, wshape, parts, activation, dtype, step):
 
 
 def _conv_plan_of(where, x, weight, parts, activation, step=False):
-    if not (isinstance(x, _Tensor) and isinstance(weight, _Tensor)):
-        raise _missing(where, x=x, weight=weight)
-    if parts is not None:
-        try:
-            parts = tuple(map(operator.index, parts))
-        except TypeError:
-            raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
-                              f"parts is {parts!r}, not up to three channel counts") from None
-    if not _known(activation, _ACTIVATIONS):
-        raise Mamba2Error(MAMBA2_ERR_UNSUPPORTED, where, f"unknown activation {activation!r}")
-    return _conv_plan(where, x.shape, x.stride(), weight.shape, parts, activation, x.dtype, step)
+    try:
+        if parts is not None and type(parts) is not tuple:
+            parts = tuple(parts)
+        return _conv_plan(where, x.shape, x.stride(), weight.shape, parts, activation, x.dtype,
+                          step)
+    except (AttributeError, TypeError, Mamba2Error) as e:  # what is of another kind, if anything
+        _tensors(where, x=x, weight=weight)
+        if isinstance(e, Mamba2Error):
+            raise
+        if not _known(activation, _ACTIVATIONS):
+            raise Mamba2Error(MAMBA2_ERR_UNSUPPORTED, where,
+                              f"unknown activation {activation!r}") from None
+        raise Mamba2Error(MAMBA2_ERR_SHAPE, where,
+                          f"parts is {parts!r}, not up to three channel counts") from None
 
 
 def _optional(t, dtype, shape, index):
@@ -326,18 +333,19 @@ def conv1d_backward(x, weight, bias, init_state, dys, dfinal=None, *, activation
     """Gradients of conv1d_forward: ``dys`` is the gradient of y, or a tuple of the
     parts' gradients.  Returns a dict with dx, dweight, dbias (None without bias)
     and dinit."""
-    dys = (dys,) if isinstance(dys, _Tensor) or not isinstance(dys, Iterable) else tuple(dys)
-    for i, d in enumerate(dys):
-        if not isinstance(d, _Tensor):
-            raise _missing("conv1d_backward", **{f"dy{i}": d})
-        if not d.dim():
-            raise Mamba2Error(MAMBA2_ERR_SHAPE, "conv1d_backward", f"dy{i} has no channels")
+    try:
+        dys = (dys,) if isinstance(dys, _Tensor) else tuple(dys)
+        widths = tuple([d.size(-1) for d in dys])
+    except (AttributeError, IndexError, TypeError):
+        dys = dys if isinstance(dys, tuple) else (dys,)
+        _tensors("conv1d_backward", **{f"dy{i}": d for i, d in enumerate(dys)})
+        raise Mamba2Error(MAMBA2_ERR_SHAPE, "conv1d_backward", "a dy has no channels") from None
     dims, ref, state, shapes, wshape, bshape, need = _conv_plan_of(
-        "conv1d_backward", x, weight, tuple(d.shape[-1] for d in dys), activation)
+        "conv1d_backward", x, weight, widths, activation)
     with _owner(stream, x):
         workspace, n = _workspace("conv1d_backward", need, workspace, x)
-        g = {"dx": x.new_empty(x.shape), "dweight": torch.empty_like(weight),
-             "dbias": _like(bias), "dinit": x.new_empty(state)}
+        g = {"dx": x.new_empty(x.shape), "dweight": _like(weight), "dbias": _like(bias),
+             "dinit": x.new_empty(state)}
     dy3 = dys + (None,) * (3 - len(dys))
     i = x.get_device()
     if (i >= 0 and n >= need > 0 and _plain(weight, _F32, wshape, i)
@@ -487,13 +495,14 @@ def _scan_plan(where, shape, ashape, bshape, bstrides, cshape, cstrides, zstride
 
 
 def _scan_plan_of(where, u, A, B, C, z, softplus, step=False):
-    if not (isinstance(u, _Tensor) and isinstance(A, _Tensor) and isinstance(B, _Tensor)
-            and isinstance(C, _Tensor)):
-        raise _missing(where, u=u, A=A, B=B, C=C)
-    if z is not None and not isinstance(z, _Tensor):
-        raise _missing(where, z=z)
-    return _scan_plan(where, u.shape, A.shape, B.shape, B.stride(), C.shape, C.stride(),
-                      None if z is None else z.stride(), u.dtype, bool(softplus), step)
+    try:
+        return _scan_plan(where, u.shape, A.shape, B.shape, B.stride(), C.shape, C.stride(),
+                          None if z is None else z.stride(), u.dtype, bool(softplus), step)
+    except (AttributeError, TypeError, Mamba2Error):
+        _tensors(where, u=u, A=A, B=B, C=C)
+        if z is not None:
+            _tensors(where, z=z)
+        raise
 
 
 def _scan_plain(i, u, dt, A, B, C, D, z, dt_bias, ashape, cshape, bcshape):
@@ -541,7 +550,7 @@ def selective_scan_backward(u, dt, A, B, C, D, z, dt_bias, init_state, dy, dfina
     with _owner(stream, u):
         workspace, n = _workspace("selective_scan_backward", need, workspace, u)
         du, ddt = u.new_empty(u.shape), u.new_empty(u.shape)
-        dA, dB, dC = torch.empty_like(A), u.new_empty(B.shape), u.new_empty(C.shape)
+        dA, dB, dC = _like(A), u.new_empty(B.shape), u.new_empty(C.shape)
         dD = _like(D)
         dz = None if z is None else u.new_empty(u.shape)
         dbias = _like(dt_bias)
@@ -650,15 +659,19 @@ def _norm_plan(where, shape, strides, zshape, zstrides, ngroups, kind, eps, dtyp
     return (dims, ctypes.byref(dims), shape[-1:], mamba2_norm_backward_workspace_bytes(dims))
 
 
-def _norm_plan_of(where, x, weight, z, ngroups, kind, eps):
-    if not (isinstance(x, _Tensor) and isinstance(weight, _Tensor)):
-        raise _missing(where, x=x, weight=weight)
-    if z is not None and not isinstance(z, _Tensor):
-        raise _missing(where, z=z)
-    if not _known(kind, _KINDS):
-        raise Mamba2Error(MAMBA2_ERR_UNSUPPORTED, where, f"unknown norm {kind!r}")
-    return _norm_plan(where, x.shape, x.stride(), None if z is None else z.shape,
-                      None if z is None else z.stride(), ngroups, kind, float(eps), x.dtype)
+def _norm_plan_of(where, x, z, ngroups, kind, eps):
+    try:
+        return _norm_plan(where, x.shape, x.stride(), None if z is None else z.shape,
+                          None if z is None else z.stride(), ngroups, kind, float(eps), x.dtype)
+    except (AttributeError, TypeError, Mamba2Error) as e:
+        _tensors(where, x=x)
+        if z is not None:
+            _tensors(where, z=z)
+        if isinstance(e, Mamba2Error):
+            raise
+        if not _known(kind, _KINDS):
+            raise Mamba2Error(MAMBA2_ERR_UNSUPPORTED, where, f"unknown norm {kind!r}") from None
+        raise
 
 
 def _rows(t, dims):
@@ -668,7 +681,7 @@ def _rows(t, dims):
 def norm_forward(x, weight, bias=None, z=None, *, ngroups=1, kind="rms", eps=1e-5, stream=None):
     """RMS norm (kind="rms") or layer norm ("layer") of x, or of x * silu(z), over
     ``ngroups`` groups of the last axis; weight and bias [D] float32.  Returns y."""
-    dims, ref, wshape, _ = _norm_plan_of("norm_forward", x, weight, z, ngroups, kind, eps)
+    dims, ref, wshape, _ = _norm_plan_of("norm_forward", x, z, ngroups, kind, eps)
     with _owner(stream, x):
         y = x.new_empty(x.shape)
     i = x.get_device()
@@ -686,19 +699,18 @@ def norm_backward(x, weight, bias, z, dy, *, ngroups=1, kind="rms", eps=1e-5, wo
                   stream=None):
     """Gradients of norm_forward: a dict with dx, dweight, dbias (None without bias)
     and dz (None without z)."""
-    dims, ref, wshape, need = _norm_plan_of("norm_backward", x, weight, z, ngroups, kind, eps)
+    dims, ref, wshape, need = _norm_plan_of("norm_backward", x, z, ngroups, kind, eps)
     if not isinstance(dy, _Tensor):
-        raise _missing("norm_backward", dy=dy)
-    if bias is not None and not isinstance(bias, _Tensor):
-        raise _missing("norm_backward", bias=bias)
+        _tensors("norm_backward", dy=dy)
+    if not (bias is None or isinstance(bias, _Tensor)):
+        _tensors("norm_backward", bias=bias)
     if dy.shape != x.shape or not dy.is_contiguous():
         raise Mamba2Error(MAMBA2_ERR_SHAPE, "norm_backward",
                           f"dy {tuple(dy.shape)} must be contiguous and of x's shape "
                           f"{tuple(x.shape)}")
     with _owner(stream, x):
         workspace, n = _workspace("norm_backward", need, workspace, x)
-        g = {"dx": x.new_empty(x.shape), "dweight": torch.empty_like(weight),
-             "dbias": _like(bias),
+        g = {"dx": x.new_empty(x.shape), "dweight": _like(weight), "dbias": _like(bias),
              "dz": None if z is None else x.new_empty(x.shape)}
     i = x.get_device()
     if (i >= 0 and n >= need > 0 and _plain(weight, _F32, wshape, i)
