@@ -19,7 +19,7 @@
 //      backward over them.
 //   3. scan_bwd_main: per chunk the states at the start of each tile of
 //      tokens (kept in LDS), then the tiles in reverse, each with its states
-//      and decays in registers.
+//      and decays in registers.  Tiles behind a sequence's end get zeros.
 //   4. scan_bwd_sums: the sums over channel tiles (dB, dC) and over chunks
 //      (dA, dD, ddt_bias).
 //

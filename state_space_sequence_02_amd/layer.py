@@ -5,7 +5,8 @@ names and arguments and check every tensor against ``dims`` first; the short
 names (``conv1d_forward`` ...) make the dims, allocate outputs and workspace
 with torch and call them.  Where ``dims`` has a stride, the tensor may be a
 column range of a wider one (the last axis without gaps, equal steps between
-tokens); every other tensor is contiguous.
+tokens); every other tensor is contiguous.  A tensor broadcast over tokens or
+sequences (``expand``) is refused: its rows have to be there (``contiguous``).
 
 Calls run on the device of their tensors, whichever is current, on that
 device's current stream unless ``stream`` is given (a ``torch.cuda.Stream`` or
