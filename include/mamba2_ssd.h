@@ -530,6 +530,163 @@ int mamba2_norm_backward(const mamba2_norm_dims* dims, const void* x, const void
                          const float* weight, const void* dy, void* dx, void* dz, float* dweight,
                          float* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The operators of an attention layer
+ * -----------------------------------
+ * What a layer of softmax attention between SSD layers computes: positions
+ * (rotary), attention over prompts with its gradients (attention) and one
+ * token of every sequence against a cache (attention_step).  The conventions
+ * above hold, those of the operators around the SSD included (strides of
+ * tokens, outputs that overlap no input unless it is said here, fixed order
+ * of sums).  H query heads read G groups of keys and values: head h reads
+ * group h / (H/G).  The values of a sequence's own tokens are finite.
+ */
+typedef enum { MAMBA2_ROTARY_HALF = 0, MAMBA2_ROTARY_INTERLEAVED = 1 } mamba2_rotary_layout;
+
+typedef struct {
+  int64_t batch;     /* B >= 1; B * L <= 2^28 */
+  int64_t seqlen;    /* L >= 1 */
+  int64_t nheads;    /* H: 1 .. 1024 */
+  int64_t ngroups;   /* G: 0 .. 1024; 0: no k */
+  int64_t headdim;   /* D <= 1024 */
+  int64_t rotary;    /* R: the first R elements of a head are turned; even, 2 .. D */
+  int64_t q_stride;  /* elements between tokens of q; 0: H * D */
+  int64_t k_stride;  /* the same of k; 0: G * D */
+  int64_t yq_stride; /* of yq */
+  int64_t yk_stride; /* of yk */
+  float scale;       /* > 0: factor of the turned elements */
+  int32_t layout;    /* mamba2_rotary_layout */
+  int32_t dtype;     /* mamba2_dtype */
+  int32_t reserved;  /* must be 0 */
+} mamba2_rotary_dims;
+
+/*
+ * rotary: pair i (0 .. R/2 - 1) of every head of token t, turned by the angle
+ * a = position(t) * inv_freq[i]:
+ *     (x1, x2) -> scale * (x1 cos a - x2 sin a, x1 sin a + x2 cos a)
+ * The pair is elements (i, i + R/2) (MAMBA2_ROTARY_HALF) or (2i, 2i + 1)
+ * (MAMBA2_ROTARY_INTERLEAVED); elements R .. D - 1 are copied as they are.
+ *     q, yq     [B, L, H, D] rows of q_stride and yq_stride
+ *     k, yk     [B, L, G, D] rows of k_stride and yk_stride (G = 0: not used)
+ *     inv_freq  [R/2] float32
+ *     positions [B, L] int32, or NULL: token t of a sequence is at t
+ * q, k, yq, yk have the type of dims.  Angles are exact to float32 at any
+ * position (formed in float64).  yq may be q and yk may be k, with equal
+ * strides.  Packed sequences are one batch with their positions.
+ * rotary_backward: the gradients dq, dk from those of yq, yk (the same turn
+ * the other way; the strides are those of dyq, dyk and dq, dk).
+ */
+int mamba2_rotary_forward(const mamba2_rotary_dims* dims, const void* q, const void* k,
+                          const float* inv_freq, const int32_t* positions, void* yq, void* yk,
+                          void* stream);
+
+int mamba2_rotary_backward(const mamba2_rotary_dims* dims, const void* dyq, const void* dyk,
+                           const float* inv_freq, const int32_t* positions, void* dq, void* dk,
+                           void* stream);
+
+typedef struct {
+  int64_t batch;    /* B: 1 .. 65535 sequences */
+  int64_t q_len;    /* rows of q for each sequence (padded), or for all together (packed); >= 1 */
+  int64_t k_len;    /* the same of k and v */
+  int64_t nheads;   /* H: 1 .. 1024 */
+  int64_t ngroups;  /* G, divides H */
+  int64_t headdim;  /* D: a multiple of 8, at most 128 */
+  int64_t q_stride; /* elements between tokens of q; 0: H * D */
+  int64_t k_stride; /* the same of k and of v; 0: G * D */
+  int64_t v_stride;
+  int64_t dq_stride; /* of dq, dk, dv (backward) */
+  int64_t dk_stride;
+  int64_t dv_stride;
+  float scale;      /* > 0 */
+  int32_t causal;   /* 0 or 1 */
+  int32_t q_packed; /* 0 or 1: how the sequences lie in q */
+  int32_t k_packed; /* the same of k and v */
+  int32_t dtype;    /* mamba2_dtype */
+  int32_t reserved; /* must be 0 */
+} mamba2_attention_dims;
+
+/*
+ * attention: softmax attention of B sequences.  Query i of a sequence with nq
+ * queries and nk keys sees the keys j < nk, with causal only j <= i + nk - nq
+ * (the last query sees all: a prompt's piece on top of earlier keys).  Per
+ * head, with s_j = scale * q_i . k_j over the keys that it sees,
+ *     o_i = sum_j exp(s_j - lse_i) v_j,    lse_i = log sum_j exp(s_j)
+ * A query that sees no key has o = 0 and lse = -infinity.
+ *     q, o  [B, q_len, H, D]  (packed: [q_len, H, D]); q rows of q_stride
+ *     k, v  [B, k_len, G, D]  (packed: [k_len, G, D]); rows of k_stride, v_stride
+ *     lse   [B, q_len, H] float32 (packed: [q_len, H])
+ *     q_seqs, k_seqs  int32.  Padded: [B] lengths (nq, nk), or NULL (all full);
+ *           values outside 0 .. len are taken as the nearer bound.  Packed:
+ *           [B + 1] starts, not decreasing, taken the same way: sequence b is
+ *           rows starts[b] .. starts[b + 1] - 1.
+ * q, k, v and o have the type of dims.  What stands behind a sequence's
+ * tokens, or in packed rows of no sequence, is not used (it may hold
+ * anything); o there is 0, lse -infinity and gradients are zeros.
+ * Strides are multiples of 16 bytes.  Statistics and sums are float32; with
+ * bfloat16 the weights are rounded to it before the product with v.
+ * Supported: rows of q and of k <= 2^28; rows of q * H / G < 2^31 - 256;
+ * workgroups (G times the tiles of 128 rows of q * H / G, or of k; packed: and
+ * B + 2) < 2^24.
+ * Workspace at least mamba2_attention_workspace_bytes(dims) (0: dims
+ * invalid), 256-byte aligned.
+ */
+size_t mamba2_attention_workspace_bytes(const mamba2_attention_dims* dims);
+
+int mamba2_attention_forward(const mamba2_attention_dims* dims, const void* q, const void* k,
+                             const void* v, const int32_t* q_seqs, const int32_t* k_seqs, void* o,
+                             float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of attention from dout, the gradient of o (lse has none): dq, dk,
+ * dv as q, k, v with rows of dq_stride, dk_stride, dv_stride.  o and lse are
+ * what the forward wrote for the same inputs; o and dout are without gaps.
+ * dk and dv are sums over the heads of a group.  Workspace at least
+ * mamba2_attention_backward_workspace_bytes(dims), 256-byte aligned.
+ */
+size_t mamba2_attention_backward_workspace_bytes(const mamba2_attention_dims* dims);
+
+int mamba2_attention_backward(const mamba2_attention_dims* dims, const void* q, const void* k,
+                              const void* v, const int32_t* q_seqs, const int32_t* k_seqs,
+                              const void* o, const float* lse, const void* dout, void* dq,
+                              void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+typedef struct {
+  int64_t batch;    /* B: 1 .. 65535 */
+  int64_t rows;     /* rows of a sequence's cache, 1 .. 2^28 */
+  int64_t prefix;   /* rows of the shared prefix, 0 .. 2^28; 0: none */
+  int64_t nheads;   /* H, G, D as for attention */
+  int64_t ngroups;
+  int64_t headdim;
+  int64_t q_stride; /* elements between sequences of q; 0: H * D */
+  int64_t k_stride; /* the same of k and of v; 0: G * D */
+  int64_t v_stride;
+  float scale;      /* > 0 */
+  int32_t dtype;    /* mamba2_dtype */
+} mamba2_attention_step_dims;
+
+/*
+ * One token of every sequence.  Sequence b has n = lengths[b] tokens in its
+ * cache (values outside 0 .. rows are taken as the nearer bound); the token
+ * sees the prefix, those n and itself, and its key and value are written to
+ * row n of the cache.  A cache with n = rows stays as it is (the token is
+ * seen all the same).  lengths is not changed: it belongs to all layers.
+ *     q, o  [B, H, D], k, v [B, G, D]; q, k, v rows of their strides
+ *     k_cache, v_cache    [B, rows, G, D]; rows behind n are not read
+ *     k_prefix, v_prefix  [prefix, G, D]: the first tokens of every sequence
+ *     lengths             [B] int32
+ * Types and strides as for attention.  Workspace at least
+ * mamba2_attention_step_workspace_bytes(dims) (0: dims invalid), 256-byte
+ * aligned.  Bound by HBM on the caches; the prefix is read once for all.
+ * Supported: B * G * ceil(H / G / 32) < 2^24.
+ */
+size_t mamba2_attention_step_workspace_bytes(const mamba2_attention_step_dims* dims);
+
+int mamba2_attention_step(const mamba2_attention_step_dims* dims, const void* q, const void* k,
+                          const void* v, void* k_cache, void* v_cache, const int32_t* lengths,
+                          const void* k_prefix, const void* v_prefix, void* o, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* mamba2_status_string(int status);
 

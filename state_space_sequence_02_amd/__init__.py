@@ -11,7 +11,8 @@ current torch stream into a ``hipStream_t``.  The functions keep the C names:
     mamba2_last_error
 
 and, in ``layer.py``, the operators around the SSD (``conv1d_*``,
-``selective_scan_*``, ``norm_*`` and their ``mamba2_*`` forms);
+``selective_scan_*``, ``norm_*`` and their ``mamba2_*`` forms), and, in
+``attention.py``, those of an attention layer (``rotary_*``, ``attention_*``);
 
 plus ``make_dims`` and ``ssd_forward`` (allocates outputs and workspace with
 torch, then calls ``mamba2_ssd_forward``).  Importing fails loudly when the
@@ -59,6 +60,9 @@ EXPORTS = (
     "mamba2_selective_scan_forward", "mamba2_selective_scan_backward_workspace_bytes",
     "mamba2_selective_scan_backward", "mamba2_selective_scan_step", "mamba2_norm_forward",
     "mamba2_norm_backward_workspace_bytes", "mamba2_norm_backward",
+    "mamba2_rotary_forward", "mamba2_rotary_backward", "mamba2_attention_workspace_bytes",
+    "mamba2_attention_forward", "mamba2_attention_backward_workspace_bytes",
+    "mamba2_attention_backward", "mamba2_attention_step_workspace_bytes", "mamba2_attention_step",
 )
 
 # bytes of the static per-GPU scratch behind mamba2_ssd_forward_noalloc
@@ -106,6 +110,37 @@ class Mamba2NormDims(_Dims):
         ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64),
         ("eps", ctypes.c_float), ("kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class Mamba2RotaryDims(_Dims):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
+        ("ngroups", ctypes.c_int64), ("headdim", ctypes.c_int64), ("rotary", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("yq_stride", ctypes.c_int64),
+        ("yk_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("layout", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class Mamba2AttentionDims(_Dims):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("q_len", ctypes.c_int64), ("k_len", ctypes.c_int64),
+        ("nheads", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("headdim", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("dq_stride", ctypes.c_int64), ("dk_stride", ctypes.c_int64),
+        ("dv_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
+        ("q_packed", ctypes.c_int32), ("k_packed", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class Mamba2AttentionStepDims(_Dims):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("prefix", ctypes.c_int64),
+        ("nheads", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("headdim", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
     ]
 
 
@@ -161,6 +196,18 @@ def _load():
         "mamba2_norm_forward": ([NM] + [P] * 6, ctypes.c_int),
         "mamba2_norm_backward_workspace_bytes": ([NM], Z),
         "mamba2_norm_backward": ([NM] + [P] * 9 + [Z, P], ctypes.c_int),
+    }
+    RO, AT, AS = (ctypes.POINTER(Mamba2RotaryDims), ctypes.POINTER(Mamba2AttentionDims),
+                  ctypes.POINTER(Mamba2AttentionStepDims))
+    sig |= {
+        "mamba2_rotary_forward": ([RO] + [P] * 7, ctypes.c_int),
+        "mamba2_rotary_backward": ([RO] + [P] * 7, ctypes.c_int),
+        "mamba2_attention_workspace_bytes": ([AT], Z),
+        "mamba2_attention_forward": ([AT] + [P] * 8 + [Z, P], ctypes.c_int),
+        "mamba2_attention_backward_workspace_bytes": ([AT], Z),
+        "mamba2_attention_backward": ([AT] + [P] * 12 + [Z, P], ctypes.c_int),
+        "mamba2_attention_step_workspace_bytes": ([AS], Z),
+        "mamba2_attention_step": ([AS] + [P] * 10 + [Z, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -562,3 +609,9 @@ from .layer import (  # noqa: E402
     mamba2_selective_scan_backward_workspace_bytes, mamba2_selective_scan_forward,
     mamba2_selective_scan_step, mamba2_selective_scan_workspace_bytes, norm_backward, norm_forward,
     selective_scan_backward, selective_scan_forward, selective_scan_step)
+from .attention import (  # noqa: E402
+    attention_backward, attention_forward, attention_step, make_attention_dims,
+    make_attention_step_dims, make_rotary_dims, mamba2_attention_backward,
+    mamba2_attention_backward_workspace_bytes, mamba2_attention_forward, mamba2_attention_step,
+    mamba2_attention_step_workspace_bytes, mamba2_attention_workspace_bytes, mamba2_rotary_backward,
+    mamba2_rotary_forward, rotary_backward, rotary_forward, rotary_frequencies)

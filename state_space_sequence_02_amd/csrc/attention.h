@@ -1,0 +1,294 @@
+// What the attention kernels share: sequences and tiles of packed rows, the
+// tiles in LDS, and the matrix products on fragments.
+//
+// Packed rows.  Head h reads the keys and values of group g = h / rep
+// (rep = H/G).  The rep rows that one token has for a group are rows of the
+// same product, so the kernels see, per (sequence, group), n * rep packed
+// rows: row r is head g rep + r % rep of token r / rep.  Keys are then read
+// once for the heads that share them, and their gradients are sums over the
+// packed rows like any other.
+//
+// Fragments (gfx950, 32x32 products, checked on the device).  Lane l has
+// x = l & 31 and half hh = l >> 5.  An accumulator holds column x, rows
+// 8 (r / 4) + 4 hh + r % 4 for r = 0 .. 15.
+//   Along the head: a fragment is what one lane gives to a product over 16
+//   (bfloat16) or 8 (float32) elements of a row of 32 rows: 16 bytes of row x
+//   at 16-byte chunk 2 s + hh.  Which elements meet in which instruction does
+//   not matter as long as both operands agree.
+//   Along the rows: 8 accumulator registers (8 s .. 8 s + 7) of a lane are the
+//   elements of its column at 8 of 16 rows; taken as the operand of a product
+//   over those rows, the other operand has to hold the same rows: 16 s + 4 hh
+//   + j and 16 s + 8 + 4 hh + j, j = 0 .. 3.  For bfloat16 that is what two
+//   transposing reads return, so the weights never change lanes.
+#pragma once
+
+#include "common.h"
+#include "launch.h"
+#include "rowvec.h"
+
+namespace m2 {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// ------------------------------------------------------------------ sequences
+
+// One side (queries, or keys and values) of a call.
+struct Side {
+  const int32_t* seqs;  // lengths [B] or NULL (padded); starts [B + 1] (packed)
+  int64_t len;          // rows of a sequence (padded), of all together (packed)
+  int64_t B;
+  bool packed;
+};
+
+struct Seq {
+  int64_t row0;  // its first row in the tensor
+  int64_t span;  // rows of the tensor that are its own, padding among them
+  int64_t n;     // tokens
+};
+
+__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t hi) {
+  return v < 0 ? 0 : v > hi ? hi : v;
+}
+
+__device__ __forceinline__ Seq seq_of(const Side& s, int64_t b) {
+  Seq q;
+  if (!s.packed) {
+    q.row0 = b * s.len;
+    q.span = s.len;
+    q.n = s.seqs ? clamp64(s.seqs[b], s.len) : s.len;
+  } else {
+    q.row0 = clamp64(s.seqs[b], s.len);
+    q.n = clamp64(s.seqs[b + 1], s.len) - q.row0;
+    if (q.n < 0) q.n = 0;
+    q.span = q.n;
+  }
+  return q;
+}
+
+// A tile of `tile` packed rows.  Padded: tile-major over the sequences.
+// Packed: between and behind the sequences there are rows that belong to
+// none, so the tensor is cut at 0, starts[0 .. B], len: B + 2 pieces of which
+// the first and the last hold no tokens.  Piece i takes the slots from
+// floor(cut_i rep / tile) + i on: the next piece's first slot is at least as
+// far as its rows need, whatever the lengths, so the number of slots follows
+// from the sizes alone (no list is made, nothing is copied to the host).
+struct Tile {
+  Seq seq;
+  int64_t b;   // sequence; -1: rows of none
+  int64_t r0;  // first packed row
+};
+
+inline int64_t tile_slots(const Side& s, int64_t rep, int64_t tile) {
+  return s.packed ? s.len * rep / tile + s.B + 2 : s.B * ((s.len * rep + tile - 1) / tile);
+}
+
+__device__ __forceinline__ int64_t cut_of(const Side& s, int64_t i) {
+  return i == 0 ? 0 : i > s.B + 1 ? s.len : clamp64(s.seqs[i - 1], s.len);
+}
+
+// The tile of a slot, the same for all lanes.  A wavefront's lanes look at 64
+// pieces at once.
+__device__ __forceinline__ Tile tile_of(const Side& s, int64_t rep, int64_t tile, int64_t slot) {
+  Tile t;
+  if (!s.packed) {
+    const int64_t i = slot / s.B;
+    t.b = slot - i * s.B;
+    t.r0 = i * tile;
+    t.seq = seq_of(s, t.b);
+    return t;
+  }
+  int64_t lo = 0, count = s.B + 2;
+  while (count > 1) {
+    const int64_t step = (count + 63) / 64;
+    const int64_t i = lo + lane_id() * step;
+    const bool at = i < lo + count && cut_of(s, i) * rep / tile + i <= slot;
+    const uint64_t mask = __ballot(at);
+    const int last = mask ? 63 - __builtin_clzll(mask) : 0;
+    const int64_t left = count - last * step;
+    lo += last * step;
+    count = left < step ? left : step;
+  }
+  const int64_t i = __builtin_amdgcn_readfirstlane((int)lo);
+  const int64_t cut = cut_of(s, i);
+  t.r0 = (slot - (cut * rep / tile + i)) * tile;
+  t.b = i - 1;
+  t.seq.row0 = cut;
+  t.seq.span = cut_of(s, i + 1) - cut;
+  if (t.seq.span < 0) t.seq.span = 0;
+  t.seq.n = t.seq.span;
+  if (i == 0 || i == s.B + 1) {
+    t.b = -1;
+    t.seq.n = 0;
+  }
+  return t;
+}
+
+// ------------------------------------------------------------------ LDS tiles
+
+// A tile's rows hold DP elements (64 or 128, the head's size rounded up) in
+// 16-byte chunks; chunk c of row r stands at position c ^ swz(r).  Row reads
+// (16 rows, one chunk) then meet every bank once, and so do transposing reads
+// (4 rows, 4 chunks of each).
+template <typename T, int DP>
+struct TileCfg {
+  static constexpr int E = 16 / (int)sizeof(T);     // elements of a chunk
+  static constexpr int CH = DP / E;                 // chunks of a row: 8, 16 or 32
+  static constexpr int ROWB = DP * (int)sizeof(T);  // bytes of a row
+  static constexpr int STEPS = CH / 2;              // products along a row
+};
+
+template <int CH>
+__device__ __forceinline__ int swz(int r) {
+  if constexpr (CH == 8)
+    return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
+  else
+    return (r & 3) << 2 | ((r >> 2) & 3);
+}
+
+template <int CH>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return (uint32_t)(r * CH + (c ^ swz<CH>(r))) * 16;
+}
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// A lane's part of a fragment along the head: 16 bytes.
+template <typename T>
+using head_frag = raw_t<T, 16 / (int)sizeof(T)>;
+
+// c += A B over one step along the head.
+__device__ __forceinline__ f32x16 mma_head(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma_head(f32x4 a, f32x4 b, f32x16 c) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+  return c;
+}
+
+// Operand of a product over 16 rows: 8 values of a lane.
+struct f32v8 {
+  float v[8];
+};
+template <typename T>
+struct RowFrag;
+template <>
+struct RowFrag<bf16> {
+  typedef bf16x8 type;
+};
+template <>
+struct RowFrag<float> {
+  typedef f32v8 type;
+};
+template <typename T>
+using row_frag = typename RowFrag<T>::type;
+
+typedef float at_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 at_bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ at_bf16x2 pack2(float a, float b) {
+  return __builtin_convertvector((at_f32x2){a, b}, at_bf16x2);
+}
+__device__ __forceinline__ bf16x4 pack4(float a, float b, float c, float d) {
+  return __builtin_shufflevector(pack2(a, b), pack2(c, d), 0, 1, 2, 3);
+}
+
+// Registers 8 s .. 8 s + 7 of an accumulator as such an operand.  bfloat16
+// products take bfloat16 weights: one rounding (at most 2^-8 relative) of each
+// weight, independent over a sum's terms.
+template <typename T>
+__device__ __forceinline__ row_frag<T> acc_frag(const f32x16& p, int s) {
+  if constexpr (sizeof(T) == 2) {
+    return cat(pack4(p[8 * s], p[8 * s + 1], p[8 * s + 2], p[8 * s + 3]),
+               pack4(p[8 * s + 4], p[8 * s + 5], p[8 * s + 6], p[8 * s + 7]));
+  } else {
+    f32v8 f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.v[j] = p[8 * s + j];
+    return f;
+  }
+}
+
+__device__ __forceinline__ f32x16 mma_rows(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma_rows(const f32v8& a, const f32v8& b, f32x16 c) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[j], b.v[j], c, 0, 0, 0);
+  return c;
+}
+
+// A lane's reads of an LDS tile.
+template <typename T, int DP>
+struct TileReader {
+  using K = TileCfg<T, DP>;
+  // Rows r32 .. r32 + 31 at step s along the head.
+  __device__ __forceinline__ static head_frag<T> head(const char* tile, int r32, int s) {
+    const int lane = lane_id();
+    return *(const head_frag<T>*)(tile + r32 * K::ROWB +
+                                  chunk_at<K::CH>(lane & 31, 2 * s + (lane >> 5)));
+  }
+  // Column 32 dt + x at rows r16 .. r16 + 15, those of acc_frag.
+  __device__ __forceinline__ static row_frag<T> cols(const char* tile, int r16, int dt) {
+    const int lane = lane_id(), hh = lane >> 5;
+    if constexpr (sizeof(T) == 2) {
+      const int i = lane & 15;
+      const int c = 4 * dt + ((lane >> 4) & 1) * 2 + ((i & 3) >> 1);
+      const int r = 4 * hh + (i >> 2);
+      const char* at = tile + r16 * K::ROWB + (i & 1) * 8;
+      return cat(lds_read_tr((const bf16*)(at + chunk_at<K::CH>(r, c))),
+                 lds_read_tr((const bf16*)(at + chunk_at<K::CH>(r + 8, c))));
+    } else {
+      f32v8 f;
+      const int c = 8 * dt + ((lane & 31) >> 2);
+      const char* at = tile + r16 * K::ROWB + (lane & 3) * 4;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = (j >> 2) * 8 + 4 * hh + (j & 3);
+        f.v[j] = *(const float*)(at + chunk_at<K::CH>(r, c));
+      }
+      return f;
+    }
+  }
+};
+
+// The larger of a lane's value and its other half's.
+__device__ __forceinline__ float max_halves(float v) {
+  const unsigned u = __builtin_bit_cast(unsigned, v);
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned x = s[0], y = s[1];
+  return __builtin_fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+
+// Fragments along the head of one row in memory, zeros behind the head's D
+// elements.
+template <typename T, int DP>
+__device__ __forceinline__ void load_row_frags(const T* row, int D,
+                                               head_frag<T> (&f)[TileCfg<T, DP>::STEPS]) {
+  using K = TileCfg<T, DP>;
+  const int hh = lane_id() >> 5;
+#pragma unroll
+  for (int s = 0; s < K::STEPS; ++s) {
+    const int e = (2 * s + hh) * K::E;
+    f[s] = head_frag<T>{};
+    if (e < D) f[s] = *(const head_frag<T>*)(row + e);
+  }
+}
+
+// Clears a tile's chunks behind the head's end; loads never touch them.
+template <typename T, int DP>
+__device__ __forceinline__ void clear_ends(char* tile, int rows, int D, int thread, int threads) {
+  using K = TileCfg<T, DP>;
+  if (D == DP) return;
+  for (int i = thread; i < rows * K::CH; i += threads) {
+    const int r = i / K::CH, c = i % K::CH;
+    if (c * K::E >= D) *(f32x4*)(tile + chunk_at<K::CH>(r, c)) = f32x4{};
+  }
+}
+
+}  // namespace m2

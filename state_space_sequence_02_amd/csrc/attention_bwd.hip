@@ -1,0 +1,403 @@
+// Backward pass of attention.  With P_ij = exp(s_ij - lse_i) and the gradient
+// dO of the output,
+//
+//     delta_i = sum_d dO_id O_id
+//     dV_j = sum_i P_ij dO_i            dP_ij = dO_i . V_j
+//     dS_ij = P_ij (dP_ij - delta_i)
+//     dQ_i = scale sum_j dS_ij K_j      dK_j = scale sum_i dS_ij Q_i
+//
+// The weights are formed again from q, k and lse.  One kernel owns rows and
+// walks the keys (dQ, 3 products), one owns keys and walks the rows (dK and
+// dV, 4 products): seven products instead of five, but every gradient is a sum
+// in one place and in a fixed order, without atomics and without float32
+// partial dQ in memory.  dK and dV of a group are sums over the packed rows of
+// all its heads.  P and dS are rounded to the inputs' type before the products
+// that take them (bfloat16: 2^-8 at most for each term of a sum).
+#include "attention_fwd.h"
+
+namespace m2 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 128;     // packed rows (dQ) or keys (dK, dV) of a workgroup
+constexpr int kKeys = 64;      // keys of a tile in the dQ kernel
+
+struct BwdArgs {
+  const void *q, *k, *v, *dout;
+  void *dq, *dk, *dv;
+  const float *lse2, *delta;  // [rows of q][H]; lse in log2 units, 0 for rows without keys
+  Side qside, kside;
+  int64_t qs, ks, vs, dqs, dks, dvs, slots;
+  int H, G, rep, D;
+  unsigned div_m;
+  int div_l;
+  bool causal;
+  float c, scale;
+};
+
+// r / rep for 0 <= r < 2^31: M = ceil(2^(31 + l) / rep), l = ceil(log2 rep).
+__device__ __forceinline__ int over_rep(const BwdArgs& a, int r) {
+  return (int)(__umulhi(2u * (unsigned)r, a.div_m) >> a.div_l);
+}
+
+// delta and lse in log2 units: 32 lanes a (token, head) row, 4 elements each.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) attention_rows_kernel(
+    const T* __restrict__ o, const T* __restrict__ dout, const float* __restrict__ lse,
+    float* __restrict__ lse2, float* __restrict__ delta, int64_t rows, int D) {
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int e = threadIdx.x % 32 * 4;
+  float sum = 0.f;
+  if (row < rows && e < D) {
+    float x[4], y[4];
+    load_row<T, 4>(o + row * D + e, x);
+    load_row<T, 4>(dout + row * D + e, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = __builtin_fmaf(x[i], y[i], sum);
+  }
+  sum = lanes_sum<32>(sum);
+  if (row < rows && e == 0) {
+    const float l = lse[row];
+    delta[row] = sum;
+    lse2[row] = l == -__builtin_inff() ? 0.f : l * kLog2e;
+  }
+}
+
+// Starts the loads of packed rows r0 .. r0 + ROWS - 1 of a group; rows behind
+// the last are the last again.
+template <typename T, int DP, int ROWS, int NT>
+__device__ __forceinline__ void stage_packed(uint32_t lds, const T* base, int64_t stride, int rows,
+                                             int r0, const BwdArgs& a, int thread) {
+  using K = TileCfg<T, DP>;
+#pragma unroll
+  for (int i = 0; i < ROWS * K::CH / NT; ++i) {
+    const int slot = i * NT + thread;
+    const int r = slot / K::CH, c = (slot % K::CH) ^ swz<K::CH>(r);
+    const int at = r0 + r < rows ? r0 + r : rows - 1;
+    const int tok = over_rep(a, at);
+    const T* p = base + tok * stride + (at - tok * a.rep) * a.D;
+    if (c * K::E < a.D) dma16(p + c * K::E, lds + (slot & ~63) * 16);
+  }
+}
+
+// 4 bytes a lane, as dma16.
+__device__ __forceinline__ void dma4(const void* src, uint32_t lds_base) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_base);
+  asm volatile("global_load_lds_dword %0, off" : : "v"(src), "{m0}"(m0) : "memory");
+}
+
+// A column's accumulators as a row of a tensor.
+template <typename T, int DP>
+__device__ __forceinline__ void store_column(T* row, const f32x16 (&acc)[DP / 32], float scale,
+                                             int D) {
+  const int hh = lane_id() >> 5;
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const int e = 32 * d + 2 * r + 4 * hh;
+      const float v[4] = {acc[d][r] * scale, acc[d][r + 1] * scale, acc[d][r + 2] * scale,
+                          acc[d][r + 3] * scale};
+      if (e < D) store_row<T, 4>(row + e, v);
+    }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq_kernel(BwdArgs a) {
+  using K = TileCfg<T, DP>;
+  using R = TileReader<T, DP>;
+  constexpr int TILE = kKeys * K::ROWB;
+  extern __shared__ __align__(16) char lds[];
+  const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
+  const int g = blockIdx.x % a.G;
+  const Tile tile = tile_of(a.qside, a.rep, kRows, a.slots - 1 - blockIdx.x / a.G);
+  const int64_t span = tile.seq.span * a.rep;
+  if (tile.r0 >= span) return;
+  const int nq = (int)tile.seq.n, rows = nq * a.rep;
+  Seq ks = {0, 0, 0};
+  if (tile.b >= 0) ks = seq_of(a.kside, tile.b);
+  const int nk = (int)ks.n;
+  const int row = (int)tile.r0 + wave * 32 + (lane & 31);
+  const int token = row / a.rep;
+  const int head = g * a.rep + row % a.rep;
+  const auto seen = [&](int tok) {
+    const int64_t n = (int64_t)tok + nk - nq + 1;
+    return a.causal ? (int)clamp64(n, nk) : nk;
+  };
+  const int lim = row < rows ? seen(token) : 0;
+  const int last = (int)(tile.r0 + kRows < rows ? tile.r0 + kRows : rows) - 1;
+  const int most = last >= tile.r0 ? seen(last / a.rep) : 0;
+  const int tiles = (most + kKeys - 1) / kKeys;
+
+  f32x16 acc[DP / 32];
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d) acc[d] = zero16();
+  if (tiles) {
+    head_frag<T> q[K::STEPS], dout[K::STEPS];
+    const int safe = row < rows ? row : rows - 1;
+    const int64_t tok = tile.seq.row0 + safe / a.rep;
+    const int hd = g * a.rep + safe % a.rep;
+    load_row_frags<T, DP>((const T*)a.q + tok * a.qs + (int64_t)hd * a.D, a.D, q);
+    load_row_frags<T, DP>((const T*)a.dout + (tok * a.H + hd) * a.D, a.D, dout);
+    const float lse2 = a.lse2[tok * a.H + hd], delta = a.delta[tok * a.H + hd];
+    const T* k = (const T*)a.k + ks.row0 * a.ks + (int64_t)g * a.D;
+    const T* v = (const T*)a.v + ks.row0 * a.vs + (int64_t)g * a.D;
+    const uint32_t base = lds_addr(lds);
+    clear_ends<T, DP>(lds, 4 * kKeys, a.D, threadIdx.x, kThreads);
+    int low = lim, high = lim;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+      low = min(low, __shfl_xor(low, m));
+      high = max(high, __shfl_xor(high, m));
+    }
+    low = __builtin_amdgcn_readfirstlane(low);
+    high = __builtin_amdgcn_readfirstlane(high);
+    const auto stage = [&](int t) {
+      const uint32_t at = base + (t & 1) * 2 * TILE;
+      stage_rows<T, DP, kKeys, kThreads>(at, k, a.ks, nk, nullptr, t * kKeys, a.D, threadIdx.x);
+      stage_rows<T, DP, kKeys, kThreads>(at + TILE, v, a.vs, nk, nullptr, t * kKeys, a.D,
+                                         threadIdx.x);
+    };
+    stage(0);
+    for (int t = 0; t < tiles; ++t) {
+      wait_vm(0);
+      lds_barrier();
+      if (t + 1 < tiles) stage(t + 1);
+      const char* kt = lds + (t & 1) * 2 * TILE;
+      const char* vt = kt + TILE;
+      const int k0 = t * kKeys;
+#pragma unroll
+      for (int u = 0; u < kKeys / 32; ++u) {
+        const int ku = k0 + 32 * u;
+        if (high <= ku) break;
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int d = 0; d < K::STEPS; ++d) s = mma_head(R::head(kt, 32 * u, d), q[d], s);
+#pragma unroll
+        for (int d = 0; d < K::STEPS; ++d) dp = mma_head(R::head(vt, 32 * u, d), dout[d], dp);
+        if (low < ku + 32) {
+          const int left = lim - ku - 4 * hh;
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (8 * (r / 4) + r % 4 >= left) s[r] = -__builtin_inff();
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[r] = fast_exp2(__builtin_fmaf(s[r], a.c, -lse2)) * (dp[r] - delta);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const row_frag<T> ds = acc_frag<T>(s, h);
+#pragma unroll
+          for (int d = 0; d < DP / 32; ++d)
+            acc[d] = mma_rows(R::cols(kt, 32 * u + 16 * h, d), ds, acc[d]);
+        }
+      }
+    }
+  }
+  if (row >= span) return;
+  store_column<T, DP>((T*)a.dq + (tile.seq.row0 + token) * a.dqs + (int64_t)head * a.D, acc,
+                      a.scale, a.D);
+}
+
+template <typename T, int DP>
+struct DkvCfg {
+  static constexpr int ROWS = sizeof(T) == 2 ? 64 : 32;  // packed rows of a tile
+  static constexpr int TILE = ROWS * TileCfg<T, DP>::ROWB;
+  static constexpr int BUF = 2 * TILE + 2 * ROWS * 4;  // Q, dO, lse2, delta
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dkv_kernel(
+    BwdArgs a) {
+  using K = TileCfg<T, DP>;
+  using R = TileReader<T, DP>;
+  using C = DkvCfg<T, DP>;
+  extern __shared__ __align__(16) char lds[];
+  const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
+  const int g = blockIdx.x % a.G;
+  const Tile tile = tile_of(a.kside, 1, kRows, blockIdx.x / a.G);
+  if (tile.r0 >= tile.seq.span) return;
+  const int nk = (int)tile.seq.n;
+  Seq qs = {0, 0, 0};
+  if (tile.b >= 0) qs = seq_of(a.qside, tile.b);
+  const int nq = (int)qs.n, rows = nq * a.rep;
+  const int k0 = (int)tile.r0, key = k0 + wave * 32 + (lane & 31);
+  // the first packed row that sees a key; all see the keys before the first token
+  const auto first_of = [&](int kk) {
+    const int64_t tok = (int64_t)kk - ((int64_t)nk - nq);
+    return !a.causal || tok < 0 ? 0 : (int)(tok < nq ? tok * a.rep : rows);
+  };
+  const int first = first_of(key < nk ? key : nk - 1);
+  const int wave_last = k0 + wave * 32 + 31;
+  const int low = first_of(k0 + wave * 32);                          // the wavefront's earliest row
+  const int high = first_of(wave_last < nk ? wave_last : nk - 1);    // all its keys are seen from here
+  const int begin = k0 < nk ? first_of(k0) / C::ROWS : 0;
+  const int tiles = k0 < nk ? (rows + C::ROWS - 1) / C::ROWS : 0;
+
+  f32x16 dk[DP / 32], dv[DP / 32];
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = zero16();
+  if (begin < tiles) {
+    head_frag<T> kf[K::STEPS], vf[K::STEPS];
+    const int64_t at = tile.seq.row0 + (key < nk ? key : nk - 1);
+    load_row_frags<T, DP>((const T*)a.k + at * a.ks + (int64_t)g * a.D, a.D, kf);
+    load_row_frags<T, DP>((const T*)a.v + at * a.vs + (int64_t)g * a.D, a.D, vf);
+    const T* q = (const T*)a.q + qs.row0 * a.qs + (int64_t)g * a.rep * a.D;
+    const T* dout = (const T*)a.dout + (qs.row0 * a.H + g * a.rep) * a.D;
+    const float* lse2 = a.lse2 + qs.row0 * a.H + g * a.rep;
+    const float* delta = a.delta + qs.row0 * a.H + g * a.rep;
+    const uint32_t base = lds_addr(lds);
+    clear_ends<T, DP>(lds, 2 * C::ROWS, a.D, threadIdx.x, kThreads);
+    clear_ends<T, DP>(lds + C::BUF, 2 * C::ROWS, a.D, threadIdx.x, kThreads);
+    const auto stage = [&](int t) {
+      const uint32_t to = base + (t & 1) * C::BUF;
+      const int r0 = t * C::ROWS;
+      stage_packed<T, DP, C::ROWS, kThreads>(to, q, a.qs, rows, r0, a, threadIdx.x);
+      stage_packed<T, DP, C::ROWS, kThreads>(to + C::TILE, dout, (int64_t)a.H * a.D, rows, r0, a,
+                                             threadIdx.x);
+      if (wave < 2 && lane < C::ROWS) {
+        const int r = r0 + lane < rows ? r0 + lane : rows - 1;
+        const int tok = over_rep(a, r);
+        const float* p = (wave ? delta : lse2) + (int64_t)tok * a.H + (r - tok * a.rep);
+        dma4(p, to + 2 * C::TILE + wave * C::ROWS * 4);
+      }
+    };
+    stage(begin);
+    for (int t = begin; t < tiles; ++t) {
+      wait_vm(0);
+      lds_barrier();
+      if (t + 1 < tiles) stage(t + 1);
+      const char* qt = lds + (t & 1) * C::BUF;
+      const char* dt = qt + C::TILE;
+      const float* st = (const float*)(dt + C::TILE);
+      const int r0 = t * C::ROWS;
+#pragma unroll
+      for (int u = 0; u < C::ROWS / 32; ++u) {
+        const int ru = r0 + 32 * u;
+        if (ru >= rows) break;
+        if (low >= ru + 32) continue;
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int d = 0; d < K::STEPS; ++d) s = mma_head(R::head(qt, 32 * u, d), kf[d], s);
+#pragma unroll
+        for (int d = 0; d < K::STEPS; ++d) dp = mma_head(R::head(dt, 32 * u, d), vf[d], dp);
+        if (high > ru || ru + 32 > rows) {
+          const int lo = first - ru - 4 * hh, hi = rows - ru - 4 * hh;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int i = 8 * (r / 4) + r % 4;
+            if (i < lo || i >= hi) s[r] = -__builtin_inff();
+          }
+        }
+        f32x16 ds;
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const f32x4 l4 = *(const f32x4*)(st + 32 * u + 2 * r + 4 * hh);
+          const f32x4 d4 = *(const f32x4*)(st + C::ROWS + 32 * u + 2 * r + 4 * hh);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[r + i] = fast_exp2(__builtin_fmaf(s[r + i], a.c, -l4[i]));
+            ds[r + i] = s[r + i] * (dp[r + i] - d4[i]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const row_frag<T> pf = acc_frag<T>(s, h), df = acc_frag<T>(ds, h);
+#pragma unroll
+          for (int d = 0; d < DP / 32; ++d) {
+            dv[d] = mma_rows(R::cols(dt, 32 * u + 16 * h, d), pf, dv[d]);
+            dk[d] = mma_rows(R::cols(qt, 32 * u + 16 * h, d), df, dk[d]);
+          }
+        }
+      }
+    }
+  }
+  if (key >= tile.seq.span) return;
+  if (key >= nk) {
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = zero16();
+  }
+  const int64_t to = tile.seq.row0 + key;
+  store_column<T, DP>((T*)a.dk + to * a.dks + (int64_t)g * a.D, dk, a.scale, a.D);
+  store_column<T, DP>((T*)a.dv + to * a.dvs + (int64_t)g * a.D, dv, 1.f, a.D);
+}
+
+template <typename F>
+hipError_t launch_lds(F kernel, int64_t blocks, int bytes, const BwdArgs& a, hipStream_t s) {
+  const hipError_t e =
+      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return e;
+  kernel<<<(unsigned)blocks, kThreads, bytes, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t go(BwdArgs a, hipStream_t s) {
+  a.slots = tile_slots(a.kside, 1, kRows);
+  hipError_t e = launch_lds(attention_dkv_kernel<T, DP>, a.slots * a.G, 2 * DkvCfg<T, DP>::BUF, a, s);
+  if (e != hipSuccess) return e;
+  a.slots = tile_slots(a.qside, a.rep, kRows);
+  return launch_lds(attention_dq_kernel<T, DP>, a.slots * a.G, 4 * kKeys * TileCfg<T, DP>::ROWB, a,
+                    s);
+}
+
+}  // namespace
+
+int64_t attention_key_blocks(const AttentionDims& d) {
+  return tile_slots({nullptr, d.Lk, d.B, d.kpacked}, 1, kRows) * d.G;
+}
+
+size_t attention_backward_bytes(const AttentionDims& d) {
+  return (size_t)d.q_rows() * d.H * 2 * sizeof(float);
+}
+
+hipError_t launch_attention_backward(const AttentionDims& d, const void* q, const void* k,
+                                     const void* v, const int32_t* q_seqs, const int32_t* k_seqs,
+                                     const void* o, const float* lse, const void* dout, void* dq,
+                                     void* dk, void* dv, void* ws, hipStream_t s) {
+  const int64_t rows = d.q_rows() * d.H;
+  float* lse2 = (float*)ws;
+  float* delta = lse2 + rows;
+  BwdArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.lse2 = lse2;
+  a.delta = delta;
+  a.qside = {q_seqs, d.Lq, d.B, d.qpacked};
+  a.kside = {k_seqs, d.Lk, d.B, d.kpacked};
+  a.qs = d.qs;
+  a.ks = d.ks;
+  a.vs = d.vs;
+  a.dqs = d.dqs;
+  a.dks = d.dks;
+  a.dvs = d.dvs;
+  a.H = (int)d.H;
+  a.G = (int)d.G;
+  a.rep = (int)(d.H / d.G);
+  a.D = (int)d.D;
+  a.div_l = 0;
+  while ((1 << a.div_l) < a.rep) ++a.div_l;
+  a.div_m = (unsigned)((((uint64_t)1 << (31 + a.div_l)) + a.rep - 1) / a.rep);
+  a.causal = d.causal;
+  a.c = d.scale * kLog2e;
+  a.scale = d.scale;
+  const unsigned blocks = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
+  if (d.bf16)
+    attention_rows_kernel<bf16><<<blocks, kThreads, 0, s>>>((const bf16*)o, (const bf16*)dout, lse,
+                                                            lse2, delta, rows, a.D);
+  else
+    attention_rows_kernel<float><<<blocks, kThreads, 0, s>>>((const float*)o, (const float*)dout,
+                                                             lse, lse2, delta, rows, a.D);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (d.bf16) return d.D <= 64 ? go<bf16, 64>(a, s) : go<bf16, 128>(a, s);
+  return d.D <= 64 ? go<float, 64>(a, s) : go<float, 128>(a, s);
+}
+
+}  // namespace m2

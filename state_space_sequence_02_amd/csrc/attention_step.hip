@@ -1,0 +1,254 @@
+// attention_step: one token of every sequence against its cache of keys and
+// values, with or without a prefix that all sequences share.  Sequence b sees
+// the prefix, rows 0 .. n - 1 of its cache (n = lengths[b]) and the token
+// itself, whose key and value go to row n of the cache (if it has one: a full
+// cache keeps what it holds, the token is still seen).  They are read from the
+// call's inputs, never from the cache, so no workgroup waits for the one that
+// writes them.
+//
+// Bound by HBM on the caches, which are read once: a workgroup takes the rep
+// rows of one (sequence, group) and a range of the keys; its wavefronts walk
+// tiles of 32 keys on their own, with the next tile on its way into LDS, and
+// join at the end.  The prefix is one product for the whole batch: batch * rep
+// packed rows against the prefix's keys (attention.hip), so it is read once
+// for all sequences and not once for each.  Ranges and prefix leave float32
+// parts that one more kernel joins; a single range without a prefix needs none.
+#include "attention_fwd.h"
+
+namespace m2 {
+
+namespace {
+
+struct StepArgs {
+  const void *q, *k, *v;
+  void *k_cache, *v_cache;
+  const int32_t* lengths;
+  void* o;
+  float *part_o, *part_lse;  // NULL: o is written
+  int64_t qs, ks, vs, rows;  // rows of a cache
+  int B, H, G, rep, D, tiles;  // tiles of 32 packed rows
+  float c;
+};
+
+// Wavefronts of a workgroup: as many as two tiles of K and V for each fit LDS.
+template <typename T, int DP>
+constexpr int waves_of() { return sizeof(T) * DP > 256 ? 2 : 4; }
+
+template <typename T, int DP>
+__global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_kernel(StepArgs a) {
+  using K = TileCfg<T, DP>;
+  constexpr int W = waves_of<T, DP>();
+  constexpr int TILE = 32 * K::ROWB;
+  constexpr int LOADS = 2 * 32 * K::CH / 64;  // of a wavefront for a tile of K and V
+  extern __shared__ __align__(16) char lds[];  // [W][2][K tile, V tile]
+  const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
+  const int g = blockIdx.x % a.G, rest = blockIdx.x / a.G;
+  const int b = rest / a.tiles, r0 = rest % a.tiles * 32;
+  const int64_t cap = a.rows;
+  const int n = (int)clamp64(a.lengths[b], cap);
+  const int64_t cs = (int64_t)a.G * a.D;
+  const int64_t cache = (int64_t)b * cap * cs + (int64_t)g * a.D;
+  const T* kn = (const T*)a.k + b * a.ks + (int64_t)g * a.D;
+  const T* vn = (const T*)a.v + b * a.vs + (int64_t)g * a.D;
+  T* kc = (T*)a.k_cache + cache;
+  T* vc = (T*)a.v_cache + cache;
+  if (blockIdx.y == 0 && r0 == 0 && n < cap) {
+    for (int i = threadIdx.x * 4; i < a.D; i += 64 * W * 4) {
+      *(raw_t<T, 4>*)(kc + n * cs + i) = *(const raw_t<T, 4>*)(kn + i);
+      *(raw_t<T, 4>*)(vc + n * cs + i) = *(const raw_t<T, 4>*)(vn + i);
+    }
+  }
+
+  const int row = r0 + (lane & 31);
+  const int head = g * a.rep + (row < a.rep ? row : a.rep - 1);
+  const int nk = n + 1;
+  const int tiles = (nk + 31) / 32;
+  const int per = (tiles + gridDim.y - 1) / gridDim.y;
+  const int t0 = blockIdx.y * per, t1 = t0 + per < tiles ? t0 + per : tiles;
+  char* mine = lds + wave * 4 * TILE;
+  const uint32_t base = lds_addr(mine);
+  RowState<T, DP> st;
+  st.clear();
+  if (t0 + wave < t1) {
+    head_frag<T> q[K::STEPS];
+    load_row_frags<T, DP>((const T*)a.q + b * a.qs + (int64_t)head * a.D, a.D, q);
+    clear_ends<T, DP>(mine, 4 * 32, a.D, lane, 64);
+    const auto stage = [&](int t, int buf) {
+      const uint32_t to = base + buf * 2 * TILE;
+      stage_rows<T, DP, 32, 64>(to, kc, cs, nk, kn, t * 32, a.D, lane);
+      stage_rows<T, DP, 32, 64>(to + TILE, vc, cs, nk, vn, t * 32, a.D, lane);
+    };
+    wait_vm(0);
+    stage(t0 + wave, 0);
+    int buf = 0;
+    for (int t = t0 + wave; t < t1; t += W, buf ^= 1) {
+      // the other buffer's reads are done: their results were used
+      if (t + W < t1) {
+        stage(t + W, buf ^ 1);
+        wait_vm(LOADS);
+      } else {
+        wait_vm(0);
+      }
+      asm volatile("" ::: "memory");
+      const char* kt = mine + buf * 2 * TILE;
+      if (t * 32 + 32 <= nk)
+        st.template step<1, false>(q, kt, kt + TILE, 32, a.c);
+      else
+        st.template step<1, true>(q, kt, kt + TILE, nk - t * 32, a.c);
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      asm volatile("" ::: "memory");
+    }
+  }
+
+  // Join the wavefronts: each scales its sums to the common maximum.
+  __syncthreads();
+  float* tops = (float*)lds;            // [W][32]
+  float* sums = tops + W * 32;          // [W][32]
+  float* outs = sums + W * 32;          // [W][32][DP + 4]
+  constexpr int LD = DP + 4;
+  const int x = lane & 31;
+  const float l = st.l + __shfl_xor(st.l, 32);
+  if (hh == 0) {
+    tops[wave * 32 + x] = st.m;
+    sums[wave * 32 + x] = l;
+  }
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const float v[4] = {st.o[d][r], st.o[d][r + 1], st.o[d][r + 2], st.o[d][r + 3]};
+      store_row<float, 4>(outs + (wave * 32 + x) * LD + 32 * d + 2 * r + 4 * hh, v);
+    }
+  __syncthreads();
+  const int left = a.rep - r0 < 32 ? a.rep - r0 : 32;
+  const int quads = a.D / 4;
+  for (int i = threadIdx.x; i < left * quads; i += 64 * W) {
+    const int rr = i / quads, e = i % quads * 4;
+    float top = tops[rr];
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = __builtin_fmaxf(top, tops[w * 32 + rr]);
+    const float ref = top == -__builtin_inff() ? 0.f : top;
+    float sum = 0.f;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = fast_exp2((tops[w * 32 + rr] - ref) * a.c);
+      sum += f * sums[w * 32 + rr];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += f * outs[(w * 32 + rr) * LD + e + j];
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= inv;
+    const int64_t at = (int64_t)b * a.H + g * a.rep + r0 + rr;
+    if (a.part_o) {
+      const int64_t p = (int64_t)blockIdx.y * a.B * a.H + at;
+      store_row<float, 4>(a.part_o + p * a.D + e, v);
+      if (e == 0)
+        a.part_lse[p] = sum > 0.f ? top * a.c + __builtin_amdgcn_logf(sum) : -__builtin_inff();
+    } else {
+      store_row<T, 4>((T*)a.o + at * a.D + e, v);
+    }
+  }
+}
+
+template <typename T, int DP>
+hipError_t go(const StepArgs& a, int splits, hipStream_t s) {
+  constexpr int W = waves_of<T, DP>();
+  constexpr int bytes = W * 4 * 32 * TileCfg<T, DP>::ROWB;
+  static_assert(bytes >= (W * 64 + W * 32 * (DP + 4)) * 4, "the join's floats fit the tiles' place");
+  const auto kernel = attention_step_kernel<T, DP>;
+  const hipError_t e =
+      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return e;
+  kernel<<<dim3((unsigned)((int64_t)a.B * a.tiles * a.G), splits), 64 * W, bytes, s>>>(a);
+  return hipGetLastError();
+}
+
+int64_t row_tiles(const AttentionStepDims& d) { return (d.H / d.G + 31) / 32; }
+
+// Ranges of the cache: enough workgroups for the device, at least two tiles
+// for each wavefront of them where the cache is full.
+int splits_of(const AttentionStepDims& d) {
+  const int64_t blocks = attention_step_blocks(d);
+  const int64_t most = (d.rows + 255) / 256;
+  int64_t n = 512 / blocks;
+  if (n > most) n = most;
+  if (n > 64) n = 64;
+  return n < 2 ? 1 : (int)n;
+}
+
+AttentionDims prefix_dims(const AttentionStepDims& d) {
+  AttentionDims p = {};
+  p.B = 1;
+  p.Lq = d.B;
+  p.Lk = d.prefix;
+  p.H = d.H;
+  p.G = d.G;
+  p.D = d.D;
+  p.qs = d.qs;
+  p.ks = p.vs = d.G * d.D;
+  p.scale = d.scale;
+  p.bf16 = d.bf16;
+  return p;
+}
+
+}  // namespace
+
+int64_t attention_step_blocks(const AttentionStepDims& d) { return d.B * row_tiles(d) * d.G; }
+
+AttentionDims attention_step_prefix(const AttentionStepDims& d) { return prefix_dims(d); }
+
+size_t attention_step_bytes(const AttentionStepDims& d) {
+  int n = splits_of(d);
+  if (n == 1 && !d.prefix) return 0;
+  if (d.prefix) n += attention_parts(prefix_dims(d));
+  return (size_t)n * d.B * d.H * (d.D + 1) * 4;
+}
+
+hipError_t launch_attention_step(const AttentionStepDims& d, const void* q, const void* k,
+                                 const void* v, void* k_cache, void* v_cache,
+                                 const int32_t* lengths, const void* k_prefix,
+                                 const void* v_prefix, void* o, void* ws, hipStream_t s) {
+  StepArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.lengths = lengths;
+  a.o = o;
+  a.qs = d.qs;
+  a.ks = d.ks;
+  a.vs = d.vs;
+  a.rows = d.rows;
+  a.B = (int)d.B;
+  a.H = (int)d.H;
+  a.G = (int)d.G;
+  a.rep = (int)(d.H / d.G);
+  a.D = (int)d.D;
+  a.tiles = (int)row_tiles(d);
+  a.c = d.scale * kLog2e;
+  const int splits = splits_of(d);
+  const int more = d.prefix ? attention_parts(prefix_dims(d)) : 0;
+  const int64_t rows = d.B * d.H;
+  if (splits + more > 1) {
+    a.part_o = (float*)ws;
+    a.part_lse = a.part_o + (splits + more) * rows * d.D;
+  }
+  hipError_t e;
+  if (d.bf16)
+    e = d.D <= 64 ? go<bf16, 64>(a, splits, s) : go<bf16, 128>(a, splits, s);
+  else
+    e = d.D <= 64 ? go<float, 64>(a, splits, s) : go<float, 128>(a, splits, s);
+  if (e != hipSuccess || splits + more == 1) return e;
+  if (more) {
+    e = launch_attention_parts(prefix_dims(d), q, k_prefix, v_prefix,
+                               a.part_o + splits * rows * d.D, a.part_lse + splits * rows, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch_attention_join(a.part_o, a.part_lse, o, nullptr, rows, d.D, splits + more, d.bf16,
+                               s);
+}
+
+}  // namespace m2

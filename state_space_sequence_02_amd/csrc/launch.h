@@ -190,6 +190,58 @@ hipError_t launch_selective_scan_step(const ScanDims& d, const void* u, const vo
                                       const void* z, const float* dt_bias, float* state, void* y,
                                       hipStream_t s);
 
+// The operators of an attention layer (rotary.hip, attention*.hip).  Strides as above.
+struct RotaryDims {
+  int64_t B, L, H, G, D, R, qs, ks, yqs, yks;
+  float scale;
+  bool bf16, half;
+};
+hipError_t launch_rotary(const RotaryDims& d, const void* q, const void* k, const float* inv_freq,
+                         const int32_t* positions, void* yq, void* yk, bool back, hipStream_t s);
+
+struct AttentionDims {
+  int64_t B, Lq, Lk, H, G, D, qs, ks, vs, dqs, dks, dvs;
+  float scale;
+  bool causal, qpacked, kpacked, bf16;
+  int64_t q_rows() const { return qpacked ? Lq : B * Lq; }
+  int64_t k_rows() const { return kpacked ? Lk : B * Lk; }
+};
+// Largest head; workgroups along x of the largest launch.
+constexpr int64_t kAttentionMaxHead = 128;
+int64_t attention_blocks(const AttentionDims& d);
+int64_t attention_key_blocks(const AttentionDims& d);
+size_t attention_forward_bytes(const AttentionDims& d);
+hipError_t launch_attention(const AttentionDims& d, const void* q, const void* k, const void* v,
+                            const int32_t* q_seqs, const int32_t* k_seqs, void* o, float* lse,
+                            void* ws, hipStream_t s);
+// The forward in attention_parts(d) ranges of the keys: normalised float32
+// outputs [parts][rows of q][H][D] and their log2 sums [parts][rows of q][H];
+// and their join (lse may be NULL).
+int attention_parts(const AttentionDims& d);
+hipError_t launch_attention_parts(const AttentionDims& d, const void* q, const void* k,
+                                  const void* v, float* part_o, float* part_lse, hipStream_t s);
+hipError_t launch_attention_join(const float* part_o, const float* part_lse, void* o, float* lse,
+                                 int64_t rows, int64_t D, int parts, bool bf16, hipStream_t s);
+size_t attention_backward_bytes(const AttentionDims& d);
+hipError_t launch_attention_backward(const AttentionDims& d, const void* q, const void* k,
+                                     const void* v, const int32_t* q_seqs, const int32_t* k_seqs,
+                                     const void* o, const float* lse, const void* dout, void* dq,
+                                     void* dk, void* dv, void* ws, hipStream_t s);
+
+struct AttentionStepDims {
+  int64_t B, rows, prefix, H, G, D, qs, ks, vs;
+  float scale;
+  bool bf16;
+};
+int64_t attention_step_blocks(const AttentionStepDims& d);
+// The prefix as a prompt's keys: the batch's tokens are its rows.
+AttentionDims attention_step_prefix(const AttentionStepDims& d);
+size_t attention_step_bytes(const AttentionStepDims& d);
+hipError_t launch_attention_step(const AttentionStepDims& d, const void* q, const void* k,
+                                 const void* v, void* k_cache, void* v_cache,
+                                 const int32_t* lengths, const void* k_prefix,
+                                 const void* v_prefix, void* o, void* ws, hipStream_t s);
+
 // out[m] = sum over rows p of part[p][m], columns [0, ends[0]), [ends[0],
 // ends[1]) and [ends[1], ends[2]) going to outs[0..2] (NULL: not written).
 hipError_t launch_partial_sums(const float* part, int64_t P, int64_t M, const int64_t ends[3],

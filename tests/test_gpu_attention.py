@@ -1,0 +1,268 @@
+"""The operators of an attention layer on the GPU, element by element against
+float64 within bounds that count the roundings (attention_reference.py)."""
+import math
+
+import pytest
+import torch
+
+import attention_reference as ref
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def m2():
+    import state_space_sequence_02_amd as lib
+    return lib
+
+
+def rnd(g, *shape, dtype=F32, scale=1.0):
+    return (scale * torch.randn(shape, generator=g)).to(dtype)
+
+
+def whole(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def close(got, want, bound, name):
+    got = ref.to64(got).reshape(want.shape)
+    none = torch.isinf(want)
+    assert torch.equal(got[none], want[none]), name
+    off = (got - want)[~none].abs()
+    over = off - bound[~none]
+    assert not torch.isnan(off).any(), f"{name}: NaN"
+    worst = float(over.max()) if over.numel() else 0.0
+    assert worst <= 0, f"{name}: over its bound by {worst:.3e} (largest error {float(off.max()):.3e})"
+
+
+# ---------------------------------------------------------------------- rotary
+
+
+ROTARY = [
+    # lead, H, G, D, R, layout, dtype, extra columns, positions
+    ((2, 37), 4, 2, 64, 64, "half", BF, 0, False),
+    ((2, 37), 4, 2, 64, 64, "interleaved", BF, 16, True),
+    ((3, 5), 3, 1, 50, 22, "interleaved", F32, 0, True),
+    ((3, 5), 3, 1, 50, 22, "half", BF, 7, True),
+    ((1, 1), 1, 1, 2, 2, "half", F32, 0, False),
+    ((130,), 32, 8, 128, 128, "half", BF, 64, True),
+    ((1000,), 5, 0, 96, 32, "interleaved", F32, 4, True),
+    ((2, 3, 11), 2, 2, 32, 16, "half", F32, 0, False),
+    ((1, 33), 2, 1, 700, 602, "half", F32, 0, True),
+]
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("lead,H,G,D,R,layout,dtype,extra,far", ROTARY)
+def test_rotary(m2, lead, H, G, D, R, layout, dtype, extra, far, back):
+    g = torch.Generator().manual_seed(11)
+    say(f"[rotary] {lead} {H} {G} {D} {R} {layout} {dtype} back={back}")
+    pad = -(-H * D // 8) * 8
+    row = rnd(g, *lead, pad + G * D + extra, dtype=dtype).cuda()
+    q = row[..., :H * D].unflatten(-1, (H, D))
+    k = row[..., pad:pad + G * D].unflatten(-1, (G, D)) if G else None
+    inv = (10000.0 ** (-torch.arange(0, R, 2, dtype=torch.float64) / R)).float().cuda()
+    pos = None
+    if far:
+        pos = torch.randint(-5, 1 << 30, lead, generator=g).to(torch.int32).cuda()
+    fn = m2.rotary_backward if back else m2.rotary_forward
+    got = fn(q, k, inv, pos, layout=layout, scale=1.25)
+    torch.cuda.synchronize()
+    tokens = math.prod(lead)
+    at = (torch.arange(lead[-1]).repeat(tokens // lead[-1]) if pos is None else pos.cpu().flatten())
+    for x, y, name in zip((q, k), (got if G else (got,)), "qk"):
+        x64 = ref.to64(x).reshape(tokens, -1, D)
+        want = ref.rotary(x64, inv.cpu(), at, layout, 1.25, back)
+        close(y, want, ref.rotary_bound(x64, want, R, layout, 1.25, dtype), name)
+        assert y.is_contiguous() and y.shape == x.shape
+
+
+def test_rotary_in_place(m2):
+    g = torch.Generator().manual_seed(12)
+    row = rnd(g, 3, 40, 8 * 64, dtype=BF).cuda()
+    inv, scale = m2.rotary_frequencies(64, device="cuda")
+    q, k = row[..., :384].unflatten(-1, (6, 64)), row[..., 384:].unflatten(-1, (2, 64))
+    want = m2.rotary_forward(q, k, inv)
+    dims = m2.make_rotary_dims(3, 40, 6, 2, 64, 64, BF, q_stride=512, k_stride=512, yq_stride=512,
+                               yk_stride=512)
+    m2.mamba2_rotary_forward(dims, q, k, inv, None, q, k)
+    torch.cuda.synchronize()
+    assert scale == 1.0
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+def test_rotary_turns_back(m2):
+    """The backward is the forward's transpose: for any x, y: <turn(x), y> = <x, back(y)>, in
+    float32 to the sums' own roundings."""
+    g = torch.Generator().manual_seed(13)
+    x, y = rnd(g, 2, 50, 3, 40).cuda(), rnd(g, 2, 50, 3, 40).cuda()
+    inv, _ = m2.rotary_frequencies(24, device="cuda")
+    a = (m2.rotary_forward(x, None, inv, scale=1.5).double() * y.double()).sum()
+    b = (x.double() * m2.rotary_backward(y, None, inv, scale=1.5).double()).sum()
+    size = 1.5 * 2 * (x.double().abs() * y.double().abs()).sum() * 12 * ref.U
+    # pairs: at most |x1||y1| + |x2||y1| + ...; bounded by twice the norms' product per pair
+    size = size + 12 * ref.U * 3 * float(x.double().norm() * y.double().norm())
+    assert abs(float(a - b)) <= float(size)
+
+
+# ------------------------------------------------------------------- attention
+
+
+def build(g, dtype, H, G, D, form, nq, nk, extra, tail, fill):
+    """Inputs on the GPU, their keyword arguments, flat float64 copies and the spans."""
+    same = form in ("padded", "packed") and nq == nk
+    lead = lambda n: (sum(n) + tail,) if "packed" in form else (len(n), max(max(n), 1) + tail)  # noqa: E731
+    lq, lk = lead(nq), (lead(nk) if form != "packed-cache" else (len(nk), max(max(nk), 1) + tail))
+    if same:
+        row = rnd(g, *lq, (H + 2 * G) * D + extra, dtype=dtype)
+        cols = [row[..., a * D:b * D].unflatten(-1, (b - a, D)) for a, b in
+                ((0, H), (H, H + G), (H + G, H + 2 * G))]
+    else:
+        cols = [rnd(g, *lq, H * D + extra, dtype=dtype)[..., :H * D].unflatten(-1, (H, D)),
+                rnd(g, *lk, G, D, dtype=dtype), rnd(g, *lk, G, D, dtype=dtype)]
+    kw = {}
+    sides = {}
+    for side, n, l in (("q", nq, lq), ("k", nk, lk)):
+        if len(l) == 1:
+            at = [tail // 2]
+            for v in n:
+                at.append(at[-1] + v)
+            kw[side + "_starts"] = whole(at)
+            sides[side] = ref.spans(at, None, l[0], len(n), 0)
+        else:
+            if tail or min(n) < l[1]:
+                kw[side + "_lengths"] = whole(n)
+            sides[side] = ref.spans(None, n, 0, len(n), l[1])
+    # what belongs to no token holds anything
+    flat = [c.reshape(-1, *c.shape[-2:]) for c in cols]
+    for i, side in enumerate("qkk"):
+        gone = torch.ones(flat[i].shape[0], dtype=torch.bool)
+        for a, n in sides[side]:
+            gone[a:a + n] = False
+        cols[i][gone.view(cols[i].shape[:-2])] = fill
+    flat = [torch.nan_to_num(ref.to64(c)).reshape(-1, *c.shape[-2:]) for c in cols]
+    if same:
+        dev = row.cuda()
+        dev = [dev[..., a * D:b * D].unflatten(-1, (b - a, D)) for a, b in
+               ((0, H), (H, H + G), (H + G, H + 2 * G))]
+    else:
+        dev = [c.cuda() for c in cols]
+    return dev, kw, flat, sides["q"], sides["k"]
+
+
+ATTENTION = [
+    # dtype, H, G, D, form, causal, queries, keys, extra columns, rows of no sequence
+    (BF, 4, 2, 64, "padded", True, [128, 128], [128, 128], 0, 0),
+    (BF, 4, 2, 64, "padded", False, [77, 0, 131], [77, 0, 131], 8, 5),
+    (BF, 2, 2, 128, "padded", True, [200], [200], 0, 0),
+    (BF, 6, 2, 128, "packed", True, [1, 65, 0, 130, 64, 31], [1, 65, 0, 130, 64, 31], 16, 7),
+    (BF, 8, 1, 40, "packed", False, [3, 190], [3, 190], 0, 3),
+    (BF, 4, 4, 8, "padded", True, [1, 1, 1], [1, 1, 1], 0, 0),
+    (BF, 3, 1, 72, "cross", True, [100, 5, 40], [37, 90, 0], 0, 2),
+    (BF, 16, 2, 64, "cross", True, [3], [700], 0, 0),
+    (BF, 40, 1, 64, "cross", False, [7, 2], [50, 130], 0, 1),
+    (BF, 5, 5, 128, "packed-cache", True, [20, 1, 63], [84, 129, 63], 0, 4),
+    (F32, 4, 2, 64, "padded", True, [150, 33], [150, 33], 4, 2),
+    (F32, 3, 3, 128, "packed", True, [40, 0, 90], [40, 0, 90], 0, 6),
+    (F32, 6, 2, 24, "cross", False, [65, 0], [129, 3], 0, 1),
+    (F32, 2, 1, 104, "cross", True, [90, 2], [30, 70], 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype,H,G,D,form,causal,nq,nk,extra,tail", ATTENTION)
+def test_attention(m2, dtype, H, G, D, form, causal, nq, nk, extra, tail):
+    say(f"[attention] {dtype} H={H} G={G} D={D} {form} causal={causal} {nq} {nk} {extra} {tail}")
+    g = torch.Generator().manual_seed(21)
+    (q, k, v), kw, flat, qs, ks = build(g, dtype, H, G, D, form, nq, nk, extra, tail, NAN)
+    dout = rnd(g, *q.shape, dtype=dtype)
+    d64 = ref.to64(dout).reshape(-1, H, D)
+    gone = torch.ones(d64.shape[0], dtype=torch.bool)
+    for a, n in qs:
+        gone[a:a + n] = False
+    dout.view(-1, H, D)[gone] = NAN
+    scale = 0.7 / math.sqrt(D)
+    o, lse = m2.attention_forward(q, k, v, causal=causal, scale=scale, **kw)
+    torch.cuda.synchronize()
+    want, bound = ref.attention(*flat, qs, ks, causal, scale, dtype, d64)
+    close(o, want["o"], bound["o"], "o")
+    close(lse, want["lse"], bound["lse"], "lse")
+    got = m2.attention_backward(q, k, v, o, lse, dout.cuda(), causal=causal, scale=scale, **kw)
+    torch.cuda.synchronize()
+    for name in ("dq", "dk", "dv"):
+        close(got[name], want[name], bound[name], name)
+
+
+@pytest.mark.parametrize("dtype,H,G,D,nq,nk", [
+    (BF, 8, 8, 128, 9, 4000), (BF, 4, 1, 64, 1, 3001), (F32, 2, 2, 64, 5, 2600),
+])
+def test_attention_few_rows(m2, dtype, H, G, D, nq, nk):
+    """Few rows against many keys: the keys are split and the parts joined."""
+    say(f"[few rows] {dtype} {H} {G} {D} {nq} {nk}")
+    g = torch.Generator().manual_seed(22)
+    q, k, v = rnd(g, 2, nq, H, D, dtype=dtype), rnd(g, 2, nk, G, D, dtype=dtype), \
+        rnd(g, 2, nk, G, D, dtype=dtype)
+    k_len, q_len = [nk, 700], [nq, nq]
+    dims = m2.make_attention_dims(2, nq, nk, H, G, D, dtype)
+    assert m2.mamba2_attention_workspace_bytes(dims) > 256  # parts
+    o, lse = m2.attention_forward(q.cuda(), k.cuda(), v.cuda(), k_lengths=whole(k_len))
+    torch.cuda.synchronize()
+    scale = dims.scale
+    want, bound = ref.attention(ref.to64(q).flatten(0, 1), ref.to64(k).flatten(0, 1),
+                                ref.to64(v).flatten(0, 1), ref.spans(None, q_len, 0, 2, nq),
+                                ref.spans(None, k_len, 0, 2, nk), True, scale, dtype)
+    close(o, want["o"], bound["o"], "o")
+    close(lse, want["lse"], bound["lse"], "lse")
+
+
+# ------------------------------------------------------------------- one token
+
+
+STEP = [
+    # dtype, B, rows, prefix, H, G, D, lengths
+    (BF, 3, 100, 0, 8, 2, 64, [0, 99, 100]),
+    (BF, 4, 700, 0, 32, 8, 128, [640, 31, 32, 700]),
+    (BF, 2, 65, 130, 4, 4, 128, [64, 1]),
+    (BF, 5, 33, 300, 12, 4, 64, [-3, 33, 40, 0, 7]),
+    (BF, 1, 1, 1, 1, 1, 8, [0]),
+    (BF, 2, 50, 20, 80, 2, 56, [17, 50]),
+    (F32, 3, 90, 70, 6, 2, 64, [0, 90, 45]),
+    (F32, 2, 260, 0, 4, 1, 128, [255, 256]),
+    (F32, 2, 40, 0, 3, 3, 24, [39, 12]),
+]
+
+
+@pytest.mark.parametrize("dtype,B,rows,prefix,H,G,D,lengths", STEP)
+def test_attention_step(m2, dtype, B, rows, prefix, H, G, D, lengths):
+    say(f"[step] {dtype} B={B} rows={rows} prefix={prefix} H={H} G={G} D={D} {lengths}")
+    g = torch.Generator().manual_seed(31)
+    row = rnd(g, B, (H + 2 * G) * D + 8, dtype=dtype)
+    q, k, v = (row[:, a * D:b * D].unflatten(-1, (b - a, D)) for a, b in
+               ((0, H), (H, H + G), (H + G, H + 2 * G)))
+    kc, vc = rnd(g, B, rows, G, D, dtype=dtype), rnd(g, B, rows, G, D, dtype=dtype)
+    kp = rnd(g, prefix, G, D, dtype=dtype) if prefix else None
+    vp = rnd(g, prefix, G, D, dtype=dtype) if prefix else None
+    scale = 1 / math.sqrt(D)
+    want, bound, wk, wv = ref.step(*(ref.to64(t) for t in (q, k, v, kc, vc)), lengths,
+                                   ref.to64(kp), ref.to64(vp), scale, dtype)
+    for i, n in enumerate(lengths):  # rows that hold nothing yet
+        kc[i, max(n, 0):] = NAN
+        vc[i, max(n, 0):] = NAN
+    dev = row.cuda()
+    q, k, v = (dev[:, a * D:b * D].unflatten(-1, (b - a, D)) for a, b in
+               ((0, H), (H, H + G), (H + G, H + 2 * G)))
+    kd, vd = kc.cuda(), vc.cuda()
+    o = m2.attention_step(q, k, v, kd, vd, whole(lengths),
+                          None if kp is None else kp.cuda(), None if vp is None else vp.cuda())
+    torch.cuda.synchronize()
+    close(o, want, bound, "o")
+    for i, n in enumerate(lengths):
+        n = min(max(n, 0), rows)
+        for cache, old, new in ((kd, kc, k), (vd, vc, v)):
+            got = cache[i].cpu()
+            assert torch.equal(got[:n], old[i, :n])
+            assert torch.isnan(got[n + 1:]).all()
+            if n < rows:
+                assert torch.equal(got[n], new[i].cpu())
