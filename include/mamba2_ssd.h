@@ -622,7 +622,7 @@ typedef struct {
  * q, k, v and o have the type of dims.  What stands behind a sequence's
  * tokens, or in packed rows of no sequence, is not used (it may hold
  * anything); o there is 0, lse -infinity and gradients are zeros.
- * Strides are multiples of 16 bytes.  Statistics and sums are float32; with
+ * Strides are multiples of 16 bytes and at most 2^22.  Statistics and sums are float32; with
  * bfloat16 the weights are rounded to it before the product with v.
  * Supported: rows of q and of k <= 2^28; rows of q * H / G < 2^31 - 256;
  * workgroups (G times the tiles of 128 rows of q * H / G, or of k; packed: and

@@ -22,6 +22,7 @@ constexpr int64_t kMaxBatch = 65535;
 constexpr int64_t kMaxTokens = (int64_t)1 << 28;       // rows of one side
 constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxStride = (int64_t)1 << 24;       // elements between tokens
+constexpr int64_t kMaxTileStride = (int64_t)1 << 22;   // of attention: a tile within 2^30 bytes
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 256;  // rows of q times heads of a group, tile included
 constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;  // workgroups of 256 along x
 
@@ -43,9 +44,10 @@ int check_stride(int64_t* stride, int64_t least, int64_t step, const char* name)
   if (*stride < least)
     return fail(MAMBA2_ERR_SHAPE, "%s (%lld) is shorter than a row (%lld)", name,
                 (long long)*stride, (long long)least);
-  if (*stride > kMaxStride)
+  const int64_t most = step > 1 ? kMaxTileStride : kMaxStride;
+  if (*stride > most)
     return fail(MAMBA2_ERR_UNSUPPORTED, "%s (%lld) is beyond %lld", name, (long long)*stride,
-                (long long)kMaxStride);
+                (long long)most);
   if (*stride % step)
     return fail(MAMBA2_ERR_UNSUPPORTED, "%s (%lld) is no multiple of %lld elements (16 bytes)",
                 name, (long long)*stride, (long long)step);

@@ -50,15 +50,20 @@ __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t hi) {
   return v < 0 ? 0 : v > hi ? hi : v;
 }
 
+// An element that is the same for all lanes, in a scalar register.
+__device__ __forceinline__ int uniform_at(const int32_t* p, int64_t i) {
+  return __builtin_amdgcn_readfirstlane(p[i]);
+}
+
 __device__ __forceinline__ Seq seq_of(const Side& s, int64_t b) {
   Seq q;
   if (!s.packed) {
     q.row0 = b * s.len;
     q.span = s.len;
-    q.n = s.seqs ? clamp64(s.seqs[b], s.len) : s.len;
+    q.n = s.seqs ? clamp64(uniform_at(s.seqs, b), s.len) : s.len;
   } else {
-    q.row0 = clamp64(s.seqs[b], s.len);
-    q.n = clamp64(s.seqs[b + 1], s.len) - q.row0;
+    q.row0 = clamp64(uniform_at(s.seqs, b), s.len);
+    q.n = clamp64(uniform_at(s.seqs, b + 1), s.len) - q.row0;
     if (q.n < 0) q.n = 0;
     q.span = q.n;
   }
@@ -109,11 +114,11 @@ __device__ __forceinline__ Tile tile_of(const Side& s, int64_t rep, int64_t tile
     count = left < step ? left : step;
   }
   const int64_t i = __builtin_amdgcn_readfirstlane((int)lo);
-  const int64_t cut = cut_of(s, i);
+  const int64_t cut = __builtin_amdgcn_readfirstlane((int)cut_of(s, i));
   t.r0 = (slot - (cut * rep / tile + i)) * tile;
   t.b = i - 1;
   t.seq.row0 = cut;
-  t.seq.span = cut_of(s, i + 1) - cut;
+  t.seq.span = __builtin_amdgcn_readfirstlane((int)cut_of(s, i + 1)) - cut;
   if (t.seq.span < 0) t.seq.span = 0;
   t.seq.n = t.seq.span;
   if (i == 0 || i == s.B + 1) {
@@ -223,34 +228,60 @@ __device__ __forceinline__ f32x16 mma_rows(const f32v8& a, const f32v8& b, f32x1
   return c;
 }
 
-// A lane's reads of an LDS tile.
+// A lane's reads of LDS tiles.  What a step or a column range changes of an
+// address are bits of the chunk, and the swizzle only flips bits, so each
+// address is one exclusive or away from the lane's own; rows and tiles are
+// constants of the instruction.  Tiles begin at multiples of a row.
 template <typename T, int DP>
 struct TileReader {
   using K = TileCfg<T, DP>;
-  // Rows r32 .. r32 + 31 at step s along the head.
-  __device__ __forceinline__ static head_frag<T> head(const char* tile, int r32, int s) {
-    const int lane = lane_id();
-    return *(const head_frag<T>*)(tile + r32 * K::ROWB +
-                                  chunk_at<K::CH>(lane & 31, 2 * s + (lane >> 5)));
-  }
-  // Column 32 dt + x at rows r16 .. r16 + 15, those of acc_frag.
-  __device__ __forceinline__ static row_frag<T> cols(const char* tile, int r16, int dt) {
+  uint32_t row, col;
+
+  __device__ __forceinline__ TileReader(uint32_t tile) {
     const int lane = lane_id(), hh = lane >> 5;
+    row = tile + chunk_at<K::CH>(lane & 31, hh);
     if constexpr (sizeof(T) == 2) {
       const int i = lane & 15;
-      const int c = 4 * dt + ((lane >> 4) & 1) * 2 + ((i & 3) >> 1);
-      const int r = 4 * hh + (i >> 2);
-      const char* at = tile + r16 * K::ROWB + (i & 1) * 8;
-      return cat(lds_read_tr((const bf16*)(at + chunk_at<K::CH>(r, c))),
-                 lds_read_tr((const bf16*)(at + chunk_at<K::CH>(r + 8, c))));
+      col = tile + chunk_at<K::CH>(4 * hh + (i >> 2), ((lane >> 4) & 1) * 2 + ((i & 3) >> 1)) +
+            (i & 1) * 8;
+    } else {
+      // row 4 hh + j adds j << 2 to the chunk's flips
+      col = tile + chunk_at<K::CH>(4 * hh, (lane & 31) >> 2) + (lane & 3) * 4;
+    }
+  }
+  template <typename V>
+  __device__ __forceinline__ static V at(uint32_t a, int offset) {
+    typedef __attribute__((address_space(3))) const V* lds_ptr;
+    return *(lds_ptr)(a + offset);
+  }
+  // The same reads of a tile that begins `bytes` (multiples of a row) later.
+  __device__ __forceinline__ TileReader later(uint32_t bytes) const {
+    TileReader r = *this;
+    r.row += bytes;
+    r.col += bytes;
+    return r;
+  }
+  // Rows r32 .. r32 + 31 at step s along the head; `offset`: bytes from the
+  // reader's tile, a constant.
+  __device__ __forceinline__ head_frag<T> head(int offset, int r32, int s) const {
+    return at<head_frag<T>>(row ^ (32 * s), offset + r32 * K::ROWB);
+  }
+  // Column 32 dt + x at rows r16 .. r16 + 15, those of acc_frag.
+  __device__ __forceinline__ row_frag<T> cols(int offset, int r16, int dt) const {
+    const int o = offset + r16 * K::ROWB;
+    if constexpr (sizeof(T) == 2) {
+      typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+      const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)((col ^ (64 * dt)) + o));
+      const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_ptr)((col ^ (64 * dt + 32)) + o + 8 * K::ROWB));
+      return cat(__builtin_bit_cast(bf16x4, lo), __builtin_bit_cast(bf16x4, hi));
     } else {
       f32v8 f;
-      const int c = 8 * dt + ((lane & 31) >> 2);
-      const char* at = tile + r16 * K::ROWB + (lane & 3) * 4;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int r = (j >> 2) * 8 + 4 * hh + (j & 3);
-        f.v[j] = *(const float*)(at + chunk_at<K::CH>(r, c));
+        // 8 rows on flip bit 1 of the chunk, row j bits 2 and 3
+        const uint32_t a = col ^ (128 * dt) ^ ((j & 3) * 64) ^ ((j >> 2) * 32);
+        f.v[j] = at<float>(a, o + ((j >> 2) * 8 + (j & 3)) * K::ROWB);
       }
       return f;
     }
@@ -279,6 +310,64 @@ __device__ __forceinline__ void load_row_frags(const T* row, int D,
     if (e < D) f[s] = *(const head_frag<T>*)(row + e);
   }
 }
+
+// 16-byte direct-to-LDS load from a uniform base plus this lane's 32-bit
+// offset; otherwise as dma16.  The wait states are those that a vector memory
+// instruction needs behind a vector instruction that wrote its scalar base,
+// which the compiler does not insert ahead of inline asm.
+__device__ __forceinline__ void dma16_at(const void* base, uint32_t offset, uint32_t lds_base) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_base);
+  const uint64_t a = (uint64_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(offset), "s"((uint64_t)hi << 32 | lo), "{m0}"(m0)
+               : "memory");
+}
+
+// Loads of ROWS rows of a tensor into an LDS tile by NT threads.
+template <typename T, int DP, int ROWS, int NT>
+struct Stager {
+  using K = TileCfg<T, DP>;
+  static constexpr int PER = ROWS * K::CH / NT;  // loads of a thread
+  uint32_t off[PER];
+
+  __device__ __forceinline__ static int row_of(int i, int thread) {
+    return (i * NT + thread) / K::CH;
+  }
+  __device__ __forceinline__ static int chunk_of(int i, int thread) {
+    return ((i * NT + thread) % K::CH) ^ swz<K::CH>(row_of(i, thread));
+  }
+  __device__ __forceinline__ Stager(int64_t stride, int thread) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      off[i] = (uint32_t)(row_of(i, thread) * (uint32_t)stride * (uint32_t)sizeof(T) +
+                          chunk_of(i, thread) * 16);
+  }
+  // The rows from `at` on, all of them there.
+  __device__ __forceinline__ void load(uint32_t lds, const T* at, int D, int thread) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (chunk_of(i, thread) * K::E < D)
+        dma16_at(at, off[i], lds + ((i * NT + thread) & ~63) * 16);
+  }
+  // Rows r0 on of n (at least one); those behind the last are the last again:
+  // finite values under weights of zero, and nothing behind the sequence is
+  // read.  `last`: where row n - 1 stands if not with the others, else NULL.
+  __device__ __forceinline__ static void load_tail(uint32_t lds, const T* base, int64_t stride,
+                                                   int r0, int n, const T* last, int D,
+                                                   int thread) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = chunk_of(i, thread), r = r0 + row_of(i, thread);
+      const int at = r < n - 1 ? r : n - 1;
+      const T* p = base + at * stride;
+      if (last && at == n - 1) p = last;
+      if (c * K::E < D) dma16(p + c * K::E, lds + ((i * NT + thread) & ~63) * 16);
+    }
+  }
+};
 
 // Clears a tile's chunks behind the head's end; loads never touch them.
 template <typename T, int DP>

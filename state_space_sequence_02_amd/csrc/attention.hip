@@ -75,23 +75,30 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_ke
     }
     low = __builtin_amdgcn_readfirstlane(low);
     high = __builtin_amdgcn_readfirstlane(high);
+    using St = Stager<T, DP, kKeys, kThreads>;
+    const St ks_(a.ks, threadIdx.x), vs_(a.vs, threadIdx.x);
     const auto stage = [&](int t) {
-      const uint32_t at = base + (t & 1) * 2 * TILE;
-      stage_rows<T, DP, kKeys, kThreads>(at, k, a.ks, nk, nullptr, t * kKeys, a.D, threadIdx.x);
-      stage_rows<T, DP, kKeys, kThreads>(at + TILE, v, a.vs, nk, nullptr, t * kKeys, a.D,
-                                         threadIdx.x);
+      const uint32_t to = base + (t & 1) * 2 * TILE;
+      const int r0 = t * kKeys;
+      if (r0 + kKeys <= nk) {
+        ks_.load(to, k + r0 * a.ks, a.D, threadIdx.x);
+        vs_.load(to + TILE, v + r0 * a.vs, a.D, threadIdx.x);
+      } else {
+        St::load_tail(to, k, a.ks, r0, nk, nullptr, a.D, threadIdx.x);
+        St::load_tail(to + TILE, v, a.vs, r0, nk, nullptr, a.D, threadIdx.x);
+      }
     };
+    const TileReader<T, DP> first(base);
     stage(t0);
     for (int t = t0; t < t1; ++t) {
       wait_vm(0);
       lds_barrier();  // tile t is there, and every wavefront is done with tile t - 1
       if (t + 1 < t1) stage(t + 1);
-      const char* kt = lds + (t & 1) * 2 * TILE;
       const int k0 = t * kKeys;
-      if (low >= k0 + kKeys)
-        st.template step<2, false>(q, kt, kt + TILE, lim - k0, a.c);
-      else if (high > k0)
-        st.template step<2, true>(q, kt, kt + TILE, lim - k0, a.c);
+      if (high > k0) {
+        const TileReader<T, DP> kr = first.later((t & 1) * 2 * TILE);
+        st.template step<kKeys / 32>(q, kr, kr.later(TILE), low < k0 + kKeys, lim - k0, a.c);
+      }
     }
   }
 

@@ -106,7 +106,6 @@ __device__ __forceinline__ void store_column(T* row, const f32x16 (&acc)[DP / 32
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq_kernel(BwdArgs a) {
   using K = TileCfg<T, DP>;
-  using R = TileReader<T, DP>;
   constexpr int TILE = kKeys * K::ROWB;
   extern __shared__ __align__(16) char lds[];
   const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
@@ -153,19 +152,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
     }
     low = __builtin_amdgcn_readfirstlane(low);
     high = __builtin_amdgcn_readfirstlane(high);
+    using St = Stager<T, DP, kKeys, kThreads>;
+    const St ks_(a.ks, threadIdx.x), vs_(a.vs, threadIdx.x);
     const auto stage = [&](int t) {
-      const uint32_t at = base + (t & 1) * 2 * TILE;
-      stage_rows<T, DP, kKeys, kThreads>(at, k, a.ks, nk, nullptr, t * kKeys, a.D, threadIdx.x);
-      stage_rows<T, DP, kKeys, kThreads>(at + TILE, v, a.vs, nk, nullptr, t * kKeys, a.D,
-                                         threadIdx.x);
+      const uint32_t to = base + (t & 1) * 2 * TILE;
+      const int r0 = t * kKeys;
+      if (r0 + kKeys <= nk) {
+        ks_.load(to, k + r0 * a.ks, a.D, threadIdx.x);
+        vs_.load(to + TILE, v + r0 * a.vs, a.D, threadIdx.x);
+      } else {
+        St::load_tail(to, k, a.ks, r0, nk, nullptr, a.D, threadIdx.x);
+        St::load_tail(to + TILE, v, a.vs, r0, nk, nullptr, a.D, threadIdx.x);
+      }
     };
+    const TileReader<T, DP> rd(base);
     stage(0);
     for (int t = 0; t < tiles; ++t) {
       wait_vm(0);
       lds_barrier();
       if (t + 1 < tiles) stage(t + 1);
-      const char* kt = lds + (t & 1) * 2 * TILE;
-      const char* vt = kt + TILE;
+      const TileReader<T, DP> kr = rd.later((t & 1) * 2 * TILE), vr = kr.later(TILE);
       const int k0 = t * kKeys;
 #pragma unroll
       for (int u = 0; u < kKeys / 32; ++u) {
@@ -173,9 +179,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
         if (high <= ku) break;
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
-        for (int d = 0; d < K::STEPS; ++d) s = mma_head(R::head(kt, 32 * u, d), q[d], s);
+        for (int d = 0; d < K::STEPS; ++d) s = mma_head(kr.head(0, 32 * u, d), q[d], s);
 #pragma unroll
-        for (int d = 0; d < K::STEPS; ++d) dp = mma_head(R::head(vt, 32 * u, d), dout[d], dp);
+        for (int d = 0; d < K::STEPS; ++d) dp = mma_head(vr.head(0, 32 * u, d), dout[d], dp);
         if (low < ku + 32) {
           const int left = lim - ku - 4 * hh;
 #pragma unroll
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
           const row_frag<T> ds = acc_frag<T>(s, h);
 #pragma unroll
           for (int d = 0; d < DP / 32; ++d)
-            acc[d] = mma_rows(R::cols(kt, 32 * u + 16 * h, d), ds, acc[d]);
+            acc[d] = mma_rows(kr.cols(0, 32 * u + 16 * h, d), ds, acc[d]);
         }
       }
     }
@@ -204,14 +210,13 @@ template <typename T, int DP>
 struct DkvCfg {
   static constexpr int ROWS = sizeof(T) == 2 ? 64 : 32;  // packed rows of a tile
   static constexpr int TILE = ROWS * TileCfg<T, DP>::ROWB;
-  static constexpr int BUF = 2 * TILE + 2 * ROWS * 4;  // Q, dO, lse2, delta
+  static constexpr int BUF = 2 * TILE + 512;  // Q, dO, lse2, delta
 };
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dkv_kernel(
     BwdArgs a) {
   using K = TileCfg<T, DP>;
-  using R = TileReader<T, DP>;
   using C = DkvCfg<T, DP>;
   extern __shared__ __align__(16) char lds[];
   const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
@@ -263,14 +268,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dk
         dma4(p, to + 2 * C::TILE + wave * C::ROWS * 4);
       }
     };
+    const TileReader<T, DP> rd(base);
     stage(begin);
     for (int t = begin; t < tiles; ++t) {
       wait_vm(0);
       lds_barrier();
       if (t + 1 < tiles) stage(t + 1);
-      const char* qt = lds + (t & 1) * C::BUF;
-      const char* dt = qt + C::TILE;
-      const float* st = (const float*)(dt + C::TILE);
+      const TileReader<T, DP> qr = rd.later((t & 1) * C::BUF), dr = qr.later(C::TILE);
+      const float* st = (const float*)(lds + (t & 1) * C::BUF + 2 * C::TILE);
       const int r0 = t * C::ROWS;
 #pragma unroll
       for (int u = 0; u < C::ROWS / 32; ++u) {
@@ -279,9 +284,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dk
         if (low >= ru + 32) continue;
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
-        for (int d = 0; d < K::STEPS; ++d) s = mma_head(R::head(qt, 32 * u, d), kf[d], s);
+        for (int d = 0; d < K::STEPS; ++d) s = mma_head(qr.head(0, 32 * u, d), kf[d], s);
 #pragma unroll
-        for (int d = 0; d < K::STEPS; ++d) dp = mma_head(R::head(dt, 32 * u, d), vf[d], dp);
+        for (int d = 0; d < K::STEPS; ++d) dp = mma_head(dr.head(0, 32 * u, d), vf[d], dp);
         if (high > ru || ru + 32 > rows) {
           const int lo = first - ru - 4 * hh, hi = rows - ru - 4 * hh;
 #pragma unroll
@@ -306,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dk
           const row_frag<T> pf = acc_frag<T>(s, h), df = acc_frag<T>(ds, h);
 #pragma unroll
           for (int d = 0; d < DP / 32; ++d) {
-            dv[d] = mma_rows(R::cols(dt, 32 * u + 16 * h, d), pf, dv[d]);
-            dk[d] = mma_rows(R::cols(qt, 32 * u + 16 * h, d), df, dk[d]);
+            dv[d] = mma_rows(dr.cols(0, 32 * u + 16 * h, d), pf, dv[d]);
+            dk[d] = mma_rows(qr.cols(0, 32 * u + 16 * h, d), df, dk[d]);
           }
         }
       }

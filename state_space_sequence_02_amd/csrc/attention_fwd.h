@@ -16,33 +16,6 @@
 
 namespace m2 {
 
-// Rows of K and V of one (sequence, group).
-template <typename T>
-struct Keys {
-  const T *k, *v;            // row 0
-  int64_t ks, vs;            // elements between rows
-  int n;                     // rows, >= 1
-  const T *k_last, *v_last;  // row n - 1, where it stands elsewhere; else NULL
-};
-
-// Starts the loads of rows r0 .. r0 + ROWS - 1 into an LDS tile, by NT
-// threads.  Rows behind the last are the last again: finite values under
-// weights of zero, and nothing behind the sequence is read.
-template <typename T, int DP, int ROWS, int NT>
-__device__ __forceinline__ void stage_rows(uint32_t lds, const T* base, int64_t stride, int n,
-                                           const T* last, int r0, int D, int thread) {
-  using K = TileCfg<T, DP>;
-#pragma unroll
-  for (int i = 0; i < ROWS * K::CH / NT; ++i) {
-    const int slot = i * NT + thread;
-    const int r = slot / K::CH, c = (slot % K::CH) ^ swz<K::CH>(r);
-    const int at = r0 + r < n - 1 ? r0 + r : n - 1;
-    const T* p = base + at * stride;
-    if (last && at == n - 1) p = last;
-    if (c * K::E < D) dma16(p + c * K::E, lds + (slot & ~63) * 16);
-  }
-}
-
 template <typename T, int DP>
 struct RowState {
   f32x16 o[DP / 32];
@@ -55,20 +28,21 @@ struct RowState {
     l = 0.f;
   }
 
-  // One tile of 32 SUBS keys.  lim: keys of the tile that this lane's row sees.
-  template <int SUBS, bool MASK>
+  // One tile of 32 SUBS keys.  lim: keys of the tile that this lane's row sees;
+  // mask: whether that is not all of them for some lane (uniform).
+  template <int SUBS>
   __device__ __forceinline__ void step(const head_frag<T> (&q)[TileCfg<T, DP>::STEPS],
-                                       const char* kt, const char* vt, int lim, float c) {
-    using R = TileReader<T, DP>;
+                                       const TileReader<T, DP>& kr, const TileReader<T, DP>& vr,
+                                       bool mask, int lim, float c) {
     f32x16 s[SUBS];
 #pragma unroll
     for (int u = 0; u < SUBS; ++u) {
       s[u] = zero16();
 #pragma unroll
       for (int d = 0; d < TileCfg<T, DP>::STEPS; ++d)
-        s[u] = mma_head(R::head(kt, 32 * u, d), q[d], s[u]);
+        s[u] = mma_head(kr.head(0, 32 * u, d), q[d], s[u]);
     }
-    if constexpr (MASK) {
+    if (mask) {
       const int left = lim - 4 * (lane_id() >> 5);
 #pragma unroll
       for (int u = 0; u < SUBS; ++u)
@@ -106,7 +80,7 @@ struct RowState {
         const row_frag<T> p = acc_frag<T>(s[u], h);
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
-          o[d] = mma_rows(R::cols(vt, 32 * u + 16 * h, d), p, o[d]);
+          o[d] = mma_rows(vr.cols(0, 32 * u + 16 * h, d), p, o[d]);
       }
     }
   }

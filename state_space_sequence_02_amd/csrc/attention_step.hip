@@ -39,13 +39,12 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_ke
   using K = TileCfg<T, DP>;
   constexpr int W = waves_of<T, DP>();
   constexpr int TILE = 32 * K::ROWB;
-  constexpr int LOADS = 2 * 32 * K::CH / 64;  // of a wavefront for a tile of K and V
   extern __shared__ __align__(16) char lds[];  // [W][2][K tile, V tile]
   const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
   const int g = blockIdx.x % a.G, rest = blockIdx.x / a.G;
   const int b = rest / a.tiles, r0 = rest % a.tiles * 32;
   const int64_t cap = a.rows;
-  const int n = (int)clamp64(a.lengths[b], cap);
+  const int n = (int)clamp64(uniform_at(a.lengths, b), cap);
   const int64_t cs = (int64_t)a.G * a.D;
   const int64_t cache = (int64_t)b * cap * cs + (int64_t)g * a.D;
   const T* kn = (const T*)a.k + b * a.ks + (int64_t)g * a.D;
@@ -73,11 +72,19 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_ke
     head_frag<T> q[K::STEPS];
     load_row_frags<T, DP>((const T*)a.q + b * a.qs + (int64_t)head * a.D, a.D, q);
     clear_ends<T, DP>(mine, 4 * 32, a.D, lane, 64);
+    using St = Stager<T, DP, 32, 64>;
+    const St off(cs, lane);
     const auto stage = [&](int t, int buf) {
       const uint32_t to = base + buf * 2 * TILE;
-      stage_rows<T, DP, 32, 64>(to, kc, cs, nk, kn, t * 32, a.D, lane);
-      stage_rows<T, DP, 32, 64>(to + TILE, vc, cs, nk, vn, t * 32, a.D, lane);
+      if (t * 32 + 32 <= n) {
+        off.load(to, kc + t * 32 * cs, a.D, lane);
+        off.load(to + TILE, vc + t * 32 * cs, a.D, lane);
+      } else {
+        St::load_tail(to, kc, cs, t * 32, nk, kn, a.D, lane);
+        St::load_tail(to + TILE, vc, cs, t * 32, nk, vn, a.D, lane);
+      }
     };
+    const TileReader<T, DP> first(base);
     wait_vm(0);
     stage(t0 + wave, 0);
     int buf = 0;
@@ -85,16 +92,13 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_ke
       // the other buffer's reads are done: their results were used
       if (t + W < t1) {
         stage(t + W, buf ^ 1);
-        wait_vm(LOADS);
+        wait_vm(2 * St::PER);
       } else {
         wait_vm(0);
       }
       asm volatile("" ::: "memory");
-      const char* kt = mine + buf * 2 * TILE;
-      if (t * 32 + 32 <= nk)
-        st.template step<1, false>(q, kt, kt + TILE, 32, a.c);
-      else
-        st.template step<1, true>(q, kt, kt + TILE, nk - t * 32, a.c);
+      const TileReader<T, DP> kr = first.later(buf * 2 * TILE);
+      st.template step<1>(q, kr, kr.later(TILE), t * 32 + 32 > nk, nk - t * 32, a.c);
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       asm volatile("" ::: "memory");
     }
