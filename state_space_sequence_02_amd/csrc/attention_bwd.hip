@@ -24,9 +24,10 @@ constexpr int kRows = 128;     // packed rows (dQ) or keys (dK, dV) of a workgro
 constexpr int kKeys = 64;      // keys of a tile in the dQ kernel
 
 struct BwdArgs {
-  const void *q, *k, *v, *dout;
+  const void *q, *k, *v, *o, *dout;
+  const float* lse;
   void *dq, *dk, *dv;
-  const float *lse2, *delta;  // [rows of q][H]; lse in log2 units, 0 for rows without keys
+  float *lse2, *delta;  // [rows of q][H]; lse in log2 units, 0 for rows without keys
   Side qside, kside;
   int64_t qs, ks, vs, dqs, dks, dvs, slots;
   int H, G, rep, D;
@@ -39,29 +40,6 @@ struct BwdArgs {
 // r / rep for 0 <= r < 2^31: M = ceil(2^(31 + l) / rep), l = ceil(log2 rep).
 __device__ __forceinline__ int over_rep(const BwdArgs& a, int r) {
   return (int)(__umulhi(2u * (unsigned)r, a.div_m) >> a.div_l);
-}
-
-// delta and lse in log2 units: 32 lanes a (token, head) row, 4 elements each.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attention_rows_kernel(
-    const T* __restrict__ o, const T* __restrict__ dout, const float* __restrict__ lse,
-    float* __restrict__ lse2, float* __restrict__ delta, int64_t rows, int D) {
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  const int e = threadIdx.x % 32 * 4;
-  float sum = 0.f;
-  if (row < rows && e < D) {
-    float x[4], y[4];
-    load_row<T, 4>(o + row * D + e, x);
-    load_row<T, 4>(dout + row * D + e, y);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum = __builtin_fmaf(x[i], y[i], sum);
-  }
-  sum = lanes_sum<32>(sum);
-  if (row < rows && e == 0) {
-    const float l = lse[row];
-    delta[row] = sum;
-    lse2[row] = l == -__builtin_inff() ? 0.f : l * kLog2e;
-  }
 }
 
 // Starts the loads of packed rows r0 .. r0 + ROWS - 1 of a group; rows behind
@@ -132,14 +110,30 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
   f32x16 acc[DP / 32];
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) acc[d] = zero16();
-  if (tiles) {
+  if (tile.r0 < rows) {
     head_frag<T> q[K::STEPS], dout[K::STEPS];
     const int safe = row < rows ? row : rows - 1;
     const int64_t tok = tile.seq.row0 + safe / a.rep;
     const int hd = g * a.rep + safe % a.rep;
+    const int64_t at = tok * a.H + hd;
     load_row_frags<T, DP>((const T*)a.q + tok * a.qs + (int64_t)hd * a.D, a.D, q);
-    load_row_frags<T, DP>((const T*)a.dout + (tok * a.H + hd) * a.D, a.D, dout);
-    const float lse2 = a.lse2[tok * a.H + hd], delta = a.delta[tok * a.H + hd];
+    load_row_frags<T, DP>((const T*)a.dout + at * a.D, a.D, dout);
+    // delta and lse of a row, also for the other kernel
+    head_frag<T> o[K::STEPS];
+    load_row_frags<T, DP>((const T*)a.o + at * a.D, a.D, o);
+    float delta = 0.f;
+#pragma unroll
+    for (int s = 0; s < K::STEPS; ++s)
+#pragma unroll
+      for (int e = 0; e < K::E; ++e)
+        delta = __builtin_fmaf(to_f32(o[s][e]), to_f32(dout[s][e]), delta);
+    delta = add_xor32(delta);
+    float lse2 = a.lse[at];
+    lse2 = lse2 == -__builtin_inff() ? 0.f : lse2 * kLog2e;
+    if (row < rows && hh == 0) {
+      a.lse2[at] = lse2;
+      a.delta[at] = delta;
+    }
     const T* k = (const T*)a.k + ks.row0 * a.ks + (int64_t)g * a.D;
     const T* v = (const T*)a.v + ks.row0 * a.vs + (int64_t)g * a.D;
     const uint32_t base = lds_addr(lds);
@@ -166,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
       }
     };
     const TileReader<T, DP> rd(base);
-    stage(0);
+    if (tiles) stage(0);
     for (int t = 0; t < tiles; ++t) {
       wait_vm(0);
       lds_barrier();
@@ -206,21 +200,56 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
                       a.scale, a.D);
 }
 
+// The dK and dV kernel: 4 wavefronts along the keys, in bfloat16 two such sets
+// that take the rows of a tile in halves and add their sums at the end: a
+// workgroup fills its CU and the longest walk (the first keys of a causal
+// sequence) takes half as long as with one set (2 x 4096 rows, 32 heads of
+// 128: LATER us instead of 894, with 512 workgroups of one set all at once).
 template <typename T, int DP>
 struct DkvCfg {
+  static constexpr int SETS = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int THREADS = 256 * SETS;
   static constexpr int ROWS = sizeof(T) == 2 ? 64 : 32;  // packed rows of a tile
+  static constexpr int SUBS = ROWS / 32 / SETS;          // 32-row parts of a set
   static constexpr int TILE = ROWS * TileCfg<T, DP>::ROWB;
-  static constexpr int BUF = 2 * TILE + 512;  // Q, dO, lse2, delta
+  static constexpr int STATS = 2 * ROWS * 4 < 512 ? 512 : 2 * ROWS * 4;
+  static constexpr int BUF = 2 * TILE + STATS;  // Q, dO, lse2 and delta
+  static constexpr int JOIN = SETS == 2 ? 4 * 32 * DP * 4 : 0;
+  static constexpr int LDS = 2 * BUF > JOIN ? 2 * BUF : JOIN;
 };
 
+// A wavefront's sums to and from LDS.
+template <int N>
+__device__ __forceinline__ void put(char* lds, int wave, const f32x16 (&v)[N]) {
+  f32x4* to = (f32x4*)lds + wave * (N * 4 * 64) + lane_id();
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      to[(d * 4 + r) * 64] = f32x4{v[d][4 * r], v[d][4 * r + 1], v[d][4 * r + 2], v[d][4 * r + 3]};
+}
+template <int N>
+__device__ __forceinline__ void add(const char* lds, int wave, f32x16 (&v)[N]) {
+  const f32x4* from = (const f32x4*)lds + wave * (N * 4 * 64) + lane_id();
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const f32x4 x = from[(d * 4 + r) * 64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[d][4 * r + i] += x[i];
+    }
+}
+
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dkv_kernel(
-    BwdArgs a) {
+__global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 : 1))
+    attention_dkv_kernel(BwdArgs a) {
   using K = TileCfg<T, DP>;
   using C = DkvCfg<T, DP>;
   extern __shared__ __align__(16) char lds[];
-  const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
+  const int lane = lane_id(), wave = wave_id() & 3, set = wave_id() >> 2, hh = lane >> 5;
   const int g = blockIdx.x % a.G;
+  // the first keys of a causal sequence are seen by most rows: they go first
   const Tile tile = tile_of(a.kside, 1, kRows, blockIdx.x / a.G);
   if (tile.r0 >= tile.seq.span) return;
   const int nk = (int)tile.seq.n;
@@ -235,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dk
   };
   const int first = first_of(key < nk ? key : nk - 1);
   const int wave_last = k0 + wave * 32 + 31;
-  const int low = first_of(k0 + wave * 32);                          // the wavefront's earliest row
-  const int high = first_of(wave_last < nk ? wave_last : nk - 1);    // all its keys are seen from here
+  const int low = first_of(k0 + wave * 32);                        // the wavefront's earliest row
+  const int high = first_of(wave_last < nk ? wave_last : nk - 1);  // all its keys are seen from here
   const int begin = k0 < nk ? first_of(k0) / C::ROWS : 0;
   const int tiles = k0 < nk ? (rows + C::ROWS - 1) / C::ROWS : 0;
 
@@ -253,19 +282,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dk
     const float* lse2 = a.lse2 + qs.row0 * a.H + g * a.rep;
     const float* delta = a.delta + qs.row0 * a.H + g * a.rep;
     const uint32_t base = lds_addr(lds);
-    clear_ends<T, DP>(lds, 2 * C::ROWS, a.D, threadIdx.x, kThreads);
-    clear_ends<T, DP>(lds + C::BUF, 2 * C::ROWS, a.D, threadIdx.x, kThreads);
+    clear_ends<T, DP>(lds, 2 * C::ROWS, a.D, threadIdx.x, C::THREADS);
+    clear_ends<T, DP>(lds + C::BUF, 2 * C::ROWS, a.D, threadIdx.x, C::THREADS);
     const auto stage = [&](int t) {
       const uint32_t to = base + (t & 1) * C::BUF;
       const int r0 = t * C::ROWS;
-      stage_packed<T, DP, C::ROWS, kThreads>(to, q, a.qs, rows, r0, a, threadIdx.x);
-      stage_packed<T, DP, C::ROWS, kThreads>(to + C::TILE, dout, (int64_t)a.H * a.D, rows, r0, a,
-                                             threadIdx.x);
-      if (wave < 2 && lane < C::ROWS) {
-        const int r = r0 + lane < rows ? r0 + lane : rows - 1;
-        const int tok = over_rep(a, r);
-        const float* p = (wave ? delta : lse2) + (int64_t)tok * a.H + (r - tok * a.rep);
-        dma4(p, to + 2 * C::TILE + wave * C::ROWS * 4);
+      stage_packed<T, DP, C::ROWS, C::THREADS>(to, q, a.qs, rows, r0, a, threadIdx.x);
+      stage_packed<T, DP, C::ROWS, C::THREADS>(to + C::TILE, dout, (int64_t)a.H * a.D, rows, r0, a,
+                                               threadIdx.x);
+      // wavefront 0: lse2, wavefront 1: delta of the tile's rows, 64 at a time
+      const int w = wave_id();
+#pragma unroll
+      for (int i = 0; i < (C::ROWS + 63) / 64; ++i) {
+        if (w < 2 && lane < C::ROWS) {
+          const int r = r0 + 64 * i + lane < rows ? r0 + 64 * i + lane : rows - 1;
+          const int tok = over_rep(a, r);
+          const float* p = (w ? delta : lse2) + (int64_t)tok * a.H + (r - tok * a.rep);
+          dma4(p, to + 2 * C::TILE + w * C::ROWS * 4 + i * 256);
+        }
       }
     };
     const TileReader<T, DP> rd(base);
@@ -274,14 +308,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dk
       wait_vm(0);
       lds_barrier();
       if (t + 1 < tiles) stage(t + 1);
-      const TileReader<T, DP> qr = rd.later((t & 1) * C::BUF), dr = qr.later(C::TILE);
-      const float* st = (const float*)(lds + (t & 1) * C::BUF + 2 * C::TILE);
-      const int r0 = t * C::ROWS;
+      const int half = set * C::SUBS * 32;  // this set's rows of the tile
+      const TileReader<T, DP> qr = rd.later((t & 1) * C::BUF + half * K::ROWB),
+                              dr = qr.later(C::TILE);
+      const float* st = (const float*)(lds + (t & 1) * C::BUF + 2 * C::TILE) + half;
+      const int r0 = t * C::ROWS + half;
 #pragma unroll
-      for (int u = 0; u < C::ROWS / 32; ++u) {
+      for (int u = 0; u < C::SUBS; ++u) {
         const int ru = r0 + 32 * u;
-        if (ru >= rows) break;
-        if (low >= ru + 32) continue;
+        if (ru >= rows || low >= ru + 32) continue;
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
         for (int d = 0; d < K::STEPS; ++d) s = mma_head(qr.head(0, 32 * u, d), kf[d], s);
@@ -318,33 +353,48 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dk
       }
     }
   }
+  if constexpr (C::SETS == 2) {
+    if (begin < tiles) {  // the first set takes dV, the second dK
+      __syncthreads();
+      if (set == 1) put(lds, wave, dv);
+      __syncthreads();
+      if (set == 0) add(lds, wave, dv);
+      __syncthreads();
+      if (set == 0) put(lds, wave, dk);
+      __syncthreads();
+      if (set == 1) add(lds, wave, dk);
+    }
+  }
   if (key >= tile.seq.span) return;
   if (key >= nk) {
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = zero16();
   }
   const int64_t to = tile.seq.row0 + key;
-  store_column<T, DP>((T*)a.dk + to * a.dks + (int64_t)g * a.D, dk, a.scale, a.D);
-  store_column<T, DP>((T*)a.dv + to * a.dvs + (int64_t)g * a.D, dv, 1.f, a.D);
+  if (set == C::SETS - 1)
+    store_column<T, DP>((T*)a.dk + to * a.dks + (int64_t)g * a.D, dk, a.scale, a.D);
+  if (set == 0) store_column<T, DP>((T*)a.dv + to * a.dvs + (int64_t)g * a.D, dv, 1.f, a.D);
 }
 
 template <typename F>
-hipError_t launch_lds(F kernel, int64_t blocks, int bytes, const BwdArgs& a, hipStream_t s) {
+hipError_t launch_lds(F kernel, int64_t blocks, int threads, int bytes, const BwdArgs& a,
+                      hipStream_t s) {
   const hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
-  kernel<<<(unsigned)blocks, kThreads, bytes, s>>>(a);
+  kernel<<<(unsigned)blocks, threads, bytes, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, int DP>
 hipError_t go(BwdArgs a, hipStream_t s) {
-  a.slots = tile_slots(a.kside, 1, kRows);
-  hipError_t e = launch_lds(attention_dkv_kernel<T, DP>, a.slots * a.G, 2 * DkvCfg<T, DP>::BUF, a, s);
-  if (e != hipSuccess) return e;
+  using C = DkvCfg<T, DP>;
   a.slots = tile_slots(a.qside, a.rep, kRows);
-  return launch_lds(attention_dq_kernel<T, DP>, a.slots * a.G, 4 * kKeys * TileCfg<T, DP>::ROWB, a,
-                    s);
+  const hipError_t e = launch_lds(attention_dq_kernel<T, DP>, a.slots * a.G, kThreads,
+                                  4 * kKeys * TileCfg<T, DP>::ROWB, a, s);
+  if (e != hipSuccess) return e;
+  a.slots = tile_slots(a.kside, 1, kRows);
+  return launch_lds(attention_dkv_kernel<T, DP>, a.slots * a.G, C::THREADS, C::LDS, a, s);
 }
 
 }  // namespace
@@ -368,6 +418,8 @@ hipError_t launch_attention_backward(const AttentionDims& d, const void* q, cons
   a.q = q;
   a.k = k;
   a.v = v;
+  a.o = o;
+  a.lse = lse;
   a.dout = dout;
   a.dq = dq;
   a.dk = dk;
@@ -392,15 +444,6 @@ hipError_t launch_attention_backward(const AttentionDims& d, const void* q, cons
   a.causal = d.causal;
   a.c = d.scale * kLog2e;
   a.scale = d.scale;
-  const unsigned blocks = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
-  if (d.bf16)
-    attention_rows_kernel<bf16><<<blocks, kThreads, 0, s>>>((const bf16*)o, (const bf16*)dout, lse,
-                                                            lse2, delta, rows, a.D);
-  else
-    attention_rows_kernel<float><<<blocks, kThreads, 0, s>>>((const float*)o, (const float*)dout,
-                                                             lse, lse2, delta, rows, a.D);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   if (d.bf16) return d.D <= 64 ? go<bf16, 64>(a, s) : go<bf16, 128>(a, s);
   return d.D <= 64 ? go<float, 64>(a, s) : go<float, 128>(a, s);
 }
