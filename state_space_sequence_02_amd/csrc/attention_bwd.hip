@@ -30,6 +30,8 @@ struct BwdArgs {
   float *lse2, *delta;  // [rows of q][H]; lse in log2 units, 0 for rows without keys
   Side qside, kside;
   int64_t qs, ks, vs, dqs, dks, dvs, slots;
+  int64_t q_rows, k_rows;
+  float* part;  // where a walk is split: [gridDim.y][rows][heads][D], of dK and then of dV
   int H, G, rep, D;
   unsigned div_m;
   int div_l;
@@ -105,7 +107,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
   const int lim = row < rows ? seen(token) : 0;
   const int last = (int)(tile.r0 + kRows < rows ? tile.r0 + kRows : rows) - 1;
   const int most = last >= tile.r0 ? seen(last / a.rep) : 0;
-  const int tiles = (most + kKeys - 1) / kKeys;
+  const int all = (most + kKeys - 1) / kKeys;
+  const int per = (all + gridDim.y - 1) / gridDim.y;
+  const int t0 = blockIdx.y * per, tiles = t0 + per < all ? t0 + per : all;
 
   f32x16 acc[DP / 32];
 #pragma unroll
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
     delta = add_xor32(delta);
     float lse2 = a.lse[at];
     lse2 = lse2 == -__builtin_inff() ? 0.f : lse2 * kLog2e;
-    if (row < rows && hh == 0) {
+    if (row < rows && hh == 0 && blockIdx.y == 0) {
       a.lse2[at] = lse2;
       a.delta[at] = delta;
     }
@@ -160,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
       }
     };
     const TileReader<T, DP> rd(base);
-    if (tiles) stage(0);
-    for (int t = 0; t < tiles; ++t) {
+    if (t0 < tiles) stage(t0);
+    for (int t = t0; t < tiles; ++t) {
       wait_vm(0);
       lds_barrier();
       if (t + 1 < tiles) stage(t + 1);
@@ -196,6 +200,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
     }
   }
   if (row >= span) return;
+  if (a.part) {
+    const int64_t to = (blockIdx.y * a.q_rows + tile.seq.row0 + token) * a.H + head;
+    store_column<float, DP>(a.part + to * a.D, acc, a.scale, a.D);
+    return;
+  }
   store_column<T, DP>((T*)a.dq + (tile.seq.row0 + token) * a.dqs + (int64_t)head * a.D, acc,
                       a.scale, a.D);
 }
@@ -266,8 +275,10 @@ __global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 
   const int wave_last = k0 + wave * 32 + 31;
   const int low = first_of(k0 + wave * 32);                        // the wavefront's earliest row
   const int high = first_of(wave_last < nk ? wave_last : nk - 1);  // all its keys are seen from here
-  const int begin = k0 < nk ? first_of(k0) / C::ROWS : 0;
-  const int tiles = k0 < nk ? (rows + C::ROWS - 1) / C::ROWS : 0;
+  const int begin0 = k0 < nk ? first_of(k0) / C::ROWS : 0;
+  const int all = k0 < nk ? (rows + C::ROWS - 1) / C::ROWS : 0;
+  const int per = (all - begin0 + gridDim.y - 1) / gridDim.y;
+  const int begin = begin0 + blockIdx.y * per, tiles = begin + per < all ? begin + per : all;
 
   f32x16 dk[DP / 32], dv[DP / 32];
 #pragma unroll
@@ -371,30 +382,105 @@ __global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 
     for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = zero16();
   }
   const int64_t to = tile.seq.row0 + key;
+  if (a.part) {
+    float* p = a.part + ((blockIdx.y * a.k_rows + to) * a.G + g) * a.D;
+    if (set == C::SETS - 1) store_column<float, DP>(p, dk, a.scale, a.D);
+    if (set == 0)
+      store_column<float, DP>(p + gridDim.y * a.k_rows * a.G * a.D, dv, 1.f, a.D);
+    return;
+  }
   if (set == C::SETS - 1)
     store_column<T, DP>((T*)a.dk + to * a.dks + (int64_t)g * a.D, dk, a.scale, a.D);
   if (set == 0) store_column<T, DP>((T*)a.dv + to * a.dvs + (int64_t)g * a.D, dv, 1.f, a.D);
 }
 
+// The sum of a split walk's parts in their order, 4 elements a thread; the
+// second of two outputs where gridDim.y is 2.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) sum_kernel(const float* __restrict__ part, T* out0,
+                                                       T* out1, int64_t s0, int64_t s1, int64_t rows,
+                                                       int width, int parts) {
+  const int quads = width / 4;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= rows * quads) return;
+  const int64_t row = i / quads, e = i % quads * 4;
+  const float* p = part + (int64_t)blockIdx.y * parts * rows * width + row * width + e;
+  f32x4 sum = {};
+  for (int k = 0; k < parts; ++k) {
+    const f32x4 v = *(const f32x4*)(p + k * rows * width);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] += v[j];
+  }
+  const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+  store_row<T, 4>((blockIdx.y ? out1 + row * s1 : out0 + row * s0) + e, v);
+}
+
+template <typename T>
+hipError_t launch_sum(const float* part, T* out0, T* out1, int64_t s0, int64_t s1, int64_t rows,
+                      int width, int parts, hipStream_t s) {
+  const int64_t n = rows * (width / 4);
+  sum_kernel<T><<<dim3((unsigned)((n + kThreads - 1) / kThreads), out1 ? 2 : 1), kThreads, 0, s>>>(
+      part, out0, out1, s0, s1, rows, width, parts);
+  return hipGetLastError();
+}
+
+// Ranges that the walks are split into, with float32 parts: one (no parts)
+// where the tiles alone give half the device work, else as many as fill it, of
+// at least 4 steps each.
+struct Splits {
+  int dq, dkv;
+};
+int split_of(int64_t blocks, int64_t steps) {
+  int64_t n = blocks < 128 ? 256 / blocks : 1;
+  if (n > steps / 4) n = steps / 4;
+  if (n > 32) n = 32;
+  return n < 2 ? 1 : (int)n;
+}
+Splits splits_of(const AttentionDims& d) {
+  const int64_t rep = d.H / d.G, lq = d.qpacked ? d.Lq / d.B : d.Lq;
+  const int64_t lk = d.kpacked ? d.Lk / d.B : d.Lk;
+  const int64_t tile = d.bf16 ? DkvCfg<bf16, 64>::ROWS : DkvCfg<float, 64>::ROWS;
+  return {split_of(attention_blocks(d), lk / kKeys),
+          split_of(attention_key_blocks(d), lq * rep / tile)};
+}
+size_t part_bytes(const AttentionDims& d) {
+  const Splits n = splits_of(d);
+  const size_t q = n.dq > 1 ? (size_t)n.dq * d.q_rows() * d.H * d.D * 4 : 0;
+  const size_t kv = n.dkv > 1 ? (size_t)n.dkv * 2 * d.k_rows() * d.G * d.D * 4 : 0;
+  return q > kv ? q : kv;
+}
+
 template <typename F>
-hipError_t launch_lds(F kernel, int64_t blocks, int threads, int bytes, const BwdArgs& a,
-                      hipStream_t s) {
+hipError_t launch_lds(F kernel, int64_t blocks, int splits, int threads, int bytes,
+                      const BwdArgs& a, hipStream_t s) {
   const hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
-  kernel<<<(unsigned)blocks, threads, bytes, s>>>(a);
+  kernel<<<dim3((unsigned)blocks, splits), threads, bytes, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, int DP>
-hipError_t go(BwdArgs a, hipStream_t s) {
+hipError_t go(BwdArgs a, float* part, Splits n, hipStream_t s) {
   using C = DkvCfg<T, DP>;
   a.slots = tile_slots(a.qside, a.rep, kRows);
-  const hipError_t e = launch_lds(attention_dq_kernel<T, DP>, a.slots * a.G, kThreads,
-                                  4 * kKeys * TileCfg<T, DP>::ROWB, a, s);
+  a.part = n.dq > 1 ? part : nullptr;
+  hipError_t e = launch_lds(attention_dq_kernel<T, DP>, a.slots * a.G, n.dq, kThreads,
+                            4 * kKeys * TileCfg<T, DP>::ROWB, a, s);
   if (e != hipSuccess) return e;
+  if (a.part) {
+    e = launch_sum<T>(part, (T*)a.dq, nullptr, a.dqs, 0, a.q_rows, a.H * a.D, n.dq, s);
+    if (e != hipSuccess) return e;
+  }
   a.slots = tile_slots(a.kside, 1, kRows);
-  return launch_lds(attention_dkv_kernel<T, DP>, a.slots * a.G, C::THREADS, C::LDS, a, s);
+  a.part = n.dkv > 1 ? part : nullptr;
+  e = launch_lds(attention_dkv_kernel<T, DP>, a.slots * a.G, n.dkv, C::THREADS, C::LDS, a, s);
+  if (e != hipSuccess || !a.part) return e;
+  return launch_sum<T>(part, (T*)a.dk, (T*)a.dv, a.dks, a.dvs, a.k_rows, a.G * a.D, n.dkv, s);
+}
+
+size_t row_bytes(const AttentionDims& d) {
+  return ((size_t)d.q_rows() * d.H * 2 * sizeof(float) + 255) & ~(size_t)255;
 }
 
 }  // namespace
@@ -404,7 +490,7 @@ int64_t attention_key_blocks(const AttentionDims& d) {
 }
 
 size_t attention_backward_bytes(const AttentionDims& d) {
-  return (size_t)d.q_rows() * d.H * 2 * sizeof(float);
+  return row_bytes(d) + part_bytes(d);
 }
 
 hipError_t launch_attention_backward(const AttentionDims& d, const void* q, const void* k,
@@ -434,6 +520,8 @@ hipError_t launch_attention_backward(const AttentionDims& d, const void* q, cons
   a.dqs = d.dqs;
   a.dks = d.dks;
   a.dvs = d.dvs;
+  a.q_rows = d.q_rows();
+  a.k_rows = d.k_rows();
   a.H = (int)d.H;
   a.G = (int)d.G;
   a.rep = (int)(d.H / d.G);
@@ -444,8 +532,10 @@ hipError_t launch_attention_backward(const AttentionDims& d, const void* q, cons
   a.causal = d.causal;
   a.c = d.scale * kLog2e;
   a.scale = d.scale;
-  if (d.bf16) return d.D <= 64 ? go<bf16, 64>(a, s) : go<bf16, 128>(a, s);
-  return d.D <= 64 ? go<float, 64>(a, s) : go<float, 128>(a, s);
+  float* part = (float*)((char*)ws + row_bytes(d));
+  const Splits n = splits_of(d);
+  if (d.bf16) return d.D <= 64 ? go<bf16, 64>(a, part, n, s) : go<bf16, 128>(a, part, n, s);
+  return d.D <= 64 ? go<float, 64>(a, part, n, s) : go<float, 128>(a, part, n, s);
 }
 
 }  // namespace m2
