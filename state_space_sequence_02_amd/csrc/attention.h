@@ -288,6 +288,46 @@ struct TileReader {
   }
 };
 
+// A column's accumulators as a row of a tensor.
+template <typename T, int DP>
+__device__ __forceinline__ void store_column(T* row, const f32x16 (&acc)[DP / 32], float scale,
+                                             int D) {
+  const int hh = lane_id() >> 5;
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const int e = 32 * d + 2 * r + 4 * hh;
+      const float v[4] = {acc[d][r] * scale, acc[d][r + 1] * scale, acc[d][r + 2] * scale,
+                          acc[d][r + 3] * scale};
+      if (e < D) store_row<T, 4>(row + e, v);
+    }
+}
+
+// A wavefront's sums to LDS, and v = f0 v + f1 those of another.
+template <int N>
+__device__ __forceinline__ void put_sums(char* lds, int wave, const f32x16 (&v)[N]) {
+  f32x4* to = (f32x4*)lds + wave * (N * 4 * 64) + lane_id();
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      to[(d * 4 + r) * 64] = f32x4{v[d][4 * r], v[d][4 * r + 1], v[d][4 * r + 2], v[d][4 * r + 3]};
+}
+template <int N>
+__device__ __forceinline__ void add_scaled_sums(const char* lds, int wave, f32x16 (&v)[N], float f0,
+                                                float f1) {
+  const f32x4* from = (const f32x4*)lds + wave * (N * 4 * 64) + lane_id();
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const f32x4 x = from[(d * 4 + r) * 64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[d][4 * r + i] = f0 * v[d][4 * r + i] + f1 * x[i];
+    }
+}
+
 // The larger of a lane's value and its other half's.
 __device__ __forceinline__ float max_halves(float v) {
   const unsigned u = __builtin_bit_cast(unsigned, v);

@@ -10,6 +10,7 @@ namespace {
 constexpr int kRows = 128;  // packed rows of a workgroup: 4 wavefronts of 32
 constexpr int kKeys = 64;   // keys of a tile
 constexpr int kThreads = 256;
+constexpr int kMaxParts = 64;
 
 struct FwdArgs {
   const void *q, *k, *v;
@@ -23,12 +24,25 @@ struct FwdArgs {
   float c;  // scale * log2(e)
 };
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_kernel(FwdArgs a) {
+// SETS = 2: two sets of 4 wavefronts take every other tile and join at the
+// end, so that few rows walk their keys in half the time.
+template <typename T, int DP, int SETS>
+struct FwdCfg {
+  static constexpr int TILE = kKeys * TileCfg<T, DP>::ROWB;
+  static constexpr int BUF = 2 * SETS * TILE;  // K and V of a tile for each set
+  static constexpr int JOIN = SETS == 2 ? (4 * 32 * DP + 4 * 128) * 4 : 0;
+  static constexpr int LDS = 2 * BUF > JOIN ? 2 * BUF : JOIN;
+  static constexpr int WAVES_PER_SIMD = sizeof(T) == 2 || SETS == 2 ? 2 : 1;
+};
+
+template <typename T, int DP, int SETS>
+__global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES_PER_SIMD))
+    attention_kernel(FwdArgs a) {
   using K = TileCfg<T, DP>;
-  constexpr int TILE = kKeys * K::ROWB;
-  extern __shared__ __align__(16) char lds[];  // [2][K tile, V tile]
-  const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
+  using C = FwdCfg<T, DP, SETS>;
+  extern __shared__ __align__(16) char lds[];  // [2][SETS][K tile, V tile]
+  const int lane = lane_id(), wave = wave_id() & 3, set = wave_id() >> 2, hh = lane >> 5;
+  const int thread = threadIdx.x & (kThreads - 1);
   const int g = blockIdx.x % a.G;
   // causal rows at the end of a sequence see most keys: they go first
   const Tile tile = tile_of(a.qside, a.rep, kRows, a.slots - 1 - blockIdx.x / a.G);
@@ -64,8 +78,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_ke
                           a.D, q);
     const T* k = (const T*)a.k + ks.row0 * a.ks + (int64_t)g * a.D;
     const T* v = (const T*)a.v + ks.row0 * a.vs + (int64_t)g * a.D;
-    const uint32_t base = lds_addr(lds);
-    clear_ends<T, DP>(lds, 4 * kKeys, a.D, threadIdx.x, kThreads);
+    const uint32_t base = lds_addr(lds) + set * 2 * C::TILE;
+    clear_ends<T, DP>(lds, 4 * SETS * kKeys, a.D, threadIdx.x, kThreads * SETS);
     // the fewest and the most keys of this wavefront's rows
     int low = lim, high = lim;
 #pragma unroll
@@ -76,33 +90,57 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_ke
     low = __builtin_amdgcn_readfirstlane(low);
     high = __builtin_amdgcn_readfirstlane(high);
     using St = Stager<T, DP, kKeys, kThreads>;
-    const St ks_(a.ks, threadIdx.x), vs_(a.vs, threadIdx.x);
-    const auto stage = [&](int t) {
-      const uint32_t to = base + (t & 1) * 2 * TILE;
+    const St ks_(a.ks, thread), vs_(a.vs, thread);
+    const auto stage = [&](int t, int buf) {
+      const uint32_t to = base + buf * C::BUF;
       const int r0 = t * kKeys;
+      if (t >= t1) return;
       if (r0 + kKeys <= nk) {
-        ks_.load(to, k + r0 * a.ks, a.D, threadIdx.x);
-        vs_.load(to + TILE, v + r0 * a.vs, a.D, threadIdx.x);
+        ks_.load(to, k + r0 * a.ks, a.D, thread);
+        vs_.load(to + C::TILE, v + r0 * a.vs, a.D, thread);
       } else {
-        St::load_tail(to, k, a.ks, r0, nk, nullptr, a.D, threadIdx.x);
-        St::load_tail(to + TILE, v, a.vs, r0, nk, nullptr, a.D, threadIdx.x);
+        St::load_tail(to, k, a.ks, r0, nk, nullptr, a.D, thread);
+        St::load_tail(to + C::TILE, v, a.vs, r0, nk, nullptr, a.D, thread);
       }
     };
     const TileReader<T, DP> first(base);
-    stage(t0);
-    for (int t = t0; t < t1; ++t) {
+    stage(t0 + set, 0);
+    for (int t = t0, buf = 0; t < t1; t += SETS, buf ^= 1) {
       wait_vm(0);
-      lds_barrier();  // tile t is there, and every wavefront is done with tile t - 1
-      if (t + 1 < t1) stage(t + 1);
-      const int k0 = t * kKeys;
-      if (high > k0) {
-        const TileReader<T, DP> kr = first.later((t & 1) * 2 * TILE);
-        st.template step<kKeys / 32>(q, kr, kr.later(TILE), low < k0 + kKeys, lim - k0, a.c);
+      lds_barrier();  // tile t is there, and every wavefront is done with the one before
+      const int mine = t + set;
+      stage(mine + SETS, buf ^ 1);
+      const int k0 = mine * kKeys;
+      if (high > k0 && mine < t1) {
+        const TileReader<T, DP> kr = first.later(buf * C::BUF);
+        st.template step<kKeys / 32>(q, kr, kr.later(C::TILE), low < k0 + kKeys, lim - k0, a.c);
       }
     }
   }
 
-  const float l = st.l + __shfl_xor(st.l, 32);
+  float l = st.l + __shfl_xor(st.l, 32);
+  if constexpr (SETS == 2) {
+    if (t0 < t1) {  // the first set takes the second's sums
+      __syncthreads();
+      float* stats = (float*)lds + 4 * 32 * DP + wave * 128;
+      if (set == 1) {
+        put_sums(lds, wave, st.o);
+        stats[lane] = st.m;
+        stats[64 + lane] = l;
+      }
+      __syncthreads();
+      if (set == 0) {
+        const float m1 = stats[lane], l1 = stats[64 + lane];
+        const float top = __builtin_fmaxf(st.m, m1);
+        const float ref = top == -__builtin_inff() ? 0.f : top;
+        const float f0 = fast_exp2((st.m - ref) * a.c), f1 = fast_exp2((m1 - ref) * a.c);
+        l = l * f0 + l1 * f1;
+        st.m = top;
+        add_scaled_sums(lds, wave, st.o, f0, f1);
+      }
+    }
+    if (set == 1) return;
+  }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   if (row >= span) return;
   const int64_t at = (tile.seq.row0 + token) * a.H + head;
@@ -111,71 +149,64 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_ke
   if (a.part_o) {
     const int64_t p = (int64_t)blockIdx.y * a.q_rows * a.H + at;
     if (hh == 0) a.part_lse[p] = lse;
-    float* o = a.part_o + p * a.D;
-#pragma unroll
-    for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        const int e = 32 * d + 2 * r + 4 * hh;
-        const float v[4] = {st.o[d][r] * inv, st.o[d][r + 1] * inv, st.o[d][r + 2] * inv,
-                            st.o[d][r + 3] * inv};
-        if (e < a.D) store_row<float, 4>(o + e, v);
-      }
+    store_column<float, DP>(a.part_o + p * a.D, st.o, inv, a.D);
     return;
   }
   if (hh == 0) a.lse[at] = lse * kLn2;
-  T* o = (T*)a.o + at * a.D;
-#pragma unroll
-  for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      const int e = 32 * d + 2 * r + 4 * hh;
-      const float v[4] = {st.o[d][r] * inv, st.o[d][r + 1] * inv, st.o[d][r + 2] * inv,
-                          st.o[d][r + 3] * inv};
-      if (e < a.D) store_row<T, 4>(o + e, v);
-    }
+  store_column<T, DP>((T*)a.o + at * a.D, st.o, inv, a.D);
 }
 
-// Joins the parts of `rows` (token, head) rows: 32 lanes a row, 4 elements each.
+// Joins the parts of `rows` (token, head) rows: 32 lanes a row, 4 elements
+// each.  A lane weighs parts lane and lane + 32; rows without keys in a part
+// left zeros there.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) join_kernel(const float* __restrict__ part_o,
                                                         const float* __restrict__ part_lse,
                                                         T* __restrict__ o, float* __restrict__ lse,
                                                         int64_t rows, int D, int parts) {
   const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  const int e = threadIdx.x % 32 * 4;
+  const int lane = threadIdx.x % 32, e = lane * 4;
   if (row >= rows) return;
-  float top = -__builtin_inff();
-  for (int p = 0; p < parts; ++p) top = __builtin_fmaxf(top, part_lse[p * rows + row]);
-  const float base = top == -__builtin_inff() ? 0.f : top;
-  float sum = 0.f;
-  f32x4 acc = {};
-  for (int p = 0; p < parts; ++p) {
-    const float w = fast_exp2(part_lse[p * rows + row] - base);
-    sum += w;
-    if (e < D && w > 0.f) {
-      const f32x4 v = *(const f32x4*)(part_o + (p * rows + row) * D + e);
+  const float none = -__builtin_inff();
+  const float l0 = lane < parts ? part_lse[lane * rows + row] : none;
+  const float l1 = lane + 32 < parts ? part_lse[(lane + 32) * rows + row] : none;
+  float top = __builtin_fmaxf(l0, l1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+  for (int m = 1; m < 32; m *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, m, 32));
+  const float base = top == none ? 0.f : top;
+  const float w0 = fast_exp2(l0 - base), w1 = fast_exp2(l1 - base);
+  const float sum = lanes_sum<32>(w0 + w1);
+  f32x4 acc = {};
+  const int last = parts - 1;
+  const float* p = part_o + row * D + (e < D ? e : 0);
+  for (int k = 0; k < parts; k += 4) {
+    f32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *(const f32x4*)(p + min(k + i, last) * rows * D);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float w = __shfl(k + i < 32 ? w0 : w1, (k + i) & 31, 32);
+      if (k + i > last) w = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = __builtin_fmaf(w, v[i][j], acc[j]);
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (lse && e == 0)
-    lse[row] = sum > 0.f ? (base + __builtin_amdgcn_logf(sum)) * kLn2 : -__builtin_inff();
+  if (lse && lane == 0) lse[row] = sum > 0.f ? (base + __builtin_amdgcn_logf(sum)) * kLn2 : none;
   if (e < D) {
     const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
     store_row<T, 4>(o + row * D + e, v);
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int SETS>
 hipError_t go(const FwdArgs& a, hipStream_t s) {
-  constexpr int bytes = 4 * kKeys * TileCfg<T, DP>::ROWB;
-  const auto kernel = attention_kernel<T, DP>;
+  constexpr int bytes = FwdCfg<T, DP, SETS>::LDS;
+  const auto kernel = attention_kernel<T, DP, SETS>;
   const hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
-  kernel<<<dim3((unsigned)(a.slots * a.G), a.splits), kThreads, bytes, s>>>(a);
+  kernel<<<dim3((unsigned)(a.slots * a.G), a.splits), kThreads * SETS, bytes, s>>>(a);
   return hipGetLastError();
 }
 
@@ -184,17 +215,25 @@ Side query_side(const AttentionDims& d, const int32_t* seqs) {
 }
 Side key_side(const AttentionDims& d, const int32_t* seqs) { return {seqs, d.Lk, d.B, d.kpacked}; }
 
-// Parts that the keys are split into: one where the rows alone fill the
-// device, else as many as do, but at least 4 tiles of keys for each.
-int splits_of(const AttentionDims& d) {
+// Where the rows give no two workgroups for each CU: two sets in each (float32
+// heads above 64 do not fit twice), and the keys split into as many parts as
+// fill the device, of at least 4 tiles for each set (float32, whose products
+// take 16 times as long: one).
+struct Plan {
+  int sets, splits;
+};
+Plan plan_of(const AttentionDims& d) {
   const int64_t blocks = tile_slots(query_side(d, nullptr), d.H / d.G, kRows) * d.G;
+  if (blocks > 256) return {1, 1};
+  const int sets = d.bf16 || d.D <= 64 ? 2 : 1;
   const int64_t keys = d.kpacked ? d.Lk / d.B : d.Lk;
-  const int64_t most = keys / (4 * kKeys);
-  int64_t n = 512 / blocks;
+  const int64_t most = keys / ((d.bf16 ? 4 : 1) * sets * kKeys);
+  int64_t n = 256 / blocks;
   if (n > most) n = most;
-  if (n > 64) n = 64;
-  return n < 2 ? 1 : (int)n;
+  if (n > kMaxParts / 2) n = kMaxParts / 2;
+  return {sets, n < 2 ? 1 : (int)n};
 }
+int splits_of(const AttentionDims& d) { return plan_of(d).splits; }
 
 }  // namespace
 
@@ -249,8 +288,13 @@ FwdArgs args_of(const AttentionDims& d, const void* q, const void* k, const void
 }
 
 hipError_t run(const AttentionDims& d, const FwdArgs& a, hipStream_t s) {
-  if (d.bf16) return d.D <= 64 ? go<bf16, 64>(a, s) : go<bf16, 128>(a, s);
-  return d.D <= 64 ? go<float, 64>(a, s) : go<float, 128>(a, s);
+  const bool narrow = d.D <= 64;
+  if (plan_of(d).sets == 2) {
+    if (d.bf16) return narrow ? go<bf16, 64, 2>(a, s) : go<bf16, 128, 2>(a, s);
+    return go<float, 64, 2>(a, s);
+  }
+  if (d.bf16) return narrow ? go<bf16, 64, 1>(a, s) : go<bf16, 128, 1>(a, s);
+  return narrow ? go<float, 64, 1>(a, s) : go<float, 128, 1>(a, s);
 }
 
 }  // namespace

@@ -67,22 +67,6 @@ __device__ __forceinline__ void dma4(const void* src, uint32_t lds_base) {
   asm volatile("global_load_lds_dword %0, off" : : "v"(src), "{m0}"(m0) : "memory");
 }
 
-// A column's accumulators as a row of a tensor.
-template <typename T, int DP>
-__device__ __forceinline__ void store_column(T* row, const f32x16 (&acc)[DP / 32], float scale,
-                                             int D) {
-  const int hh = lane_id() >> 5;
-#pragma unroll
-  for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      const int e = 32 * d + 2 * r + 4 * hh;
-      const float v[4] = {acc[d][r] * scale, acc[d][r + 1] * scale, acc[d][r + 2] * scale,
-                          acc[d][r + 3] * scale};
-      if (e < D) store_row<T, 4>(row + e, v);
-    }
-}
-
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq_kernel(BwdArgs a) {
   using K = TileCfg<T, DP>;
@@ -227,29 +211,6 @@ struct DkvCfg {
   static constexpr int LDS = 2 * BUF > JOIN ? 2 * BUF : JOIN;
 };
 
-// A wavefront's sums to and from LDS.
-template <int N>
-__device__ __forceinline__ void put(char* lds, int wave, const f32x16 (&v)[N]) {
-  f32x4* to = (f32x4*)lds + wave * (N * 4 * 64) + lane_id();
-#pragma unroll
-  for (int d = 0; d < N; ++d)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      to[(d * 4 + r) * 64] = f32x4{v[d][4 * r], v[d][4 * r + 1], v[d][4 * r + 2], v[d][4 * r + 3]};
-}
-template <int N>
-__device__ __forceinline__ void add(const char* lds, int wave, f32x16 (&v)[N]) {
-  const f32x4* from = (const f32x4*)lds + wave * (N * 4 * 64) + lane_id();
-#pragma unroll
-  for (int d = 0; d < N; ++d)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const f32x4 x = from[(d * 4 + r) * 64];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[d][4 * r + i] += x[i];
-    }
-}
-
 template <typename T, int DP>
 __global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 : 1))
     attention_dkv_kernel(BwdArgs a) {
@@ -367,13 +328,13 @@ __global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 
   if constexpr (C::SETS == 2) {
     if (begin < tiles) {  // the first set takes dV, the second dK
       __syncthreads();
-      if (set == 1) put(lds, wave, dv);
+      if (set == 1) put_sums(lds, wave, dv);
       __syncthreads();
-      if (set == 0) add(lds, wave, dv);
+      if (set == 0) add_scaled_sums(lds, wave, dv, 1.f, 1.f);
       __syncthreads();
-      if (set == 0) put(lds, wave, dk);
+      if (set == 0) put_sums(lds, wave, dk);
       __syncthreads();
-      if (set == 1) add(lds, wave, dk);
+      if (set == 1) add_scaled_sums(lds, wave, dk, 1.f, 1.f);
     }
   }
   if (key >= tile.seq.span) return;

@@ -178,7 +178,7 @@ int splits_of(const AttentionStepDims& d) {
   const int64_t most = (d.rows + 255) / 256;
   int64_t n = 512 / blocks;
   if (n > most) n = most;
-  if (n > 64) n = 64;
+  if (n > 32) n = 32;
   return n < 2 ? 1 : (int)n;
 }
 
