@@ -96,8 +96,8 @@ __device__ __forceinline__ int64_t cut_of(const Side& s, int64_t i) {
 __device__ __forceinline__ Tile tile_of(const Side& s, int64_t rep, int64_t tile, int64_t slot) {
   Tile t;
   if (!s.packed) {
-    const int64_t i = slot / s.B;
-    t.b = slot - i * s.B;
+    const uint32_t i = (uint32_t)slot / (uint32_t)s.B;  // slots < 2^24
+    t.b = (uint32_t)slot - i * (uint32_t)s.B;
     t.r0 = i * tile;
     t.seq = seq_of(s, t.b);
     return t;
@@ -218,6 +218,15 @@ __device__ __forceinline__ row_frag<T> acc_frag(const f32x16& p, int s) {
   }
 }
 
+// Holds a value's computation where it is written (the compiler would move it
+// behind a branch, next to its use).
+__device__ __forceinline__ void pin(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void pin(bf16x8& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void pin(f32v8& f) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) pin(f.v[j]);
+}
+
 __device__ __forceinline__ f32x16 mma_rows(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -255,10 +264,13 @@ struct TileReader {
     return *(lds_ptr)(a + offset);
   }
   // The same reads of a tile that begins `bytes` (multiples of a row) later.
+  // The empty asm keeps the few addresses behind it from being held in
+  // registers across a loop's steps.
   __device__ __forceinline__ TileReader later(uint32_t bytes) const {
     TileReader r = *this;
     r.row += bytes;
     r.col += bytes;
+    asm volatile("" : "+v"(r.row), "+v"(r.col));
     return r;
   }
   // Rows r32 .. r32 + 31 at step s along the head; `offset`: bytes from the
@@ -398,6 +410,7 @@ struct Stager {
   __device__ __forceinline__ static void load_tail(uint32_t lds, const T* base, int64_t stride,
                                                    int r0, int n, const T* last, int D,
                                                    int thread) {
+    asm volatile("" : "+v"(thread));  // rare: nothing of it is kept in registers
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int c = chunk_of(i, thread), r = r0 + row_of(i, thread);

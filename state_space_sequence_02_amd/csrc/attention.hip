@@ -68,7 +68,7 @@ __global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES
   const int per = (tiles + a.splits - 1) / a.splits;
   const int t0 = blockIdx.y * per, t1 = t0 + per < tiles ? t0 + per : tiles;
 
-  RowState<T, DP> st;
+  RowState<T, DP, kKeys / 32> st;
   st.clear();
   if (t0 < t1) {
     head_frag<T> q[K::STEPS];
@@ -80,41 +80,65 @@ __global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES
     const T* v = (const T*)a.v + ks.row0 * a.vs + (int64_t)g * a.D;
     const uint32_t base = lds_addr(lds) + set * 2 * C::TILE;
     clear_ends<T, DP>(lds, 4 * SETS * kKeys, a.D, threadIdx.x, kThreads * SETS);
-    // the fewest and the most keys of this wavefront's rows
-    int low = lim, high = lim;
+    int low = lim;  // the fewest keys of this wavefront's rows
 #pragma unroll
-    for (int m = 1; m < 32; m *= 2) {
-      low = min(low, __shfl_xor(low, m));
-      high = max(high, __shfl_xor(high, m));
-    }
-    low = __builtin_amdgcn_readfirstlane(low);
-    high = __builtin_amdgcn_readfirstlane(high);
+    for (int m = 1; m < 32; m *= 2) low = min(low, __shfl_xor(low, m));
+    low = min(__builtin_amdgcn_readfirstlane(low), t1 * kKeys);
     using St = Stager<T, DP, kKeys, kThreads>;
     const St ks_(a.ks, thread), vs_(a.vs, thread);
-    const auto stage = [&](int t, int buf) {
-      const uint32_t to = base + buf * C::BUF;
-      const int r0 = t * kKeys;
-      if (t >= t1) return;
-      if (r0 + kKeys <= nk) {
-        ks_.load(to, k + r0 * a.ks, a.D, thread);
-        vs_.load(to + C::TILE, v + r0 * a.vs, a.D, thread);
-      } else {
-        St::load_tail(to, k, a.ks, r0, nk, nullptr, a.D, thread);
-        St::load_tail(to + C::TILE, v, a.vs, r0, nk, nullptr, a.D, thread);
-      }
+    const int steps = (t1 - t0 + SETS - 1) / SETS;
+    // the last set may have no tile in its last step: keys that no row sees
+    const int end = min(lim, t1 * kKeys);
+    const auto tile_at = [&](int i) { return (t0 + i * SETS + set) * kKeys; };
+    const auto load = [&](const T* x, int64_t stride, const St& st_, uint32_t to, int i) {
+      const int r0 = tile_at(i);
+      if (r0 + kKeys <= nk)
+        st_.load(to, x + r0 * stride, a.D, thread);
+      else
+        St::load_tail(to, x, stride, r0, nk, nullptr, a.D, thread);
     };
-    const TileReader<T, DP> first(base);
-    stage(t0 + set, 0);
-    for (int t = t0, buf = 0; t < t1; t += SETS, buf ^= 1) {
+    const TileReader<T, DP> kr(base), vr = kr.later(C::TILE);
+    const float slack = 8.f / a.c;
+    using State = RowState<T, DP, kKeys / 32>;
+    typename State::Scores s0, s1;
+    load(k, a.ks, ks_, base, 0);
+    wait_vm(0);
+    lds_barrier();
+    if (steps > 1) load(k, a.ks, ks_, base + C::BUF, 1);
+    load(v, a.vs, vs_, base + C::TILE, 0);
+    State::scores(q, kr, s0);
+    if (low < tile_at(0) + kKeys) State::mask(s0, end - tile_at(0));
+    st.raise(State::top(s0), slack, a.c);
+    const auto arrive = [&](int i, int buf) {
       wait_vm(0);
-      lds_barrier();  // tile t is there, and every wavefront is done with the one before
-      const int mine = t + set;
-      stage(mine + SETS, buf ^ 1);
-      const int k0 = mine * kKeys;
-      if (high > k0 && mine < t1) {
-        const TileReader<T, DP> kr = first.later(buf * C::BUF);
-        st.template step<kKeys / 32>(q, kr, kr.later(C::TILE), low < k0 + kKeys, lim - k0, a.c);
-      }
+      lds_barrier();  // K of step i + 1 and V of step i are there, and none is read any more
+      if (i + 2 < steps) load(k, a.ks, ks_, base + buf, i + 2);
+      if (i + 1 < steps) load(v, a.vs, vs_, base + C::TILE + (C::BUF - buf), i + 1);
+    };
+    // Step i: the next tile's scores beside this tile's exponentials, then this
+    // tile's values beside the next one's maximum.
+    const auto step = [&](typename State::Scores& s, typename State::Scores& next, int i, int buf) {
+      typename State::Weights p;
+      arrive(i, buf);
+      st.scores_and_weigh(q, kr.later(C::BUF - buf), next, s, a.c, p);
+      if (low < tile_at(i + 1) + kKeys) State::mask(next, end - tile_at(i + 1));
+      st.raise(st.take_and_top(vr.later(buf), p, next), slack, a.c);
+    };
+    int i = 0;
+    for (; i + 2 < steps; i += 2) {
+      step(s0, s1, i, 0);
+      step(s1, s0, i + 1, C::BUF);
+    }
+    typename State::Weights p;
+    if (i + 1 < steps) {
+      step(s0, s1, i, 0);
+      arrive(i + 1, C::BUF);
+      st.weigh(s1, a.c, p);
+      st.take(vr.later(C::BUF), p);
+    } else {
+      arrive(i, 0);
+      st.weigh(s0, a.c, p);
+      st.take(vr.later(0), p);
     }
   }
 

@@ -66,7 +66,8 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_ke
   const int t0 = blockIdx.y * per, t1 = t0 + per < tiles ? t0 + per : tiles;
   char* mine = lds + wave * 4 * TILE;
   const uint32_t base = lds_addr(mine);
-  RowState<T, DP> st;
+  using State = RowState<T, DP, 1>;
+  State st;
   st.clear();
   if (t0 + wave < t1) {
     head_frag<T> q[K::STEPS];
@@ -98,7 +99,13 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_ke
       }
       asm volatile("" ::: "memory");
       const TileReader<T, DP> kr = first.later(buf * 2 * TILE);
-      st.template step<1>(q, kr, kr.later(TILE), t * 32 + 32 > nk, nk - t * 32, a.c);
+      typename State::Scores s;
+      typename State::Weights p;
+      State::scores(q, kr, s);
+      if (t * 32 + 32 > nk) State::mask(s, nk - t * 32);
+      st.raise(State::top(s), 8.f / a.c, a.c);
+      st.weigh(s, a.c, p);
+      st.take(kr.later(TILE), p);
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       asm volatile("" ::: "memory");
     }
