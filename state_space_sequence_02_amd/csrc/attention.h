@@ -41,9 +41,9 @@ struct Side {
 };
 
 struct Seq {
-  int64_t row0;  // its first row in the tensor
-  int64_t span;  // rows of the tensor that are its own, padding among them
-  int64_t n;     // tokens
+  int row0;  // its first row in the tensor
+  int span;  // rows of the tensor that are its own, padding among them
+  int n;     // tokens
 };
 
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t hi) {
@@ -56,22 +56,20 @@ __device__ __forceinline__ int uniform_at(const int32_t* p, int64_t i) {
 }
 
 __device__ __forceinline__ Seq seq_of(const Side& s, int64_t b) {
+  const int len = (int)s.len;
   Seq q;
   if (!s.packed) {
-    q.row0 = b * s.len;
-    q.span = s.len;
-    q.n = s.seqs ? clamp64(uniform_at(s.seqs, b), s.len) : s.len;
+    q.row0 = (int)b * len;
+    q.span = len;
+    q.n = s.seqs ? min(max(uniform_at(s.seqs, b), 0), len) : len;
   } else {
-    q.row0 = clamp64(uniform_at(s.seqs, b), s.len);
-    q.n = clamp64(uniform_at(s.seqs, b + 1), s.len) - q.row0;
-    if (q.n < 0) q.n = 0;
-    q.span = q.n;
+    q.row0 = min(max(uniform_at(s.seqs, b), 0), len);
+    q.span = q.n = max(min(uniform_at(s.seqs, b + 1), len) - q.row0, 0);
   }
   return q;
 }
 
-// A tile of `tile` packed rows.  Padded: tile-major over the sequences.
-// Packed: between and behind the sequences there are rows that belong to
+// A tile of `tile` packed rows.  Packed: between and behind the sequences there are rows that belong to
 // none, so the tensor is cut at 0, starts[0 .. B], len: B + 2 pieces of which
 // the first and the last hold no tokens.  Piece i takes the slots from
 // floor(cut_i rep / tile) + i on: the next piece's first slot is at least as
@@ -79,8 +77,8 @@ __device__ __forceinline__ Seq seq_of(const Side& s, int64_t b) {
 // from the sizes alone (no list is made, nothing is copied to the host).
 struct Tile {
   Seq seq;
-  int64_t b;   // sequence; -1: rows of none
-  int64_t r0;  // first packed row
+  int b;   // sequence; -1: rows of none
+  int r0;  // first packed row
 };
 
 inline int64_t tile_slots(const Side& s, int64_t rep, int64_t tile) {
@@ -91,41 +89,84 @@ __device__ __forceinline__ int64_t cut_of(const Side& s, int64_t i) {
   return i == 0 ? 0 : i > s.B + 1 ? s.len : clamp64(s.seqs[i - 1], s.len);
 }
 
-// The tile of a slot, the same for all lanes.  A wavefront's lanes look at 64
-// pieces at once.
-__device__ __forceinline__ Tile tile_of(const Side& s, int64_t rep, int64_t tile, int64_t slot) {
+__device__ __forceinline__ Tile piece_tile(const Side& s, int piece, int cut, int next, int r0) {
   Tile t;
+  t.r0 = __builtin_amdgcn_readfirstlane(r0);
+  t.b = __builtin_amdgcn_readfirstlane(piece) - 1;
+  t.seq.row0 = __builtin_amdgcn_readfirstlane(cut);
+  t.seq.span = max(__builtin_amdgcn_readfirstlane(next) - t.seq.row0, 0);
+  t.seq.n = t.seq.span;
+  if (t.b == (int)s.B) t.b = -1;
+  if (t.b < 0) t.seq.n = 0;
+  return t;
+}
+
+// The tile that workgroup `slot` takes, the same for all lanes; a tile behind
+// its sequence's end is none.  In causal attention a tile's work grows with
+// its number in the sequence (queries; of keys, with its number from the
+// end): the longest walks have to begin first, or the last of them runs on
+// alone.  Padded sequences are gone through tile number by tile number,
+// longest walks first.  So are packed ones while their pieces fit a
+// wavefront's lanes: F(i) = the tiles that are at least number i is a sum over
+// the lanes, workgroup n has the number i with F(i + 1) <= n < F(i), and takes
+// the (n - F(i + 1))-th piece that is so long.  With more sequences than that
+// no single one holds much of the work; they are taken as they lie.
+template <bool KEYS>
+__device__ __forceinline__ Tile tile_of(const Side& s, int rep, int tile, int slots, int slot) {
+  const int B = (int)s.B;
   if (!s.packed) {
-    const uint32_t i = (uint32_t)slot / (uint32_t)s.B;  // slots < 2^24
-    t.b = (uint32_t)slot - i * (uint32_t)s.B;
+    const uint32_t n = KEYS ? slot : slots - 1 - slot;
+    const uint32_t i = n / (uint32_t)B;
+    Tile t;
+    t.b = n - i * B;
     t.r0 = i * tile;
     t.seq = seq_of(s, t.b);
     return t;
   }
-  int64_t lo = 0, count = s.B + 2;
+  const int lane = lane_id();
+  const int pieces = B + 2;
+  if (pieces <= 64) {
+    const int cut = (int)cut_of(s, lane), next = (int)cut_of(s, lane + 1);
+    int have = 0;
+    if (lane < pieces && next > cut) have = (int)(((int64_t)(next - cut) * rep + tile - 1) / tile);
+    // sums of counts below 2^24 are exact in float32
+    const auto f = [&](int i) {
+      return __builtin_amdgcn_readfirstlane((int)lanes_sum<64>((float)max(have - i, 0)));
+    };
+    int lo = 0, hi = have;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) hi = max(hi, __shfl_xor(hi, m));
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    if (slot >= f(0)) return piece_tile(s, 0, 0, 0, 0);
+    while (hi - lo > 1) {  // F(lo) > slot >= F(hi)
+      const int mid = (lo + hi) / 2;
+      if (f(mid) > slot)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    uint64_t mask = __ballot(have > lo);
+    for (int k = slot - f(lo + 1); k > 0; --k) mask &= mask - 1;
+    const int p = __builtin_ctzll(mask);
+    return piece_tile(s, p, __builtin_amdgcn_readlane(cut, p), __builtin_amdgcn_readlane(next, p),
+                      (KEYS ? __builtin_amdgcn_readlane(have, p) - 1 - lo : lo) * tile);
+  }
+  // 64 pieces at once
+  int lo = 0, count = pieces;
   while (count > 1) {
-    const int64_t step = (count + 63) / 64;
-    const int64_t i = lo + lane_id() * step;
+    const int step = (count + 63) / 64;
+    const int i = lo + lane * step;
     const bool at = i < lo + count && cut_of(s, i) * rep / tile + i <= slot;
     const uint64_t mask = __ballot(at);
     const int last = mask ? 63 - __builtin_clzll(mask) : 0;
-    const int64_t left = count - last * step;
+    const int left = count - last * step;
     lo += last * step;
     count = left < step ? left : step;
   }
-  const int64_t i = __builtin_amdgcn_readfirstlane((int)lo);
-  const int64_t cut = __builtin_amdgcn_readfirstlane((int)cut_of(s, i));
-  t.r0 = (slot - (cut * rep / tile + i)) * tile;
-  t.b = i - 1;
-  t.seq.row0 = cut;
-  t.seq.span = __builtin_amdgcn_readfirstlane((int)cut_of(s, i + 1)) - cut;
-  if (t.seq.span < 0) t.seq.span = 0;
-  t.seq.n = t.seq.span;
-  if (i == 0 || i == s.B + 1) {
-    t.b = -1;
-    t.seq.n = 0;
-  }
-  return t;
+  const int i = __builtin_amdgcn_readfirstlane(lo);
+  const int64_t cut = cut_of(s, i);
+  return piece_tile(s, i, (int)cut, (int)cut_of(s, i + 1),
+                    (int)((slot - (cut * rep / tile + i)) * tile));
 }
 
 // ------------------------------------------------------------------ LDS tiles
@@ -264,12 +305,16 @@ struct TileReader {
     return *(lds_ptr)(a + offset);
   }
   // The same reads of a tile that begins `bytes` (multiples of a row) later.
-  // The empty asm keeps the few addresses behind it from being held in
-  // registers across a loop's steps.
   __device__ __forceinline__ TileReader later(uint32_t bytes) const {
     TileReader r = *this;
     r.row += bytes;
     r.col += bytes;
+    return r;
+  }
+  // The same, where `bytes` is a constant of an unrolled step: the empty asm
+  // keeps the addresses from being held in registers across the steps.
+  __device__ __forceinline__ TileReader fresh(uint32_t bytes) const {
+    TileReader r = later(bytes);
     asm volatile("" : "+v"(r.row), "+v"(r.col));
     return r;
   }

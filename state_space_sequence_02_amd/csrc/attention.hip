@@ -44,16 +44,15 @@ __global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES
   const int lane = lane_id(), wave = wave_id() & 3, set = wave_id() >> 2, hh = lane >> 5;
   const int thread = threadIdx.x & (kThreads - 1);
   const int g = blockIdx.x % a.G;
-  // causal rows at the end of a sequence see most keys: they go first
-  const Tile tile = tile_of(a.qside, a.rep, kRows, a.slots - 1 - blockIdx.x / a.G);
-  const int64_t span = tile.seq.span * a.rep;
+  const Tile tile = tile_of<false>(a.qside, a.rep, kRows, (int)a.slots, blockIdx.x / a.G);
+  const int span = tile.seq.span * a.rep;
   if (tile.r0 >= span) return;
-  const int nq = (int)tile.seq.n, rows = nq * a.rep;
+  const int nq = tile.seq.n, rows = nq * a.rep;
   Seq ks = {0, 0, 0};
   if (tile.b >= 0) ks = seq_of(a.kside, tile.b);
-  const int nk = (int)ks.n;
+  const int nk = ks.n;
 
-  const int row = (int)tile.r0 + wave * 32 + (lane & 31);
+  const int row = tile.r0 + wave * 32 + (lane & 31);
   const int token = row / a.rep;
   const int head = g * a.rep + row % a.rep;
   // keys that a row sees; none for rows behind the sequence
@@ -62,7 +61,7 @@ __global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES
     return a.causal ? (int)clamp64(n, nk) : nk;
   };
   const int lim = row < rows ? seen(token) : 0;
-  const int last = (int)(tile.r0 + kRows < rows ? tile.r0 + kRows : rows) - 1;
+  const int last = min(tile.r0 + kRows, rows) - 1;
   const int most = last >= tile.r0 ? seen(last / a.rep) : 0;  // of the workgroup's rows
   const int tiles = (most + kKeys - 1) / kKeys;
   const int per = (tiles + a.splits - 1) / a.splits;
@@ -76,8 +75,8 @@ __global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES
     load_row_frags<T, DP>((const T*)a.q + (tile.seq.row0 + safe / a.rep) * a.qs +
                               (int64_t)(g * a.rep + safe % a.rep) * a.D,
                           a.D, q);
-    const T* k = (const T*)a.k + ks.row0 * a.ks + (int64_t)g * a.D;
-    const T* v = (const T*)a.v + ks.row0 * a.vs + (int64_t)g * a.D;
+    const T* k = (const T*)a.k + (int64_t)ks.row0 * a.ks + (int64_t)g * a.D;
+    const T* v = (const T*)a.v + (int64_t)ks.row0 * a.vs + (int64_t)g * a.D;
     const uint32_t base = lds_addr(lds) + set * 2 * C::TILE;
     clear_ends<T, DP>(lds, 4 * SETS * kKeys, a.D, threadIdx.x, kThreads * SETS);
     int low = lim;  // the fewest keys of this wavefront's rows
@@ -100,45 +99,67 @@ __global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES
     const TileReader<T, DP> kr(base), vr = kr.later(C::TILE);
     const float slack = 8.f / a.c;
     using State = RowState<T, DP, kKeys / 32>;
-    typename State::Scores s0, s1;
-    load(k, a.ks, ks_, base, 0);
-    wait_vm(0);
-    lds_barrier();
-    if (steps > 1) load(k, a.ks, ks_, base + C::BUF, 1);
-    load(v, a.vs, vs_, base + C::TILE, 0);
-    State::scores(q, kr, s0);
-    if (low < tile_at(0) + kKeys) State::mask(s0, end - tile_at(0));
-    st.raise(State::top(s0), slack, a.c);
-    const auto arrive = [&](int i, int buf) {
-      wait_vm(0);
-      lds_barrier();  // K of step i + 1 and V of step i are there, and none is read any more
-      if (i + 2 < steps) load(k, a.ks, ks_, base + buf, i + 2);
-      if (i + 1 < steps) load(v, a.vs, vs_, base + C::TILE + (C::BUF - buf), i + 1);
-    };
-    // Step i: the next tile's scores beside this tile's exponentials, then this
-    // tile's values beside the next one's maximum.
-    const auto step = [&](typename State::Scores& s, typename State::Scores& next, int i, int buf) {
-      typename State::Weights p;
-      arrive(i, buf);
-      st.scores_and_weigh(q, kr.later(C::BUF - buf), next, s, a.c, p);
-      if (low < tile_at(i + 1) + kKeys) State::mask(next, end - tile_at(i + 1));
-      st.raise(st.take_and_top(vr.later(buf), p, next), slack, a.c);
-    };
-    int i = 0;
-    for (; i + 2 < steps; i += 2) {
-      step(s0, s1, i, 0);
-      step(s1, s0, i + 1, C::BUF);
-    }
-    typename State::Weights p;
-    if (i + 1 < steps) {
-      step(s0, s1, i, 0);
-      arrive(i + 1, C::BUF);
-      st.weigh(s1, a.c, p);
-      st.take(vr.later(C::BUF), p);
+    typename State::Scores s0, s1;  // s1: the next tile's
+    if constexpr (sizeof(T) == 4) {
+      // Products in float32 take 16 times as long as in bfloat16: nothing to
+      // put beside them matters.
+      load(k, a.ks, ks_, base, 0);
+      load(v, a.vs, vs_, base + C::TILE, 0);
+      for (int i = 0; i < steps; ++i) {
+        const int buf = (i & 1) * C::BUF;
+        wait_vm(0);
+        lds_barrier();  // tile i is there, and tile i - 1 is not read any more
+        if (i + 1 < steps) {
+          load(k, a.ks, ks_, base + (C::BUF - buf), i + 1);
+          load(v, a.vs, vs_, base + C::TILE + (C::BUF - buf), i + 1);
+        }
+        typename State::Weights p;
+        State::scores(q, kr.later(buf), s0);
+        if (low < tile_at(i) + kKeys) State::mask(s0, end - tile_at(i));
+        st.raise(State::top(s0), slack, a.c);
+        st.weigh(s0, a.c, p);
+        st.take(vr.later(buf), p);
+      }
     } else {
-      arrive(i, 0);
-      st.weigh(s0, a.c, p);
-      st.take(vr.later(0), p);
+      load(k, a.ks, ks_, base, 0);
+      wait_vm(0);
+      lds_barrier();
+      if (steps > 1) load(k, a.ks, ks_, base + C::BUF, 1);
+      load(v, a.vs, vs_, base + C::TILE, 0);
+      State::scores(q, kr, s0);
+      if (low < tile_at(0) + kKeys) State::mask(s0, end - tile_at(0));
+      st.raise(State::top(s0), slack, a.c);
+      const auto arrive = [&](int i, int buf) {
+        wait_vm(0);
+        lds_barrier();  // K of step i + 1 and V of step i are there, and none is read any more
+        if (i + 2 < steps) load(k, a.ks, ks_, base + buf, i + 2);
+        if (i + 1 < steps) load(v, a.vs, vs_, base + C::TILE + (C::BUF - buf), i + 1);
+      };
+      // Step i: the next tile's scores beside this tile's exponentials, then this
+      // tile's values beside the next one's maximum.
+      const auto step = [&](typename State::Scores& s, typename State::Scores& next, int i, int buf) {
+        typename State::Weights p;
+        arrive(i, buf);
+        st.scores_and_weigh(q, kr.fresh(C::BUF - buf), next, s, a.c, p);
+        if (low < tile_at(i + 1) + kKeys) State::mask(next, end - tile_at(i + 1));
+        st.raise(st.take_and_top(vr.fresh(buf), p, next), slack, a.c);
+      };
+      int i = 0;
+      for (; i + 2 < steps; i += 2) {
+        step(s0, s1, i, 0);
+        step(s1, s0, i + 1, C::BUF);
+      }
+      typename State::Weights p;
+      if (i + 1 < steps) {
+        step(s0, s1, i, 0);
+        arrive(i + 1, C::BUF);
+        st.weigh(s1, a.c, p);
+        st.take(vr.fresh(C::BUF), p);
+      } else {
+        arrive(i, 0);
+        st.weigh(s0, a.c, p);
+        st.take(vr.fresh(0), p);
+      }
     }
   }
 
@@ -167,7 +188,7 @@ __global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   if (row >= span) return;
-  const int64_t at = (tile.seq.row0 + token) * a.H + head;
+  const int64_t at = (int64_t)(tile.seq.row0 + token) * a.H + head;
   // log2 units until the end
   const float lse = l > 0.f ? st.m * a.c + __builtin_amdgcn_logf(l) : -__builtin_inff();
   if (a.part_o) {

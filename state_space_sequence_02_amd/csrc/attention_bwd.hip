@@ -74,14 +74,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
   extern __shared__ __align__(16) char lds[];
   const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
   const int g = blockIdx.x % a.G;
-  const Tile tile = tile_of(a.qside, a.rep, kRows, a.slots - 1 - blockIdx.x / a.G);
-  const int64_t span = tile.seq.span * a.rep;
+  const Tile tile = tile_of<false>(a.qside, a.rep, kRows, (int)a.slots, blockIdx.x / a.G);
+  const int span = tile.seq.span * a.rep;
   if (tile.r0 >= span) return;
-  const int nq = (int)tile.seq.n, rows = nq * a.rep;
+  const int nq = tile.seq.n, rows = nq * a.rep;
   Seq ks = {0, 0, 0};
   if (tile.b >= 0) ks = seq_of(a.kside, tile.b);
-  const int nk = (int)ks.n;
-  const int row = (int)tile.r0 + wave * 32 + (lane & 31);
+  const int nk = ks.n;
+  const int row = tile.r0 + wave * 32 + (lane & 31);
   const int token = row / a.rep;
   const int head = g * a.rep + row % a.rep;
   const auto seen = [&](int tok) {
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
     return a.causal ? (int)clamp64(n, nk) : nk;
   };
   const int lim = row < rows ? seen(token) : 0;
-  const int last = (int)(tile.r0 + kRows < rows ? tile.r0 + kRows : rows) - 1;
+  const int last = min(tile.r0 + kRows, rows) - 1;
   const int most = last >= tile.r0 ? seen(last / a.rep) : 0;
   const int all = (most + kKeys - 1) / kKeys;
   const int per = (all + gridDim.y - 1) / gridDim.y;
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
       a.lse2[at] = lse2;
       a.delta[at] = delta;
     }
-    const T* k = (const T*)a.k + ks.row0 * a.ks + (int64_t)g * a.D;
-    const T* v = (const T*)a.v + ks.row0 * a.vs + (int64_t)g * a.D;
+    const T* k = (const T*)a.k + (int64_t)ks.row0 * a.ks + (int64_t)g * a.D;
+    const T* v = (const T*)a.v + (int64_t)ks.row0 * a.vs + (int64_t)g * a.D;
     const uint32_t base = lds_addr(lds);
     clear_ends<T, DP>(lds, 4 * kKeys, a.D, threadIdx.x, kThreads);
     int low = lim, high = lim;
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
     store_column<float, DP>(a.part + to * a.D, acc, a.scale, a.D);
     return;
   }
-  store_column<T, DP>((T*)a.dq + (tile.seq.row0 + token) * a.dqs + (int64_t)head * a.D, acc,
+  store_column<T, DP>((T*)a.dq + (int64_t)(tile.seq.row0 + token) * a.dqs + (int64_t)head * a.D, acc,
                       a.scale, a.D);
 }
 
@@ -219,14 +219,13 @@ __global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 
   extern __shared__ __align__(16) char lds[];
   const int lane = lane_id(), wave = wave_id() & 3, set = wave_id() >> 2, hh = lane >> 5;
   const int g = blockIdx.x % a.G;
-  // the first keys of a causal sequence are seen by most rows: they go first
-  const Tile tile = tile_of(a.kside, 1, kRows, blockIdx.x / a.G);
+  const Tile tile = tile_of<true>(a.kside, 1, kRows, (int)a.slots, blockIdx.x / a.G);
   if (tile.r0 >= tile.seq.span) return;
-  const int nk = (int)tile.seq.n;
+  const int nk = tile.seq.n;
   Seq qs = {0, 0, 0};
   if (tile.b >= 0) qs = seq_of(a.qside, tile.b);
-  const int nq = (int)qs.n, rows = nq * a.rep;
-  const int k0 = (int)tile.r0, key = k0 + wave * 32 + (lane & 31);
+  const int nq = qs.n, rows = nq * a.rep;
+  const int k0 = tile.r0, key = k0 + wave * 32 + (lane & 31);
   // the first packed row that sees a key; all see the keys before the first token
   const auto first_of = [&](int kk) {
     const int64_t tok = (int64_t)kk - ((int64_t)nk - nq);
@@ -249,10 +248,10 @@ __global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 
     const int64_t at = tile.seq.row0 + (key < nk ? key : nk - 1);
     load_row_frags<T, DP>((const T*)a.k + at * a.ks + (int64_t)g * a.D, a.D, kf);
     load_row_frags<T, DP>((const T*)a.v + at * a.vs + (int64_t)g * a.D, a.D, vf);
-    const T* q = (const T*)a.q + qs.row0 * a.qs + (int64_t)g * a.rep * a.D;
-    const T* dout = (const T*)a.dout + (qs.row0 * a.H + g * a.rep) * a.D;
-    const float* lse2 = a.lse2 + qs.row0 * a.H + g * a.rep;
-    const float* delta = a.delta + qs.row0 * a.H + g * a.rep;
+    const T* q = (const T*)a.q + (int64_t)qs.row0 * a.qs + (int64_t)g * a.rep * a.D;
+    const T* dout = (const T*)a.dout + ((int64_t)qs.row0 * a.H + g * a.rep) * a.D;
+    const float* lse2 = a.lse2 + (int64_t)qs.row0 * a.H + g * a.rep;
+    const float* delta = a.delta + (int64_t)qs.row0 * a.H + g * a.rep;
     const uint32_t base = lds_addr(lds);
     clear_ends<T, DP>(lds, 2 * C::ROWS, a.D, threadIdx.x, C::THREADS);
     clear_ends<T, DP>(lds + C::BUF, 2 * C::ROWS, a.D, threadIdx.x, C::THREADS);
