@@ -32,7 +32,7 @@ struct FwdCfg {
   static constexpr int BUF = 2 * SETS * TILE;  // K and V of a tile for each set
   static constexpr int JOIN = SETS == 2 ? (4 * 32 * DP + 4 * 128) * 4 : 0;
   static constexpr int LDS = 2 * BUF > JOIN ? 2 * BUF : JOIN;
-  static constexpr int WAVES_PER_SIMD = sizeof(T) == 2 || SETS == 2 ? 2 : 1;
+  static constexpr int WAVES_PER_SIMD = sizeof(T) == 2 ? 2 : 1;
 };
 
 template <typename T, int DP, int SETS>
@@ -260,17 +260,17 @@ Side query_side(const AttentionDims& d, const int32_t* seqs) {
 }
 Side key_side(const AttentionDims& d, const int32_t* seqs) { return {seqs, d.Lk, d.B, d.kpacked}; }
 
-// Where the rows give no two workgroups for each CU: two sets in each (float32
-// heads above 64 do not fit twice), and the keys split into as many parts as
-// fill the device, of at least 4 tiles for each set (float32, whose products
-// take 16 times as long: one).
+// Where the rows give no two workgroups for each CU: two sets in each, and the
+// keys split into as many parts as fill the device, of at least 4 tiles for
+// each set.  float32 products take 16 times as long: one set, so that a
+// workgroup has its CU's matrix cores alone, and parts of at least one tile.
 struct Plan {
   int sets, splits;
 };
 Plan plan_of(const AttentionDims& d) {
   const int64_t blocks = tile_slots(query_side(d, nullptr), d.H / d.G, kRows) * d.G;
   if (blocks > 256) return {1, 1};
-  const int sets = d.bf16 || d.D <= 64 ? 2 : 1;
+  const int sets = d.bf16 ? 2 : 1;
   const int64_t keys = d.kpacked ? d.Lk / d.B : d.Lk;
   const int64_t most = keys / ((d.bf16 ? 4 : 1) * sets * kKeys);
   int64_t n = 256 / blocks;
@@ -334,10 +334,7 @@ FwdArgs args_of(const AttentionDims& d, const void* q, const void* k, const void
 
 hipError_t run(const AttentionDims& d, const FwdArgs& a, hipStream_t s) {
   const bool narrow = d.D <= 64;
-  if (plan_of(d).sets == 2) {
-    if (d.bf16) return narrow ? go<bf16, 64, 2>(a, s) : go<bf16, 128, 2>(a, s);
-    return go<float, 64, 2>(a, s);
-  }
+  if (plan_of(d).sets == 2) return narrow ? go<bf16, 64, 2>(a, s) : go<bf16, 128, 2>(a, s);
   if (d.bf16) return narrow ? go<bf16, 64, 1>(a, s) : go<bf16, 128, 1>(a, s);
   return narrow ? go<float, 64, 1>(a, s) : go<float, 128, 1>(a, s);
 }

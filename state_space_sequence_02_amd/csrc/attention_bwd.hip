@@ -20,8 +20,9 @@ namespace m2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 128;     // packed rows (dQ) or keys (dK, dV) of a workgroup
-constexpr int kKeys = 64;      // keys of a tile in the dQ kernel
+constexpr int kRows = 128;     // packed rows of a workgroup of the dQ kernel
+constexpr int kKeys = 64;       // keys of a tile in the dQ kernel
+constexpr int kTileKeys = 128;  // keys of a workgroup of the dK and dV kernel
 
 struct BwdArgs {
   const void *q, *k, *v, *o, *dout;
@@ -193,21 +194,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
                       a.scale, a.D);
 }
 
-// The dK and dV kernel: 4 wavefronts along the keys, in bfloat16 two such sets
-// that take the rows of a tile in halves and add their sums at the end: a
-// workgroup fills its CU and the longest walk (the first keys of a causal
-// sequence) takes half as long as with one set (2 x 4096 rows, 32 heads of
-// 128: LATER us instead of 894, with 512 workgroups of one set all at once).
+// The dK and dV kernel: 4 wavefronts along the keys, 32 each, and in bfloat16
+// two such sets that share the rows of a tile and add their sums at the end:
+// one workgroup fills a CU and the longest walk (the first keys of a causal
+// sequence) takes half as long.  LATER One set and two workgroups on a CU
 template <typename T, int DP>
 struct DkvCfg {
   static constexpr int SETS = sizeof(T) == 2 ? 2 : 1;
   static constexpr int THREADS = 256 * SETS;
-  static constexpr int ROWS = sizeof(T) == 2 ? 64 : 32;  // packed rows of a tile
-  static constexpr int SUBS = ROWS / 32 / SETS;          // 32-row parts of a set
+  static constexpr int SUBS = sizeof(T) == 2 ? 2 / SETS : 1;  // 32 packed rows each, of a set
+  static constexpr int ROWS = 32 * SETS * SUBS;               // packed rows of a tile
   static constexpr int TILE = ROWS * TileCfg<T, DP>::ROWB;
-  static constexpr int STATS = 2 * ROWS * 4 < 512 ? 512 : 2 * ROWS * 4;
-  static constexpr int BUF = 2 * TILE + STATS;  // Q, dO, lse2 and delta
-  static constexpr int JOIN = SETS == 2 ? 4 * 32 * DP * 4 : 0;
+  static constexpr int BUF = 2 * TILE + 512;  // Q, dO, lse2 and delta
+  static constexpr int JOIN = (SETS - 1) * 4 * 32 * DP * 4;
   static constexpr int LDS = 2 * BUF > JOIN ? 2 * BUF : JOIN;
 };
 
@@ -219,7 +218,7 @@ __global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 
   extern __shared__ __align__(16) char lds[];
   const int lane = lane_id(), wave = wave_id() & 3, set = wave_id() >> 2, hh = lane >> 5;
   const int g = blockIdx.x % a.G;
-  const Tile tile = tile_of<true>(a.kside, 1, kRows, (int)a.slots, blockIdx.x / a.G);
+  const Tile tile = tile_of<true>(a.kside, 1, kTileKeys, (int)a.slots, blockIdx.x / a.G);
   if (tile.r0 >= tile.seq.span) return;
   const int nk = tile.seq.n;
   Seq qs = {0, 0, 0};
@@ -279,11 +278,11 @@ __global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 
       wait_vm(0);
       lds_barrier();
       if (t + 1 < tiles) stage(t + 1);
-      const int half = set * C::SUBS * 32;  // this set's rows of the tile
-      const TileReader<T, DP> qr = rd.later((t & 1) * C::BUF + half * K::ROWB),
+      const int mine = set * 32 * C::SUBS;  // this set's rows of the tile
+      const TileReader<T, DP> qr = rd.later((t & 1) * C::BUF + mine * K::ROWB),
                               dr = qr.later(C::TILE);
-      const float* st = (const float*)(lds + (t & 1) * C::BUF + 2 * C::TILE) + half;
-      const int r0 = t * C::ROWS + half;
+      const float* st = (const float*)(lds + (t & 1) * C::BUF + 2 * C::TILE) + mine;
+      const int r0 = t * C::ROWS + mine;
 #pragma unroll
       for (int u = 0; u < C::SUBS; ++u) {
         const int ru = r0 + 32 * u;
@@ -324,16 +323,18 @@ __global__ void __launch_bounds__((DkvCfg<T, DP>::THREADS), (sizeof(T) == 2 ? 2 
       }
     }
   }
-  if constexpr (C::SETS == 2) {
-    if (begin < tiles) {  // the first set takes dV, the second dK
-      __syncthreads();
-      if (set == 1) put_sums(lds, wave, dv);
-      __syncthreads();
-      if (set == 0) add_scaled_sums(lds, wave, dv, 1.f, 1.f);
-      __syncthreads();
-      if (set == 0) put_sums(lds, wave, dk);
-      __syncthreads();
-      if (set == 1) add_scaled_sums(lds, wave, dk, 1.f, 1.f);
+  if constexpr (C::SETS > 1) {
+    if (begin < tiles) {  // the first set takes dV, the last dK
+      const auto join = [&](f32x16 (&v)[DP / 32], int to) {
+        __syncthreads();
+        const int place = (set < to ? set : set - 1) * 4 + wave;
+        if (set != to) put_sums(lds, place, v);
+        __syncthreads();
+        if (set == to)
+          for (int i = 0; i < C::SETS - 1; ++i) add_scaled_sums(lds, i * 4 + wave, v, 1.f, 1.f);
+      };
+      join(dv, 0);
+      join(dk, C::SETS - 1);
     }
   }
   if (key >= tile.seq.span) return;
@@ -386,22 +387,22 @@ hipError_t launch_sum(const float* part, T* out0, T* out1, int64_t s0, int64_t s
 
 // Ranges that the walks are split into, with float32 parts: one (no parts)
 // where the tiles alone give half the device work, else as many as fill it, of
-// at least 4 steps each.
+// at least 4 steps each (float32, whose steps take 16 times as long: one).
 struct Splits {
   int dq, dkv;
 };
-int split_of(int64_t blocks, int64_t steps) {
+int split_of(int64_t blocks, int64_t steps, int64_t least) {
   int64_t n = blocks < 128 ? 256 / blocks : 1;
-  if (n > steps / 4) n = steps / 4;
+  if (n > steps / least) n = steps / least;
   if (n > 32) n = 32;
   return n < 2 ? 1 : (int)n;
 }
 Splits splits_of(const AttentionDims& d) {
   const int64_t rep = d.H / d.G, lq = d.qpacked ? d.Lq / d.B : d.Lq;
-  const int64_t lk = d.kpacked ? d.Lk / d.B : d.Lk;
-  const int64_t tile = d.bf16 ? DkvCfg<bf16, 64>::ROWS : DkvCfg<float, 64>::ROWS;
-  return {split_of(attention_blocks(d), lk / kKeys),
-          split_of(attention_key_blocks(d), lq * rep / tile)};
+  const int64_t lk = d.kpacked ? d.Lk / d.B : d.Lk, least = d.bf16 ? 4 : 1;
+  const int64_t rows = d.bf16 ? 64 : 32;
+  return {split_of(attention_blocks(d), lk / kKeys, least),
+          split_of(attention_key_blocks(d), lq * rep / rows, least)};
 }
 size_t part_bytes(const AttentionDims& d) {
   const Splits n = splits_of(d);
@@ -432,8 +433,8 @@ hipError_t go(BwdArgs a, float* part, Splits n, hipStream_t s) {
     e = launch_sum<T>(part, (T*)a.dq, nullptr, a.dqs, 0, a.q_rows, a.H * a.D, n.dq, s);
     if (e != hipSuccess) return e;
   }
-  a.slots = tile_slots(a.kside, 1, kRows);
   a.part = n.dkv > 1 ? part : nullptr;
+  a.slots = tile_slots(a.kside, 1, kTileKeys);
   e = launch_lds(attention_dkv_kernel<T, DP>, a.slots * a.G, n.dkv, C::THREADS, C::LDS, a, s);
   if (e != hipSuccess || !a.part) return e;
   return launch_sum<T>(part, (T*)a.dk, (T*)a.dv, a.dks, a.dvs, a.k_rows, a.G * a.D, n.dkv, s);
@@ -446,7 +447,7 @@ size_t row_bytes(const AttentionDims& d) {
 }  // namespace
 
 int64_t attention_key_blocks(const AttentionDims& d) {
-  return tile_slots({nullptr, d.Lk, d.B, d.kpacked}, 1, kRows) * d.G;
+  return tile_slots({nullptr, d.Lk, d.B, d.kpacked}, 1, kTileKeys) * d.G;
 }
 
 size_t attention_backward_bytes(const AttentionDims& d) {
@@ -494,7 +495,8 @@ hipError_t launch_attention_backward(const AttentionDims& d, const void* q, cons
   a.scale = d.scale;
   float* part = (float*)((char*)ws + row_bytes(d));
   const Splits n = splits_of(d);
-  if (d.bf16) return d.D <= 64 ? go<bf16, 64>(a, part, n, s) : go<bf16, 128>(a, part, n, s);
+  if (d.bf16)
+    return d.D <= 64 ? go<bf16, 64>(a, part, n, s) : go<bf16, 128>(a, part, n, s);
   return d.D <= 64 ? go<float, 64>(a, part, n, s) : go<float, 128>(a, part, n, s);
 }
 
