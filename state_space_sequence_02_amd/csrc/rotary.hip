@@ -9,9 +9,9 @@
 // Bound by HBM: each element is read and written once.  The angle is formed in
 // float64 and reduced to a part of a turn there, so positions far out keep
 // their digits (in float32 a position of 10^6 would leave 0.06 rad); sine and
-// cosine are then float32 functions of that part.  A thread takes one unit (a
-// vector of pairs, or a vector behind R) of every S-th head of a token, so a
-// sine serves (H + G) / S heads.
+// cosine are then float32 functions of that part.  A workgroup forms them once
+// for its tokens in LDS; then neighbouring threads take neighbouring vectors of
+// a token's heads, so that a wavefront reads and writes whole rows.
 #include "launch.h"
 #include "rowvec.h"
 
@@ -20,6 +20,8 @@ namespace m2 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;    // of a workgroup
+constexpr int kMaxTable = 1024;  // pairs of a workgroup's tokens
 
 struct RotaryArgs {
   const void *q, *k;
@@ -27,60 +29,69 @@ struct RotaryArgs {
   const float* inv_freq;
   const int32_t* positions;
   int64_t tokens, L, qs, ks, yqs, yks;
-  int H, G, D, R;    // G = 0: no keys
-  int units, up, S;  // units of a head, threads for them (a power of two), threads for its heads
+  int H, G, D, R;     // G = 0: no keys
+  int units, up, per;  // units of a head, threads for them (a power of two), tokens of a workgroup
   float scale, sign;
 };
 
+// Unit u of a head: V pairs, or, behind the turned part, V elements.
 template <typename T, int V, bool HALF>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
-  const int team = threadIdx.x / a.up, slot = team % a.S;
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / a.up / a.S) + team / a.S;
-  if (t >= a.tokens) return;
+  // [token][cosines, then sines of the pairs]
+  __shared__ __align__(16) float table[2 * kMaxTable];
+  const int64_t t0 = (int64_t)blockIdx.x * a.per;
+  const int count = (int)(a.tokens - t0 < a.per ? a.tokens - t0 : a.per);
   const int pairs = a.R / 2;
-  // half: V pairs are two vectors of V; neighbours: a vector of 2 V elements
-  // as two of V.  Either way a thread holds two vectors of a rotated unit.
-  const int rot = (pairs + V - 1) / V;
-  const int64_t pos = a.positions ? a.positions[t] : t % a.L;
-  for (int u = threadIdx.x % a.up; u < a.units; u += a.up) {
-    const bool turn = u < rot;
-    float c[V], s[V];
-    int o1, o2;
-    if (turn) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const double turns = (double)pos * (double)a.inv_freq[u * V + e] * 0.15915494309189533577;
-        const float x = (float)(turns - __builtin_rint(turns));
-        float sn, cs;
-        sincospif(2.f * x, &sn, &cs);
-        c[e] = a.scale * cs;
-        s[e] = a.sign * a.scale * sn;
-      }
-      o1 = HALF ? u * V : 2 * u * V;
-      o2 = HALF ? o1 + pairs : o1 + V;
-    } else {
-      o1 = o2 = a.R + (u - rot) * V;
-    }
-    for (int h = slot; h < a.H + a.G; h += a.S) {
-      const bool key = h >= a.H;
-      const T* x = (const T*)(key ? a.k : a.q) + t * (key ? a.ks : a.qs) +
-                   (int64_t)(key ? h - a.H : h) * a.D;
-      T* y = (T*)(key ? a.yk : a.yq) + t * (key ? a.yks : a.yqs) +
-             (int64_t)(key ? h - a.H : h) * a.D;
-      if (!turn) {
-        *(raw_t<T, V>*)(y + o1) = *(const raw_t<T, V>*)(x + o1);
+  for (int i = threadIdx.x; i < count * pairs; i += kThreads) {
+    const int tok = i / pairs, p = i - tok * pairs;
+    const int64_t t = t0 + tok;
+    const int64_t pos = a.positions ? a.positions[t] : t % a.L;
+    const double turns = (double)pos * (double)a.inv_freq[p] * 0.15915494309189533577;
+    const float x = (float)(turns - __builtin_rint(turns));
+    float sn, cs;
+    sincospif(2.f * x, &sn, &cs);
+    table[2 * tok * pairs + p] = a.scale * cs;
+    table[(2 * tok + 1) * pairs + p] = a.sign * a.scale * sn;
+  }
+  __syncthreads();
+  const int rot = pairs / V, heads = a.H + a.G, slots = kThreads / a.up;
+  const float over = 1.f / (float)heads;
+  for (int i = threadIdx.x / a.up; i < count * heads; i += slots) {
+    // i < 2^15: the half keeps the quotient clear of whole numbers
+    const int tok = (int)(((float)i + 0.5f) * over), h = i - tok * heads;
+    const int64_t t = t0 + tok;
+    const bool key = h >= a.H;
+    const T* x = (const T*)(key ? a.k : a.q) + t * (key ? a.ks : a.qs) +
+                 (int64_t)(key ? h - a.H : h) * a.D;
+    T* y = (T*)(key ? a.yk : a.yq) + t * (key ? a.yks : a.yqs) +
+           (int64_t)(key ? h - a.H : h) * a.D;
+    const float* cs = table + 2 * tok * pairs;
+    const float* sn = cs + pairs;
+    for (int u = threadIdx.x % a.up; u < a.units; u += a.up) {
+      if (u >= rot) {
+        const int o = a.R + (u - rot) * V;
+        *(raw_t<T, V>*)(y + o) = *(const raw_t<T, V>*)(x + o);
         continue;
       }
-      float x1[V], x2[V], y1[V], y2[V];
+      // half: V pairs are two vectors of V; neighbours: a vector of 2 V
+      // elements as two of V
+      const int o1 = HALF ? u * V : 2 * u * V;
+      const int o2 = HALF ? o1 + pairs : o1 + V;
+      float x1[V], x2[V], y1[V], y2[V], c[V], s[V];
       load_row<T, V>(x + o1, x1);
       load_row<T, V>(x + o2, x2);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        c[e] = cs[u * V + e];
+        s[e] = sn[u * V + e];
+      }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         if constexpr (HALF || V == 1) {
           y1[e] = x1[e] * c[e] - x2[e] * s[e];
           y2[e] = x1[e] * s[e] + x2[e] * c[e];
         } else {
-          // element j of the 2 V: pair j / 2
+          // element e of the 2 V belongs to pair e / 2
           const int j1 = e / 2, j2 = (V + e) / 2;
           y1[e] = e % 2 ? x1[e - 1] * s[j1] + x1[e] * c[j1] : x1[e] * c[j1] - x1[e + 1] * s[j1];
           y2[e] = e % 2 ? x2[e - 1] * s[j2] + x2[e] * c[j2] : x2[e] * c[j2] - x2[e + 1] * s[j2];
@@ -106,19 +117,19 @@ void run(RotaryArgs a, bool half, hipStream_t s) {
   // vectors where every row, head, half and the end of the rotated part begin
   // at one (base pointers are at 16 bytes)
   const auto fits = [](int64_t v) { return v % V == 0; };
-  const bool vec = fits(a.D) && fits(a.R) && fits(a.R / 2) && fits(a.qs) && fits(a.yqs) &&
+  const bool vec = fits(a.D) && fits(a.R / 2) && fits(a.qs) && fits(a.yqs) &&
                    (!a.G || (fits(a.ks) && fits(a.yks)));
   const int v = vec ? V : 1;
   a.units = a.R / 2 / v + (a.D - a.R) / v;
   a.up = 1;
   while (a.up < a.units && a.up < kThreads) a.up *= 2;
-  // Threads per token for its heads: one (a sine serves all heads) once the
-  // tokens alone fill the device, more while they do not.
-  const int slots = kThreads / a.up;
-  a.S = 1;
-  while (2 * a.S <= slots && a.S < a.H + a.G && a.tokens * a.up * a.S < 256 * 2048) a.S *= 2;
-  const int64_t per = slots / a.S;
-  const unsigned blocks = (unsigned)((a.tokens + per - 1) / per);
+  // Tokens of a workgroup: one while that gives no four workgroups for each
+  // CU, then as many as share a table.
+  a.per = 1;
+  while (2 * a.per <= kMaxTokens && 2 * a.per * (a.R / 2) <= kMaxTable &&
+         a.tokens >= 1024 * 2 * a.per)
+    a.per *= 2;
+  const unsigned blocks = (unsigned)((a.tokens + a.per - 1) / a.per);
   if (vec)
     go<T, V>(a, half, blocks, s);
   else
