@@ -7,9 +7,9 @@
 // writes them.
 //
 // Bound by HBM on the caches, which are read once: a workgroup takes the rep
-// rows of one (sequence, group) and a range of the keys; its wavefronts walk
-// tiles of 32 keys on their own, with the next tile on its way into LDS, and
-// join at the end.  The prefix is one product for the whole batch: batch * rep
+// rows of one (sequence, group) and a range of the keys; its 8 wavefronts
+// walk tiles of 32 keys on their own, each next K and V on its way into LDS as
+// soon as the last is used, and join at the end.  The prefix is one product for the whole batch: batch * rep
 // packed rows against the prefix's keys (attention.hip), so it is read once
 // for all sequences and not once for each.  Ranges and prefix leave float32
 // parts that one more kernel joins; a single range without a prefix needs none.
@@ -30,19 +30,36 @@ struct StepArgs {
   float c;
 };
 
-// Wavefronts of a workgroup: as many as two tiles of K and V for each fit LDS.
+// Workgroup n of slots * G: its slot and group.  Workgroups go to the 8 XCDs in
+// turn; eight neighbours take eight slots of one group, so that an XCD reads
+// whole rows of the caches, in which the groups lie side by side (128 x 4096
+// rows of 8 x 128: 215 us; group n % G: 219).
+struct Place {
+  int slot, g;
+};
+__device__ __forceinline__ Place place_of(unsigned n, unsigned slots, unsigned G) {
+  constexpr unsigned X = 8;
+  const unsigned block = n / (X * G), first = block * X;
+  const unsigned wide = slots - first < X ? slots - first : X;  // slots of the last block
+  const unsigned r = n - block * X * G;
+  const unsigned g = r / wide;
+  return {(int)(first + r - g * wide), (int)g};
+}
+
+// Wavefronts of a workgroup: 8, if a tile of K and V for each fits LDS.
 template <typename T, int DP>
-constexpr int waves_of() { return sizeof(T) * DP > 256 ? 2 : 4; }
+constexpr int waves_of() { return sizeof(T) * DP > 256 ? 4 : 8; }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_kernel(StepArgs a) {
+__global__ void __launch_bounds__((64 * waves_of<T, DP>()), (waves_of<T, DP>() / 4)) attention_step_kernel(StepArgs a) {
   using K = TileCfg<T, DP>;
   constexpr int W = waves_of<T, DP>();
   constexpr int TILE = 32 * K::ROWB;
-  extern __shared__ __align__(16) char lds[];  // [W][2][K tile, V tile]
+  extern __shared__ __align__(16) char lds[];  // [W][K tile, V tile]
   const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
-  const int g = blockIdx.x % a.G, rest = blockIdx.x / a.G;
-  const int b = rest / a.tiles, r0 = rest % a.tiles * 32;
+  const Place at = place_of(blockIdx.x, a.B * a.tiles, a.G);
+  const int g = at.g;
+  const int b = at.slot / a.tiles, r0 = at.slot % a.tiles * 32;
   const int64_t cap = a.rows;
   const int n = (int)clamp64(uniform_at(a.lengths, b), cap);
   const int64_t cs = (int64_t)a.G * a.D;
@@ -51,20 +68,13 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_ke
   const T* vn = (const T*)a.v + b * a.vs + (int64_t)g * a.D;
   T* kc = (T*)a.k_cache + cache;
   T* vc = (T*)a.v_cache + cache;
-  if (blockIdx.y == 0 && r0 == 0 && n < cap) {
-    for (int i = threadIdx.x * 4; i < a.D; i += 64 * W * 4) {
-      *(raw_t<T, 4>*)(kc + n * cs + i) = *(const raw_t<T, 4>*)(kn + i);
-      *(raw_t<T, 4>*)(vc + n * cs + i) = *(const raw_t<T, 4>*)(vn + i);
-    }
-  }
-
   const int row = r0 + (lane & 31);
   const int head = g * a.rep + (row < a.rep ? row : a.rep - 1);
   const int nk = n + 1;
   const int tiles = (nk + 31) / 32;
   const int per = (tiles + gridDim.y - 1) / gridDim.y;
   const int t0 = blockIdx.y * per, t1 = t0 + per < tiles ? t0 + per : tiles;
-  char* mine = lds + wave * 4 * TILE;
+  char* mine = lds + wave * 2 * TILE;
   const uint32_t base = lds_addr(mine);
   using State = RowState<T, DP, 1>;
   State st;
@@ -72,42 +82,51 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_ke
   if (t0 + wave < t1) {
     head_frag<T> q[K::STEPS];
     load_row_frags<T, DP>((const T*)a.q + b * a.qs + (int64_t)head * a.D, a.D, q);
-    clear_ends<T, DP>(mine, 4 * 32, a.D, lane, 64);
+    clear_ends<T, DP>(mine, 2 * 32, a.D, lane, 64);
     using St = Stager<T, DP, 32, 64>;
     const St off(cs, lane);
-    const auto stage = [&](int t, int buf) {
-      const uint32_t to = base + buf * 2 * TILE;
-      if (t * 32 + 32 <= n) {
-        off.load(to, kc + t * 32 * cs, a.D, lane);
-        off.load(to + TILE, vc + t * 32 * cs, a.D, lane);
-      } else {
-        St::load_tail(to, kc, cs, t * 32, nk, kn, a.D, lane);
-        St::load_tail(to + TILE, vc, cs, t * 32, nk, vn, a.D, lane);
-      }
+    const auto load = [&](const T* cache, const T* token, uint32_t to, int t) {
+      if (t * 32 + 32 <= n)
+        off.load(to, cache + t * 32 * cs, a.D, lane);
+      else
+        St::load_tail(to, cache, cs, t * 32, nk, token, a.D, lane);
     };
-    const TileReader<T, DP> first(base);
-    wait_vm(0);
-    stage(t0 + wave, 0);
-    int buf = 0;
-    for (int t = t0 + wave; t < t1; t += W, buf ^= 1) {
-      // the other buffer's reads are done: their results were used
-      if (t + W < t1) {
-        stage(t + W, buf ^ 1);
-        wait_vm(2 * St::PER);
-      } else {
-        wait_vm(0);
-      }
+    // Waits for a load and for the reads before the next one into its place.
+    const auto here = [&](int later) {
+      wait_vm(later);
       asm volatile("" ::: "memory");
-      const TileReader<T, DP> kr = first.later(buf * 2 * TILE);
+    };
+    const auto read = [&] {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      asm volatile("" ::: "memory");
+    };
+    const TileReader<T, DP> kr(base), vr = kr.later(TILE);
+    load(kc, kn, base, t0 + wave);
+    load(vc, vn, base + TILE, t0 + wave);
+    for (int t = t0 + wave; t < t1; t += W) {
       typename State::Scores s;
       typename State::Weights p;
+      here(St::PER);
       State::scores(q, kr, s);
+      read();
+      const bool more = t + W < t1;
+      if (more) load(kc, kn, base, t + W);
       if (t * 32 + 32 > nk) State::mask(s, nk - t * 32);
       st.raise(State::top(s), 8.f / a.c, a.c);
       st.weigh(s, a.c, p);
-      st.take(kr.later(TILE), p);
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-      asm volatile("" ::: "memory");
+      here(more ? St::PER : 0);
+      st.take(vr, p);
+      read();
+      if (more) load(vc, vn, base + TILE, t + W);
+    }
+  }
+
+  // the token's own row of the cache, which nothing here reads
+  if (blockIdx.y == 0 && r0 == 0 && n < cap) {
+    for (int i = threadIdx.x * 4; i < a.D; i += 64 * W * 4) {
+      *(raw_t<T, 4>*)(kc + n * cs + i) = *(const raw_t<T, 4>*)(kn + i);
+      *(raw_t<T, 4>*)(vc + n * cs + i) = *(const raw_t<T, 4>*)(vn + i);
     }
   }
 
@@ -119,19 +138,21 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_ke
   constexpr int LD = DP + 4;
   const int x = lane & 31;
   const float l = st.l + __shfl_xor(st.l, 32);
-  if (hh == 0) {
-    tops[wave * 32 + x] = st.m;
-    sums[wave * 32 + x] = l;
-  }
-#pragma unroll
-  for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      const float v[4] = {st.o[d][r], st.o[d][r + 1], st.o[d][r + 2], st.o[d][r + 3]};
-      store_row<float, 4>(outs + (wave * 32 + x) * LD + 32 * d + 2 * r + 4 * hh, v);
-    }
-  __syncthreads();
   const int left = a.rep - r0 < 32 ? a.rep - r0 : 32;
+  if (x < left) {
+    if (hh == 0) {
+      tops[wave * 32 + x] = st.m;
+      sums[wave * 32 + x] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const float v[4] = {st.o[d][r], st.o[d][r + 1], st.o[d][r + 2], st.o[d][r + 3]};
+        store_row<float, 4>(outs + (wave * 32 + x) * LD + 32 * d + 2 * r + 4 * hh, v);
+      }
+  }
+  __syncthreads();
   const int quads = a.D / 4;
   for (int i = threadIdx.x; i < left * quads; i += 64 * W) {
     const int rr = i / quads, e = i % quads * 4;
@@ -166,8 +187,9 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), 1) attention_step_ke
 template <typename T, int DP>
 hipError_t go(const StepArgs& a, int splits, hipStream_t s) {
   constexpr int W = waves_of<T, DP>();
-  constexpr int bytes = W * 4 * 32 * TileCfg<T, DP>::ROWB;
-  static_assert(bytes >= (W * 64 + W * 32 * (DP + 4)) * 4, "the join's floats fit the tiles' place");
+  constexpr int tiles = W * 2 * 32 * TileCfg<T, DP>::ROWB, join = (W * 64 + W * 32 * (DP + 4)) * 4;
+  constexpr int bytes = tiles > join ? tiles : join;
+  static_assert(bytes <= 160 * 1024, "a CU's LDS");
   const auto kernel = attention_step_kernel<T, DP>;
   const hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -178,12 +200,12 @@ hipError_t go(const StepArgs& a, int splits, hipStream_t s) {
 
 int64_t row_tiles(const AttentionStepDims& d) { return (d.H / d.G + 31) / 32; }
 
-// Ranges of the cache: enough workgroups for the device, at least two tiles
-// for each wavefront of them where the cache is full.
+// Ranges of the cache: as many workgroups as CUs, at least one tile for each
+// wavefront where the cache is full.
 int splits_of(const AttentionStepDims& d) {
   const int64_t blocks = attention_step_blocks(d);
   const int64_t most = (d.rows + 255) / 256;
-  int64_t n = 512 / blocks;
+  int64_t n = 256 / blocks;
   if (n > most) n = most;
   if (n > 32) n = 32;
   return n < 2 ? 1 : (int)n;
