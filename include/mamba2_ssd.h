@@ -626,7 +626,7 @@ typedef struct {
  * bfloat16 the weights are rounded to it before the product with v.
  * Supported: rows of q and of k <= 2^28; rows of q * H / G < 2^31 - 256;
  * workgroups (G times the tiles of 128 rows of q * H / G, or of k; packed: and
- * B + 2) < 2^24.
+ * B + 2) < 2^23.
  * Workspace at least mamba2_attention_workspace_bytes(dims) (0: dims
  * invalid), 256-byte aligned.
  */
@@ -678,7 +678,7 @@ typedef struct {
  * Types and strides as for attention.  Workspace at least
  * mamba2_attention_step_workspace_bytes(dims) (0: dims invalid), 256-byte
  * aligned.  Bound by HBM on the caches; the prefix is read once for all.
- * Supported: B * G * ceil(H / G / 32) < 2^24.
+ * Supported: B * G * ceil(H / G / 32) and G * ceil(B * H / G / 128) < 2^23.
  */
 size_t mamba2_attention_step_workspace_bytes(const mamba2_attention_step_dims* dims);
 

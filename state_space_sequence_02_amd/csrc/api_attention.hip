@@ -24,7 +24,7 @@ constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxStride = (int64_t)1 << 24;       // elements between tokens
 constexpr int64_t kMaxTileStride = (int64_t)1 << 22;   // of attention: a tile within 2^30 bytes
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 256;  // rows of q times heads of a group, tile included
-constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;  // workgroups of 256 along x
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 23) - 1;  // workgroups of 512 along x
 
 int check_dtype(int32_t dtype) {
   if (dtype != MAMBA2_DTYPE_F32 && dtype != MAMBA2_DTYPE_BF16)

@@ -197,7 +197,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
 // The dK and dV kernel: 4 wavefronts along the keys, 32 each, and in bfloat16
 // two such sets that share the rows of a tile and add their sums at the end:
 // one workgroup fills a CU and the longest walk (the first keys of a causal
-// sequence) takes half as long.  LATER One set and two workgroups on a CU
+// sequence) takes half as long.  With one set, and two workgroups on a CU, the
+// training step of 2 x 4096 tokens, 32 heads of 128, took 1691 us (1240 with
+// two sets), packed 8192 x 24 x 64 385 us (297); tiles of 64 keys with four
+// sets 1347 and 305.
 template <typename T, int DP>
 struct DkvCfg {
   static constexpr int SETS = sizeof(T) == 2 ? 2 : 1;

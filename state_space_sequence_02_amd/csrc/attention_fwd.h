@@ -62,9 +62,13 @@ struct RowState {
     return max_halves(t);
   }
 
-  // Takes m to the tile's top where that is more than `slack` above: until
-  // then the weights are at most 2^8, which costs no digits, and the sums need
-  // no scaling (slack = 8 / c).
+  // How far above m a score may be: until then the weights are at most 2^8,
+  // which costs no digits, and the sums need no scaling.  Finite for any scale,
+  // so that the first tile (m = -infinity) always counts.
+  __device__ __forceinline__ static float slack_of(float c) {
+    return __builtin_fminf(8.f / c, 1e30f);
+  }
+  // Takes m to the tile's top where that is more than `slack` above.
   __device__ __forceinline__ void raise(float top, float slack, float c) {
     if (__ballot(top > m + slack)) {
       const float now = __builtin_fmaxf(m, top);

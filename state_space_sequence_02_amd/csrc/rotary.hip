@@ -22,6 +22,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 8;    // of a workgroup
 constexpr int kMaxTable = 1024;  // pairs of a workgroup's tokens
+constexpr int64_t kMaxBlocks = 1 << 20;
 
 struct RotaryArgs {
   const void *q, *k;
@@ -35,12 +36,10 @@ struct RotaryArgs {
 };
 
 // Unit u of a head: V pairs, or, behind the turned part, V elements.
+// Tokens t0 .. t0 + count - 1; table: [token][cosines, then sines of the pairs].
 template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
-  // [token][cosines, then sines of the pairs]
-  __shared__ __align__(16) float table[2 * kMaxTable];
-  const int64_t t0 = (int64_t)blockIdx.x * a.per;
-  const int count = (int)(a.tokens - t0 < a.per ? a.tokens - t0 : a.per);
+__device__ __forceinline__ void turn_tokens(const RotaryArgs& a, float* table, int64_t t0,
+                                            int count) {
   const int pairs = a.R / 2;
   for (int i = threadIdx.x; i < count * pairs; i += kThreads) {
     const int tok = i / pairs, p = i - tok * pairs;
@@ -103,6 +102,16 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
   }
 }
 
+template <typename T, int V, bool HALF>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
+  __shared__ __align__(16) float table[2 * kMaxTable];
+  const int64_t step = (int64_t)gridDim.x * a.per;
+  for (int64_t t0 = (int64_t)blockIdx.x * a.per; t0 < a.tokens; t0 += step) {
+    turn_tokens<T, V, HALF>(a, table, t0, (int)(a.tokens - t0 < a.per ? a.tokens - t0 : a.per));
+    __syncthreads();  // the table is free
+  }
+}
+
 template <typename T, int V>
 void go(const RotaryArgs& a, bool half, unsigned blocks, hipStream_t s) {
   if (half)
@@ -129,7 +138,8 @@ void run(RotaryArgs a, bool half, hipStream_t s) {
   while (2 * a.per <= kMaxTokens && 2 * a.per * (a.R / 2) <= kMaxTable &&
          a.tokens >= 1024 * 2 * a.per)
     a.per *= 2;
-  const unsigned blocks = (unsigned)((a.tokens + a.per - 1) / a.per);
+  const int64_t groups = (a.tokens + a.per - 1) / a.per;
+  const unsigned blocks = (unsigned)(groups < kMaxBlocks ? groups : kMaxBlocks);
   if (vec)
     go<T, V>(a, half, blocks, s);
   else
