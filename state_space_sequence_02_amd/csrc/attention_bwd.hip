@@ -172,8 +172,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
             if (8 * (r / 4) + r % 4 >= left) s[r] = -__builtin_inff();
         }
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          s[r] = fast_exp2(__builtin_fmaf(s[r], a.c, -lse2)) * (dp[r] - delta);
+        for (int r = 0; r < 16; ++r) s[r] = fast_exp2(__builtin_fmaf(s[r], a.c, -lse2));
+        if (ku == 0) {
+          // All keys of rows that see no more than these: their delta without
+          // o's rounding, which is what such rows' gradients feel (its share
+          // falls with the number of keys).
+          float sum = 0.f;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sum = __builtin_fmaf(s[r], dp[r], sum);
+          sum = add_xor32(sum);
+          if (lim <= 32) delta = sum;
+          if (lim <= 32 && row < rows && hh == 0) a.delta[at] = sum;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const row_frag<T> ds = acc_frag<T>(s, h);
