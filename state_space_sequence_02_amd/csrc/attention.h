@@ -302,7 +302,7 @@ struct TileReader {
   template <typename V>
   __device__ __forceinline__ static V at(uint32_t a, int offset) {
     typedef __attribute__((address_space(3))) const V* lds_ptr;
-    return *(lds_ptr)(a + offset);
+    return *(lds_ptr)(uintptr_t)(a + offset);
   }
   // The same reads of a tile that begins `bytes` (multiples of a row) later.
   __device__ __forceinline__ TileReader later(uint32_t bytes) const {
@@ -328,9 +328,9 @@ struct TileReader {
     const int o = offset + r16 * K::ROWB;
     if constexpr (sizeof(T) == 2) {
       typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-      const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)((col ^ (64 * dt)) + o));
+      const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uintptr_t)((col ^ (64 * dt)) + o));
       const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_ptr)((col ^ (64 * dt + 32)) + o + 8 * K::ROWB));
+          (lds_ptr)(uintptr_t)((col ^ (64 * dt + 32)) + o + 8 * K::ROWB));
       return cat(__builtin_bit_cast(bf16x4, lo), __builtin_bit_cast(bf16x4, hi));
     } else {
       f32v8 f;

@@ -7,9 +7,9 @@
 // writes them.
 //
 // Bound by HBM on the caches, which are read once: a workgroup takes the rep
-// rows of one (sequence, group) and a range of the keys; its 8 wavefronts
-// walk tiles of 32 keys on their own, each next K and V on its way into LDS as
-// soon as the last is used, and join at the end.  The prefix is one product for the whole batch: batch * rep
+// rows of one (sequence, group) and a range of the keys; its 4 or
+// 8 wavefronts walk tiles of 32 keys on their own, each next K and V on its way
+// into LDS as soon as the last is used, and join at the end.  The prefix is one product for the whole batch: batch * rep
 // packed rows against the prefix's keys (attention.hip), so it is read once
 // for all sequences and not once for each.  Ranges and prefix leave float32
 // parts that one more kernel joins; a single range without a prefix needs none.
@@ -47,14 +47,11 @@ __device__ __forceinline__ Place place_of(unsigned n, unsigned slots, unsigned G
   return {(int)(first + r - g * wide), (int)g};
 }
 
-// Wavefronts of a workgroup: 8, if a tile of K and V for each fits LDS.
-template <typename T, int DP>
-constexpr int waves_of() { return sizeof(T) * DP > 256 ? 4 : 8; }
-
-template <typename T, int DP>
-__global__ void __launch_bounds__((64 * waves_of<T, DP>()), (waves_of<T, DP>() / 4)) attention_step_kernel(StepArgs a) {
+// W wavefronts, 4 or 8, of which a CU holds 8 (float32 heads above 64: 4).
+template <typename T, int DP, int W>
+__global__ void __launch_bounds__((64 * W), (sizeof(T) * DP > 256 ? 1 : 2))
+    attention_step_kernel(StepArgs a) {
   using K = TileCfg<T, DP>;
-  constexpr int W = waves_of<T, DP>();
   constexpr int TILE = 32 * K::ROWB;
   extern __shared__ __align__(16) char lds[];  // [W][K tile, V tile]
   const int lane = lane_id(), wave = wave_id(), hh = lane >> 5;
@@ -185,18 +182,29 @@ __global__ void __launch_bounds__((64 * waves_of<T, DP>()), (waves_of<T, DP>() /
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int W>
 hipError_t go(const StepArgs& a, int splits, hipStream_t s) {
-  constexpr int W = waves_of<T, DP>();
   constexpr int tiles = W * 2 * 32 * TileCfg<T, DP>::ROWB, join = (W * 64 + W * 32 * (DP + 4)) * 4;
   constexpr int bytes = tiles > join ? tiles : join;
   static_assert(bytes <= 160 * 1024, "a CU's LDS");
-  const auto kernel = attention_step_kernel<T, DP>;
+  const auto kernel = attention_step_kernel<T, DP, W>;
   const hipError_t e =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
   kernel<<<dim3((unsigned)((int64_t)a.B * a.tiles * a.G), splits), 64 * W, bytes, s>>>(a);
   return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t go(const StepArgs& a, int splits, hipStream_t s) {
+  if constexpr (sizeof(T) * DP <= 256) {
+    // Long walks: one workgroup on a CU, whose wavefronts share a row's groups
+    // (128 x 4096 rows: 215 us; with two workgroups of 4 wavefronts 242).
+    // Short ones are mostly their beginning and end, which two overlap (64
+    // sequences of up to 512 rows: 17 us instead of 20; 4 of 1100: 8.1, 8.4).
+    if (a.rows > 1024 * (int64_t)splits) return go<T, DP, 8>(a, splits, s);
+  }
+  return go<T, DP, 4>(a, splits, s);
 }
 
 int64_t row_tiles(const AttentionStepDims& d) { return (d.H / d.G + 31) / 32; }

@@ -115,7 +115,9 @@ def build(g, dtype, H, G, D, form, nq, nk, extra, tail, fill):
     """Inputs on the GPU, their keyword arguments, flat float64 copies and the spans."""
     same = form in ("padded", "packed") and nq == nk
     lead = lambda n: (sum(n) + tail,) if "packed" in form else (len(n), max(max(n), 1) + tail)  # noqa: E731
-    lq, lk = lead(nq), (lead(nk) if form != "packed-cache" else (len(nk), max(max(nk), 1) + tail))
+    padded = lambda n: (len(n), max(max(n), 1) + tail)  # noqa: E731
+    lq = lead(nq) if form != "cache-packed" else padded(nq)
+    lk = lead(nk) if form != "packed-cache" else padded(nk)
     if same:
         row = rnd(g, *lq, (H + 2 * G) * D + extra, dtype=dtype)
         cols = [row[..., a * D:b * D].unflatten(-1, (b - a, D)) for a, b in
@@ -169,6 +171,9 @@ ATTENTION = [
     (F32, 3, 3, 128, "packed", True, [40, 0, 90], [40, 0, 90], 0, 6),
     (F32, 6, 2, 24, "cross", False, [65, 0], [129, 3], 0, 1),
     (F32, 2, 1, 104, "cross", True, [90, 2], [30, 70], 0, 0),
+    (BF, 4, 2, 64, "cache-packed", True, [33, 0, 64], [70, 5, 64], 0, 3),  # q padded, k packed
+    (BF, 256, 1, 16, "padded", True, [5, 2], [5, 2], 0, 0),  # a tile of rows inside one token
+    (F32, 160, 1, 8, "packed", False, [2, 1], [2, 1], 8, 1),
 ]
 
 

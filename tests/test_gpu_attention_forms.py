@@ -73,3 +73,33 @@ def test_step_of_many_sequences(m2, dtype, D):  # noqa: F811
     want, bound, _, _ = ref.step(*(ref.to64(t[some]) for t in (q, k, v, kc, vc)),
                                  [lens[i] for i in some], None, None, 1 / math.sqrt(D), dtype)
     close(o[some], want, bound, "o")
+
+
+def test_step_of_long_caches(m2):  # noqa: F811
+    """Long caches without a split: workgroups of eight wavefronts; and the same split."""
+    for B, rows in ((200, 1500), (3, 9000)):
+        H, G, D = 8, 2, 128
+        g = torch.Generator().manual_seed(43)
+        q, k, v = (rnd(g, B, n, D, dtype=BF) for n in (H, G, G))
+        gpu = torch.Generator(device="cuda").manual_seed(44)
+        kc, vc = (torch.randn(B, rows, G, D, generator=gpu, device="cuda").to(BF) for _ in range(2))
+        lens = [(977 * i + rows - 7) % (rows + 1) for i in range(B)]
+        o = m2.attention_step(q.cuda(), k.cuda(), v.cuda(), kc.clone(), vc.clone(), whole(lens))
+        torch.cuda.synchronize()
+        for i in (0, 1, B - 1):
+            one = [ref.to64(t[i:i + 1]) for t in (q, k, v, kc, vc)]
+            want, bound, _, _ = ref.step(*one, [lens[i]], None, None, 1 / math.sqrt(D), BF)
+            close(o[i:i + 1], want, bound, f"o of {B} x {rows}, {i}")
+
+
+def test_tiny_scale(m2):  # noqa: F811
+    """A scale that leaves every score 0 in float32: plain means, lse = log of the keys seen."""
+    g = torch.Generator().manual_seed(45)
+    q, k, v = rnd(g, 1, 90, 2, 32).cuda(), rnd(g, 1, 90, 2, 32).cuda(), rnd(g, 1, 90, 2, 32).cuda()
+    o, lse = m2.attention_forward(q, k, v, scale=1e-40)
+    torch.cuda.synchronize()
+    n = torch.arange(1, 91, device="cuda", dtype=torch.float64)
+    want = v[0].double().cumsum(0) / n[:, None, None]
+    # a mean of n values: n + 3 roundings of the sum of their sizes over n, at most 4
+    assert ((o[0].double() - want).abs() <= (n[:, None, None] + 3) * ref.U * 4).all()
+    assert ((lse[0].double() - n.log()[:, None]).abs() <= 8 * ref.U * (1 + n.log()[:, None])).all()
