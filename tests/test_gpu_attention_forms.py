@@ -103,3 +103,17 @@ def test_tiny_scale(m2):  # noqa: F811
     # a mean of n values: n + 3 roundings of the sum of their sizes over n, at most 4
     assert ((o[0].double() - want).abs() <= (n[:, None, None] + 3) * ref.U * 4).all()
     assert ((lse[0].double() - n.log()[:, None]).abs() <= 8 * ref.U * (1 + n.log()[:, None])).all()
+
+
+def test_rotary_of_more_tokens_than_workgroups(m2):  # noqa: F811
+    """Over 2^23 tokens: workgroups take more than one table of tokens."""
+    n = (1 << 23) + 777
+    gpu = torch.Generator(device="cuda").manual_seed(46)
+    q = torch.randn(n, 1, 2, generator=gpu, device="cuda")
+    inv = torch.tensor([0.37], device="cuda")
+    y = m2.rotary_forward(q, None, inv)
+    torch.cuda.synchronize()
+    at = torch.cat([torch.arange(50), torch.arange((1 << 23) - 20, n, 3), torch.randint(0, n, (500,))])
+    x = ref.to64(q[at.cuda()])
+    want = ref.rotary(x, inv.cpu(), at, "half", 1.0)
+    close(y[at.cuda()], want, ref.rotary_bound(x, want, 2, "half", 1.0, F32), "y")
