@@ -69,12 +69,12 @@ __device__ __forceinline__ Seq seq_of(const Side& s, int64_t b) {
   return q;
 }
 
-// A tile of `tile` packed rows.  Packed: between and behind the sequences there are rows that belong to
-// none, so the tensor is cut at 0, starts[0 .. B], len: B + 2 pieces of which
-// the first and the last hold no tokens.  Piece i takes the slots from
-// floor(cut_i rep / tile) + i on: the next piece's first slot is at least as
-// far as its rows need, whatever the lengths, so the number of slots follows
-// from the sizes alone (no list is made, nothing is copied to the host).
+// A tile of `tile` packed rows.  Packed: between and behind the sequences there
+// are rows that belong to none, so the tensor is cut at 0, starts[0 .. B], len:
+// B + 2 pieces of which the first and the last hold no tokens.  The tiles of
+// all pieces are at most floor(len rep / tile) + B + 2, whatever the lengths, so
+// the number of workgroups follows from the sizes alone (no list is made,
+// nothing is copied to the host).
 struct Tile {
   Seq seq;
   int b;   // sequence; -1: rows of none
@@ -151,7 +151,8 @@ __device__ __forceinline__ Tile tile_of(const Side& s, int rep, int tile, int sl
     return piece_tile(s, p, __builtin_amdgcn_readlane(cut, p), __builtin_amdgcn_readlane(next, p),
                       (KEYS ? __builtin_amdgcn_readlane(have, p) - 1 - lo : lo) * tile);
   }
-  // 64 pieces at once
+  // Piece i takes the slots from floor(cut_i rep / tile) + i on: the next one's
+  // first is at least as far as its rows need.  64 pieces are looked at at once.
   int lo = 0, count = pieces;
   while (count > 1) {
     const int step = (count + 63) / 64;
@@ -328,7 +329,8 @@ struct TileReader {
     const int o = offset + r16 * K::ROWB;
     if constexpr (sizeof(T) == 2) {
       typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-      const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uintptr_t)((col ^ (64 * dt)) + o));
+      const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_ptr)(uintptr_t)((col ^ (64 * dt)) + o));
       const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
           (lds_ptr)(uintptr_t)((col ^ (64 * dt + 32)) + o + 8 * K::ROWB));
       return cat(__builtin_bit_cast(bf16x4, lo), __builtin_bit_cast(bf16x4, hi));

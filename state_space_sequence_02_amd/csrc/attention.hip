@@ -270,9 +270,13 @@ Side query_side(const AttentionDims& d, const int32_t* seqs) {
 Side key_side(const AttentionDims& d, const int32_t* seqs) { return {seqs, d.Lk, d.B, d.kpacked}; }
 
 // Where the rows give no two workgroups for each CU: two sets in each, and the
-// keys split into as many parts as fill the device, of at least 4 tiles for
-// each set.  float32 products take 16 times as long: one set, so that a
-// workgroup has its CU's matrix cores alone, and parts of at least one tile.
+// keys split into as many parts as give one workgroup to each CU, of at least 4
+// tiles for each set.  One set in two workgroups for each CU has twice the
+// parts: 64 rows of 32 heads on a prefix of 16384 took 28 + 7 us with the join
+// instead of 29 + 5, 128 tokens on 32768 keys 79 + 7 instead of 84 + 5.  float32
+// products take 16 times as long: one set, so that a workgroup has its CU's
+// matrix cores alone, and parts of at least one tile (5 x 301 rows on 203 keys:
+// 12 + 3 us, 23 with two sets and no parts).
 struct Plan {
   int sets, splits;
 };

@@ -7,12 +7,13 @@
 // writes them.
 //
 // Bound by HBM on the caches, which are read once: a workgroup takes the rep
-// rows of one (sequence, group) and a range of the keys; its 4 or
-// 8 wavefronts walk tiles of 32 keys on their own, each next K and V on its way
-// into LDS as soon as the last is used, and join at the end.  The prefix is one product for the whole batch: batch * rep
-// packed rows against the prefix's keys (attention.hip), so it is read once
-// for all sequences and not once for each.  Ranges and prefix leave float32
-// parts that one more kernel joins; a single range without a prefix needs none.
+// rows of one (sequence, group) and a range of the keys; its 4 or 8 wavefronts
+// walk tiles of 32 keys on their own, each next K and V on its way into LDS as
+// soon as the last is used, and join at the end.  The prefix is one product for
+// the whole batch: batch * rep packed rows against the prefix's keys
+// (attention.hip), so it is read once for all sequences and not once for each.
+// Ranges and prefix leave float32 parts that one more kernel joins; a single
+// range without a prefix needs none.
 // 128 sequences of up to 4096 rows of 8 x 128, 1.1 GB: 215 us, 5.1 TB/s.
 #include "attention_fwd.h"
 
