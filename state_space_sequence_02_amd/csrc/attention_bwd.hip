@@ -65,7 +65,7 @@ __device__ __forceinline__ void stage_packed(uint32_t lds, const T* base, int64_
 // 4 bytes a lane, as dma16.
 __device__ __forceinline__ void dma4(const void* src, uint32_t lds_base) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_base);
-  asm volatile("global_load_lds_dword %0, off" : : "v"(src), "{m0}"(m0) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(src), "{m0}"(m0) : "memory");
 }
 
 template <typename T, int DP>

@@ -55,10 +55,12 @@ __device__ __forceinline__ bf16x8 cat(bf16x4 lo, bf16x4 hi) {
 // disambiguate from later LDS reads of the other buffer (it would then wait
 // for the load right away and undo the prefetch).  The caller owns the
 // ordering: the issuing waves wait vmcnt(0), then a barrier, before any wave
-// reads the destination.
+// reads the destination.  The s_nop is the wait state that a load to LDS needs
+// behind a scalar instruction that wrote M0, its LDS address; the compiler
+// puts none ahead of inline asm.
 __device__ __forceinline__ void dma16(const void* src, uint32_t lds_base) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_base);
-  asm volatile("global_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(m0) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(m0) : "memory");
 }
 
 // LDS byte address of a pointer into a __shared__ array.
