@@ -176,11 +176,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attention_dq
         if (ku == 0) {
           // All keys of rows that see no more than these: their delta without
           // o's rounding, which is what such rows' gradients feel (its share
-          // falls with the number of keys).
-          float sum = 0.f;
+          // falls with the number of keys).  The weights are good to lse's
+          // rounding, |lse| 2^-24 times a few, one factor for a row: over
+          // their own sum it leaves dP - delta, and only scales dS.
+          float sum = 0.f, total = 0.f;
 #pragma unroll
-          for (int r = 0; r < 16; ++r) sum = __builtin_fmaf(s[r], dp[r], sum);
+          for (int r = 0; r < 16; ++r) {
+            sum = __builtin_fmaf(s[r], dp[r], sum);
+            total += s[r];
+          }
           sum = add_xor32(sum);
+          total = add_xor32(total);
+          sum = total == 0.f ? 0.f : sum / total;  // no key: no weights
           if (lim <= 32) delta = sum;
           if (lim <= 32 && row < rows && hh == 0) a.delta[at] = sum;
         }
