@@ -195,11 +195,12 @@ __global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES
     }
     if (set == 1) return;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  // No key: l = 0.  A score beyond float32 makes l NaN, and o and lse too.
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   if (row >= span) return;
   const int64_t at = (int64_t)(tile.seq.row0 + token) * a.H + head;
   // log2 units until the end
-  const float lse = l > 0.f ? st.m * a.c + __builtin_amdgcn_logf(l) : -__builtin_inff();
+  const float lse = l == 0.f ? -__builtin_inff() : st.m * a.c + __builtin_amdgcn_logf(l);
   if (a.part_o) {
     const int64_t p = (int64_t)blockIdx.y * a.q_rows * a.H + at;
     if (hh == 0) a.part_lse[p] = lse;
@@ -245,8 +246,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const float* __restrict_
       for (int j = 0; j < 4; ++j) acc[j] = __builtin_fmaf(w, v[i][j], acc[j]);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (lse && lane == 0) lse[row] = sum > 0.f ? (base + __builtin_amdgcn_logf(sum)) * kLn2 : none;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (lse && lane == 0) lse[row] = sum == 0.f ? none : (base + __builtin_amdgcn_logf(sum)) * kLn2;
   if (e < D) {
     const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
     store_row<T, 4>(o + row * D + e, v);

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__((64 * W), (sizeof(T) * DP > 256 ? 1 : 2))
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] += f * outs[(w * 32 + rr) * LD + e + j];
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= inv;
     const int64_t at = (int64_t)b * a.H + g * a.rep + r0 + rr;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__((64 * W), (sizeof(T) * DP > 256 ? 1 : 2))
       const int64_t p = (int64_t)blockIdx.y * a.B * a.H + at;
       store_row<float, 4>(a.part_o + p * a.D + e, v);
       if (e == 0)
-        a.part_lse[p] = sum > 0.f ? top * a.c + __builtin_amdgcn_logf(sum) : -__builtin_inff();
+        a.part_lse[p] = sum == 0.f ? -__builtin_inff() : top * a.c + __builtin_amdgcn_logf(sum);
     } else {
       store_row<T, 4>((T*)a.o + at * a.D + e, v);
     }
