@@ -20,8 +20,8 @@ import torch
 from . import (MAMBA2_DTYPE_BF16, MAMBA2_DTYPE_F32, MAMBA2_ERR_DTYPE, MAMBA2_ERR_SHAPE,
                MAMBA2_ERR_UNSUPPORTED, Mamba2AttentionDims, Mamba2AttentionStepDims, Mamba2Error,
                Mamba2RotaryDims, _lib, _ptr, _req_bytes)
-from .layer import (_BF16, _F32, _I32, _Tensor, _call, _io, _known, _launch, _optional, _owner,
-                    _plain, _stride, _tensors, _want, _workspace)
+from .layer import (_BF16, _F32, _I32, _Tensor, _call, _given, _io, _known, _launch, _optional,
+                    _owner, _plain, _stride, _tensors, _want, _workspace)
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = ("none", "linear", "base", "parts")
@@ -355,6 +355,7 @@ def attention_forward(q, k, v, *, causal=True, scale=None, q_lengths=None, k_len
                 v.data_ptr(), _ptr(qs), _ptr(ks), o.data_ptr(), lse.data_ptr(),
                 workspace.data_ptr(), n)
     else:
+        _given(w, q_lengths=q_lengths, k_lengths=k_lengths)
         mamba2_attention_forward(dims, q, k, v, qs, ks, o, lse, workspace, n, stream)
     return o, lse
 
@@ -379,6 +380,7 @@ def attention_backward(q, k, v, o, lse, dout, *, causal=True, scale=None, q_leng
                 g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), workspace.data_ptr(),
                 n)
     else:
+        _given(w, q_lengths=q_lengths, k_lengths=k_lengths, o=o, lse=lse, dout=dout)
         mamba2_attention_backward(dims, q, k, v, qs, ks, o, lse, dout, g["dq"], g["dk"], g["dv"],
                                   workspace, n, stream)
     return g
@@ -482,6 +484,7 @@ def attention_step(q, k, v, k_cache, v_cache, lengths, k_prefix=None, v_prefix=N
                 v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(),
                 _ptr(k_prefix), _ptr(v_prefix), o.data_ptr(), workspace.data_ptr(), n)
     else:
+        _given(w, v_cache=v_cache, lengths=lengths, v_prefix=v_prefix)
         mamba2_attention_step(dims, q, k, v, k_cache, v_cache, lengths, k_prefix, v_prefix, o,
                               workspace, n, stream)
     return o

@@ -158,6 +158,12 @@ def _tensors(where, **tensors):
                               f"{name} is a {type(t).__name__}, not a tensor")
 
 
+def _given(where, **tensors):
+    """The same for optional tensors, in the branch that hands on to a mamba2_* function: those
+    take whole numbers as addresses, the short functions do not."""
+    _tensors(where, **{name: t for name, t in tensors.items() if t is not None})
+
+
 def _like(t):
     """The gradient's tensor of an optional input (the call refuses what is no tensor)."""
     return torch.empty_like(t) if isinstance(t, _Tensor) else None
