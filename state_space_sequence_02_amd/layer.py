@@ -331,6 +331,7 @@ def conv1d_forward(x, weight, bias=None, init_state=None, *, parts=None, activat
                 weight.data_ptr(), _ptr(bias), _ptr(init_state), _ptr(lengths), *map(_ptr, out),
                 final.data_ptr())
     else:
+        _given("conv1d_forward", weight=weight, bias=bias, init_state=init_state, lengths=lengths)
         mamba2_conv1d_forward(dims, x, weight, bias, init_state, lengths, *out, final, stream)
     return (ys[0] if parts is None else tuple(ys)), final
 
@@ -365,6 +366,8 @@ def conv1d_backward(x, weight, bias, init_state, dys, dfinal=None, *, activation
                 _ptr(dfinal), g["dx"].data_ptr(), g["dweight"].data_ptr(), _ptr(g["dbias"]),
                 g["dinit"].data_ptr(), workspace.data_ptr(), n)
     else:
+        _given("conv1d_backward", weight=weight, bias=bias, init_state=init_state, dfinal=dfinal,
+               lengths=lengths)
         mamba2_conv1d_backward(dims, x, weight, bias, init_state, lengths, *dy3, dfinal, g["dx"],
                                g["dweight"], g["dbias"], g["dinit"], workspace, n, stream)
     return g
@@ -384,6 +387,7 @@ def conv1d_step(x, weight, bias, state, *, parts=None, activation="silu", stream
         _launch(_lib.mamba2_conv1d_step, "conv1d_step", i, stream, ref, x.data_ptr(),
                 weight.data_ptr(), _ptr(bias), state.data_ptr(), *map(_ptr, out))
     else:
+        _given("conv1d_step", weight=weight, bias=bias, state=state)
         mamba2_conv1d_step(dims, x, weight, bias, state, *out, stream)
     return ys[0] if parts is None else tuple(ys)
 
@@ -543,6 +547,8 @@ def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, init_st
                 _ptr(z), _ptr(dt_bias), _ptr(init_state), _ptr(lengths), y.data_ptr(),
                 final.data_ptr(), workspace.data_ptr(), n)
     else:
+        _given("selective_scan_forward", dt=dt, D=D, dt_bias=dt_bias, init_state=init_state,
+               lengths=lengths)
         mamba2_selective_scan_forward(dims, u, dt, A, B, C, D, z, dt_bias, init_state, lengths, y,
                                       final, workspace, n, stream)
     return y, final
@@ -575,6 +581,8 @@ def selective_scan_backward(u, dt, A, B, C, D, z, dt_bias, init_state, dy, dfina
                 dC.data_ptr(), _ptr(dD), _ptr(dz), _ptr(dbias), dinit.data_ptr(),
                 workspace.data_ptr(), n)
     else:
+        _given("selective_scan_backward", dt=dt, D=D, dt_bias=dt_bias, init_state=init_state, dy=dy,
+               dfinal=dfinal, lengths=lengths)
         mamba2_selective_scan_backward(dims, u, dt, A, B, C, D, z, dt_bias, init_state, lengths,
                                        dy, dfinal, du, ddt, dA, dB, dC, dD, dz, dbias, dinit,
                                        workspace, n, stream)
@@ -596,6 +604,7 @@ def selective_scan_step(u, dt, A, B, C, D, z, dt_bias, state, *, softplus=True, 
                 u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
                 _ptr(z), _ptr(dt_bias), state.data_ptr(), y.data_ptr())
     else:
+        _given("selective_scan_step", dt=dt, D=D, dt_bias=dt_bias, state=state)
         mamba2_selective_scan_step(dims, u, dt, A, B, C, D, z, dt_bias, state, y, stream)
     return y
 
@@ -697,6 +706,7 @@ def norm_forward(x, weight, bias=None, z=None, *, ngroups=1, kind="rms", eps=1e-
         _launch(_lib.mamba2_norm_forward, "norm_forward", i, stream, ref, x.data_ptr(), _ptr(z),
                 weight.data_ptr(), _ptr(bias), y.data_ptr())
     else:
+        _given("norm_forward", weight=weight, bias=bias)
         mamba2_norm_forward(dims, _rows(x, dims), _rows(z, dims), weight, bias, _rows(y, dims),
                             stream)
     return y
@@ -728,6 +738,7 @@ def norm_backward(x, weight, bias, z, dy, *, ngroups=1, kind="rms", eps=1e-5, wo
                 weight.data_ptr(), dy.data_ptr(), g["dx"].data_ptr(), _ptr(g["dz"]),
                 g["dweight"].data_ptr(), _ptr(g["dbias"]), workspace.data_ptr(), n)
     else:
+        _given("norm_backward", weight=weight, bias=bias)
         mamba2_norm_backward(dims, _rows(x, dims), _rows(z, dims), weight, _rows(dy, dims),
                              _rows(g["dx"], dims), _rows(g["dz"], dims), g["dweight"], g["dbias"],
                              workspace, n, stream)
