@@ -50,11 +50,12 @@ def rotary_frequencies(rotary, base=10000.0, *, scaling="none", factor=1.0, orig
                        fast=32.0, slow=1.0, device=None):
     """(inv_freq[rotary/2] float32, scale) for rotary_forward: base^(-2i/rotary), stretched for
     contexts ``factor`` times as long.  ``scaling``: "none"; "linear": every frequency divided
-    by factor; "base": the base raised by factor^(rotary/(rotary-2)), so that the lowest
-    frequency is divided by factor and the highest stays; "parts": frequencies that turn more
-    than ``fast`` times within ``original_length`` tokens stay, those under ``slow`` times are
-    divided by factor, a ramp between, with scale = 0.1 ln(factor) + 1 on q and k.  Formed in
-    float64."""
+    by factor; "base" (published as the NTK-aware change of base): the base raised by
+    factor^(rotary/(rotary-2)), so that the lowest frequency is divided by factor and the highest
+    stays (rotary = 2 has but the highest, and no effect); "parts" (published as YaRN): frequencies
+    that turn more than ``fast`` times within ``original_length`` tokens stay, those under ``slow``
+    times are divided by factor, a ramp between, with scale = 0.1 ln(factor) + 1 on q and k.  Formed
+    in float64."""
     w = "rotary_frequencies"
     if scaling not in _SCALINGS:
         raise Mamba2Error(MAMBA2_ERR_UNSUPPORTED, w, f"unknown scaling {scaling!r}")
@@ -80,7 +81,10 @@ def rotary_frequencies(rotary, base=10000.0, *, scaling="none", factor=1.0, orig
         turns_at = [rotary * math.log(original_length / (t * 2 * math.pi)) / (2 * math.log(base))
                     for t in (fast, slow)]
         lo, hi = max(math.floor(turns_at[0]), 0), min(math.ceil(turns_at[1]), rotary - 1)
-        ramp = ((torch.arange(rotary // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        # no room between the ends: the context is shorter than `slow` turns of the first frequency
+        # (hi <= 0, all are divided) or all frequencies turn more than `fast` times (none is)
+        i = torch.arange(rotary // 2, dtype=torch.float64)
+        ramp = ((i - lo) / (hi - lo)).clamp(0, 1) if hi > lo else (i >= hi).to(i.dtype)
         f = f / factor * ramp + f * (1 - ramp)
         scale = 0.1 * math.log(factor) + 1.0
     return f.to(_F32).to(device), scale
