@@ -34,7 +34,7 @@ def _code(dtype):
 def _number(where, name, v):
     try:
         return float(v)
-    except (TypeError, ValueError):
+    except (TypeError, ValueError, OverflowError):
         raise Mamba2Error(MAMBA2_ERR_SHAPE, where, f"{name} is {v!r}, not a number") from None
 
 
@@ -66,21 +66,31 @@ def rotary_frequencies(rotary, base=10000.0, *, scaling="none", factor=1.0, orig
         raise Mamba2Error(MAMBA2_ERR_SHAPE, w,
                           f"base must be above 1 and factor at least 1 (got {base}, {factor})")
     if scaling == "base" and rotary > 2:
-        base *= factor ** (rotary / (rotary - 2))
+        try:
+            base *= factor ** (rotary / (rotary - 2))
+        except OverflowError:
+            base = math.inf
+        if base == math.inf:
+            raise Mamba2Error(MAMBA2_ERR_SHAPE, w, f"factor {factor} takes the base beyond float64")
     f = base ** (-torch.arange(0, rotary, 2, dtype=torch.float64) / rotary)
     scale = 1.0
     if scaling == "linear":
         f = f / factor
     elif scaling == "parts":
         fast, slow = _number(w, "fast", fast), _number(w, "slow", slow)
-        if original_length is None or not (original_length >= 1 and 0 < slow < fast):
+        if original_length is not None:
+            original_length = _number(w, "original_length", original_length)
+        try:
+            if original_length is None or not (original_length >= 1 and 0 < slow < fast):
+                raise ValueError
+            # the ramp is linear in i between the frequencies with `fast` and `slow` turns
+            turns_at = [rotary * math.log(original_length / (t * 2 * math.pi)) / (2 * math.log(base))
+                        for t in (fast, slow)]
+            lo, hi = max(math.floor(turns_at[0]), 0), min(math.ceil(turns_at[1]), rotary - 1)
+        except (ValueError, OverflowError):  # the logarithm of 0 or infinity among them
             raise Mamba2Error(MAMBA2_ERR_SHAPE, w,
-                              "parts needs original_length >= 1 and 0 < slow < fast (got "
-                              f"{original_length}, {slow}, {fast})")
-        # the ramp is linear in i between the frequencies with `fast` and `slow` turns
-        turns_at = [rotary * math.log(original_length / (t * 2 * math.pi)) / (2 * math.log(base))
-                    for t in (fast, slow)]
-        lo, hi = max(math.floor(turns_at[0]), 0), min(math.ceil(turns_at[1]), rotary - 1)
+                              "parts needs original_length >= 1 and 0 < slow < fast, all finite (got "
+                              f"{original_length}, {slow}, {fast})") from None
         # no room between the ends: the context is shorter than `slow` turns of the first frequency
         # (hi <= 0, all are divided) or all frequencies turn more than `fast` times (none is)
         i = torch.arange(rotary // 2, dtype=torch.float64)

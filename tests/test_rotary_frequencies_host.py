@@ -48,3 +48,22 @@ def test_one_frequency():
     """The single frequency of two elements is the highest one, which "base" leaves."""
     for factor in (1.0, 8.0):
         assert torch.equal(m2.rotary_frequencies(2, scaling="base", factor=factor)[0], torch.ones(1))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rotary=64, base="x"), dict(rotary=64, base=10 ** 400), dict(rotary=64, base=float("inf")),
+    dict(rotary=64, factor=None), dict(rotary=4, scaling="base", factor=1e200),
+    dict(rotary=4, scaling="base", base=1e300, factor=1e10),
+    dict(rotary=64, scaling="parts", factor=2, original_length="x"),
+    dict(rotary=64, scaling="parts", factor=2, original_length=float("inf")),
+    dict(rotary=64, scaling="parts", factor=2, original_length=float("nan")),
+    dict(rotary=64, scaling="parts", factor=2, original_length=100, fast=float("inf")),
+    dict(rotary=64, scaling="parts", factor=2, original_length=100, fast="x"),
+    dict(rotary=64, scaling="parts", factor=2, original_length=100, slow=1e-310, fast=1e308),
+    dict(rotary=64, scaling="parts", factor=2, original_length=1e308, slow=1e-300),
+])
+def test_refused(kw):
+    """What is no number, or leaves float64, with the package's error."""
+    with pytest.raises(m2.Mamba2Error) as e:
+        m2.rotary_frequencies(**kw)
+    assert e.value.status == m2.MAMBA2_ERR_SHAPE
