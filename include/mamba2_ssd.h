@@ -597,7 +597,7 @@ typedef struct {
   int64_t dq_stride; /* of dq, dk, dv (backward) */
   int64_t dk_stride;
   int64_t dv_stride;
-  float scale;      /* > 0 */
+  float scale;      /* > 0; scale * log2(e) is a float32 too */
   int32_t causal;   /* 0 or 1 */
   int32_t q_packed; /* 0 or 1: how the sequences lie in q */
   int32_t k_packed; /* the same of k and v */
@@ -664,7 +664,7 @@ typedef struct {
   int64_t q_stride; /* elements between sequences of q; 0: H * D */
   int64_t k_stride; /* the same of k and of v; 0: G * D */
   int64_t v_stride;
-  float scale;      /* > 0 */
+  float scale;      /* as for attention */
   int32_t dtype;    /* mamba2_dtype */
 } mamba2_attention_step_dims;
 

@@ -77,6 +77,15 @@ int check_scale(float scale) {
   return MAMBA2_OK;
 }
 
+// Attention's exponentials are base 2: the scale with log2(e) is a float32 factor.
+int check_attention_scale(float scale) {
+  CHECK(check_scale(scale));
+  if (isinf(scale * 1.44269504088896340736f))
+    return fail(MAMBA2_ERR_UNSUPPORTED, "scale times log2(e) is beyond float32 (scale %g)",
+                (double)scale);
+  return MAMBA2_OK;
+}
+
 int validate(const mamba2_rotary_dims* p, m2::RotaryDims* d) {
   if (!p) return fail(MAMBA2_ERR_NULL, "dims is NULL");
   CHECK(check_dtype(p->dtype));
@@ -129,7 +138,7 @@ int validate(const mamba2_attention_dims* p, m2::AttentionDims* d) {
   CHECK(check_flag(p->causal, "causal"));
   CHECK(check_flag(p->q_packed, "q_packed"));
   CHECK(check_flag(p->k_packed, "k_packed"));
-  CHECK(check_scale(p->scale));
+  CHECK(check_attention_scale(p->scale));
   if (p->reserved != 0) return fail(MAMBA2_ERR_SHAPE, "dims.reserved must be 0");
   if (p->batch > kMaxBatch || p->q_len > kMaxTokens || p->k_len > kMaxTokens)
     return fail(MAMBA2_ERR_UNSUPPORTED, "sizes beyond the supported range");
@@ -171,7 +180,7 @@ int validate(const mamba2_attention_step_dims* p, m2::AttentionStepDims* d) {
     return fail(MAMBA2_ERR_SHAPE, "sizes must be >= 1 (batch=%lld rows=%lld) and prefix >= 0 (%lld)",
                 (long long)p->batch, (long long)p->rows, (long long)p->prefix);
   CHECK(check_heads(p->nheads, p->ngroups, p->headdim));
-  CHECK(check_scale(p->scale));
+  CHECK(check_attention_scale(p->scale));
   if (p->batch > kMaxBatch || p->rows > kMaxTokens || p->prefix > kMaxTokens)
     return fail(MAMBA2_ERR_UNSUPPORTED, "sizes beyond the supported range");
   d->B = p->batch;
