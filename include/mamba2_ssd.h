@@ -612,9 +612,10 @@ typedef struct {
  * head, with s_j = scale * q_i . k_j over the keys that it sees,
  *     o_i = sum_j exp(s_j - lse_i) v_j,    lse_i = log sum_j exp(s_j)
  * A query that sees no key has o = 0 and lse = -infinity.
- * Scores are float32: one above its range makes the query's o and lse NaN (and
- * gradients of its sequence), one below it is a weight of 0, and a query all
- * of whose scores are below it counts as one that sees no key.
+ * Scores are float32 (q_i . k_j, and times scale * log2(e)): one above its range
+ * makes the query's o and lse NaN (and gradients of its sequence), one below it
+ * is a weight of 0; a query all of whose scores are below it has NaN too, or
+ * counts as one that sees no key.
  *     q, o  [B, q_len, H, D]  (packed: [q_len, H, D]); q rows of q_stride
  *     k, v  [B, k_len, G, D]  (packed: [k_len, G, D]); rows of k_stride, v_stride
  *     lse   [B, q_len, H] float32 (packed: [q_len, H])

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__((kThreads * SETS), (FwdCfg<T, DP, SETS>::WAVES
     }
     if (set == 1) return;
   }
-  // No key: l = 0.  A score beyond float32 makes l NaN, and o and lse too.
+  l = row_sum(l, st.m);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   if (row >= span) return;
   const int64_t at = (int64_t)(tile.seq.row0 + token) * a.H + head;

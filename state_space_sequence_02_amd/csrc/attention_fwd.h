@@ -16,6 +16,13 @@
 
 namespace m2 {
 
+// A row's sum of weights, with m its maximum.  A score beyond float32 leaves
+// NaN in it, or 0 or infinity where only m c is beyond: o and lse of the row
+// are then NaN.  0 is left to rows that have seen no key (m = -infinity).
+__device__ __forceinline__ float row_sum(float l, float m) {
+  return m == -__builtin_inff() || (l > 0.f && l < __builtin_inff()) ? l : __builtin_nanf("");
+}
+
 template <typename T, int DP, int SUBS>
 struct RowState {
   static constexpr int STEPS = TileCfg<T, DP>::STEPS, COLS = DP / 32;

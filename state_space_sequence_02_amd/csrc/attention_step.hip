@@ -168,6 +168,7 @@ __global__ void __launch_bounds__((64 * W), (sizeof(T) * DP > 256 ? 1 : 2))
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] += f * outs[(w * 32 + rr) * LD + e + j];
     }
+    sum = row_sum(sum, top);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= inv;

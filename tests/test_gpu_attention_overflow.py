@@ -68,6 +68,46 @@ def test_prompt(m2, dtype, B, nq, nk, H, G, D, i, j, parts):  # noqa: F811
             close(l, alone["lse"][0, 0], limit["lse"][0, 0], "lse without the key")
 
 
+@pytest.mark.parametrize("dtype,B,nq,nk,H,G,D,i,j,parts", CASES)
+def test_products_within_and_scores_beyond(m2, dtype, B, nq, nk, H, G, D, i, j, parts):  # noqa: F811
+    """A product of 1e10 that the scale (1e30) takes beyond float32; all others are 0."""
+    say(f"[scores] {dtype} {B} {nq} {nk} {H} {G} {D}")
+    for sign in (1, -1):
+        q, k, v = pair(torch.Generator().manual_seed(65), dtype, B, nq, nk, H, G, D, i, j, sign)
+        q, k = (torch.where(x.abs() == x.abs().max(), 1e5 * x.sign(), 0 * x) for x in (q, k))
+        o, lse = m2.attention_forward(*(x.cuda() for x in (q, k, v)), scale=1e30)
+        # the same scores by a scale of 1: 0, and below -1e38 or not looked at
+        want, bound = ref.attention(ref.to64(q[0]) * 1e15, ref.to64(k[0]) * 1e15, ref.to64(v[0]),
+                                    [(0, nq)], [(0, nk)], True, 1.0, dtype)
+        torch.cuda.synchronize()
+        rows = torch.ones(nq, H, dtype=torch.bool)
+        rows[i, 1] = False
+        for name, got in (("o", o), ("lse", lse)):
+            close(got[0].cpu()[rows], want[name][rows], bound[name][rows], name)
+        one, l = o[0, i, 1].cpu(), lse[0, i, 1].cpu()
+        if sign > 0:
+            assert torch.isnan(one).all() and torch.isnan(l)
+        elif i + nk - nq:  # the mean of the other keys
+            n = i + nk - nq + 1
+            rest = ref.to64(v[0, :n, 1 // (H // G)])
+            rest = (rest.sum(0) - rest[j]) / (n - 1)
+            assert ((ref.to64(one) - rest).abs() <= 2 * ref.half_step(dtype) * (rest.abs() + 1)).all()
+            assert abs(float(l) - math.log(n - 1)) <= 16 * ref.U * math.log(n)
+
+
+@pytest.mark.parametrize("dtype,B,nq,nk,H,G,D,i,j,parts", CASES)
+def test_queries_that_are_not_numbers(m2, dtype, B, nq, nk, H, G, D, i, j, parts):  # noqa: F811
+    """A row of which no score is a number is no row without keys either."""
+    q, k, v = pair(torch.Generator().manual_seed(66), dtype, B, nq, nk, H, G, D, i, j, 1)
+    q[0, i, 1] = float("nan")
+    o, lse = m2.attention_forward(*(x.cuda() for x in (q, k, v)))
+    torch.cuda.synchronize()
+    assert torch.isnan(o[0, i, 1]).all() and torch.isnan(lse[0, i, 1])
+    rows = torch.ones(nq, H, dtype=torch.bool)
+    rows[i, 1] = False
+    assert torch.isfinite(o[0].cpu()[rows]).all() and torch.isfinite(lse[0].cpu()[rows]).all()
+
+
 def test_gradients(m2):  # noqa: F811
     """dq of the row is not a number either, nor what its keys get from it; another sequence's
     gradients do not feel it."""
@@ -85,10 +125,12 @@ def test_gradients(m2):  # noqa: F811
             assert torch.isfinite(want[n]).all() and torch.equal(got[n][1:], want[n]), n
 
 
+@pytest.mark.parametrize("huge,scale", [(HUGE, None), (1e5, 1e30)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,prefix", [(100, 0), (2000, 0), (100, 300)])
-def test_step(m2, dtype, rows, prefix):  # noqa: F811
-    """One token: against a key of the cache, and of the prefix."""
+def test_step(m2, dtype, rows, prefix, huge, scale):  # noqa: F811
+    """One token: against a key of the cache, and of the prefix; with a scale that takes a product
+    there all other scores are 0."""
     B, H, G, D = 3, 4, 2, 64
     g = torch.Generator().manual_seed(64)
     for place in ("cache", "prefix") if prefix else ("cache",):
@@ -97,16 +139,17 @@ def test_step(m2, dtype, rows, prefix):  # noqa: F811
         kp, vp = (rnd(g, prefix, G, D, dtype=dtype) if prefix else None for _ in range(2))
         for x in (q, k, kc, kp):
             if x is not None:
-                x[..., 0] = 0
-        q[1, 3, 0] = HUGE
-        (kc[1] if place == "cache" else kp)[70, 1, 0] = HUGE
+                x[..., :1 if scale is None else D] = 0
+        q[1, 3, 0] = huge
+        (kc[1] if place == "cache" else kp)[70, 1, 0] = huge
         lens = [rows - 1, rows, 20]
         o = m2.attention_step(*(x.cuda() for x in (q, k, v, kc, vc)), whole(lens),
-                              None if kp is None else kp.cuda(), None if vp is None else vp.cuda())
+                              None if kp is None else kp.cuda(), None if vp is None else vp.cuda(),
+                              scale=scale)
         torch.cuda.synchronize()
         o = o.cpu()
         want, bound, _, _ = ref.step(*(ref.to64(t) for t in (q, k, v, kc, vc)), lens, ref.to64(kp),
-                                     ref.to64(vp), 1 / math.sqrt(D), dtype)
+                                     ref.to64(vp), 1 / math.sqrt(D) if scale is None else 1.0, dtype)
         assert torch.isnan(o[1, 3]).all(), place
         others = torch.ones(B, H, dtype=torch.bool)
         others[1, 3] = False
