@@ -270,11 +270,17 @@ Side query_side(const AttentionDims& d, const int32_t* seqs) {
 }
 Side key_side(const AttentionDims& d, const int32_t* seqs) { return {seqs, d.Lk, d.B, d.kpacked}; }
 
-// Where the rows give no two workgroups for each CU: two sets in each, and the
-// keys split into as many parts as give one workgroup to each CU, of at least 4
-// tiles for each set.  One set in two workgroups for each CU has twice the
-// parts: 64 rows of 32 heads on a prefix of 16384 took 28 + 7 us with the join
-// instead of 29 + 5, 128 tokens on 32768 keys 79 + 7 instead of 84 + 5.  float32
+// While the rows give at most one workgroup for each CU (256; packed rows count
+// with the slots that may stay empty): two sets in each, and the keys split into
+// as many parts as give one workgroup to each CU, of at least 4 tiles for each
+// set.  One set in two workgroups for each CU has twice the parts: 64 rows of 32
+// heads on a prefix of 16384 took 28 + 7 us with the join instead of 29 + 5, 128
+// tokens on 32768 keys 79 + 7 instead of 84 + 5.  Above 256 workgroups one set.
+// From 257 to 512 two sets would gain where one causal sequence's walks differ
+// (1152, 1536 and 2048 tokens, 32 heads of 128: 26, 34 and 50 us instead of 29,
+// 37 and 52; 2048 tokens, 24 heads of 64: 27 instead of 33) and lose where they
+// are equal or short (the same without a causal limit: 48, 60, 83 and 49 instead
+// of 39, 52, 75 and 42; 4 x 400 tokens: 23 instead of 19).  float32
 // products take 16 times as long: one set, so that a workgroup has its CU's
 // matrix cores alone, and parts of at least one tile (5 x 301 rows on 203 keys:
 // 12 + 3 us, 23 with two sets and no parts).

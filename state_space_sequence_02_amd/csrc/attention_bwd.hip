@@ -408,10 +408,13 @@ hipError_t launch_sum(const float* part, T* out0, T* out1, int64_t s0, int64_t s
 }
 
 // Ranges that the walks are split into, with float32 parts: one (no parts)
-// where the tiles alone give half the device work, else as many as fill it, of
-// at least 4 steps each (float32, whose steps take 16 times as long: one).  5 x
-// 301 rows on 203 keys in float32: dK and dV 18 + 3 us (99 in one walk), dQ 15 +
-// 3 (27).
+// where the tiles are 128 workgroups or more, else as many as fill the device,
+// of at least 4 steps each (float32, whose steps take 16 times as long: one).  5
+// x 301 rows on 203 keys in float32: dK and dV 18 + 3 us (99 in one walk), dQ 15
+// + 3 (27).  The rule counts workgroups, not the lengths of causal walks: those
+// of one sequence of 2048 or 4096 tokens, 8 groups (128 and 256 workgroups of dK
+// and dV), are as long as the longest of 2 x 4096, so its training step takes
+// 364 or 842 us where 2 x 4096 takes 1307.
 struct Splits {
   int dq, dkv;
 };

@@ -204,6 +204,8 @@ hipError_t go(const StepArgs& a, int splits, hipStream_t s) {
     // (128 x 4096 rows: 215 us; with two workgroups of 4 wavefronts 242).
     // Short ones are mostly their beginning and end, which two overlap (64
     // sequences of up to 512 rows: 17 us instead of 20; 4 of 1100: 8.1, 8.4).
+    // Around the border the rates of full caches are near: 64 of 1024 rows (four
+    // wavefronts) 6.1 TB/s and of 1100 (eight) 5.7, 128 of either 5.3.
     if (a.rows > 1024 * (int64_t)splits) return go<T, DP, 8>(a, splits, s);
   }
   return go<T, DP, 4>(a, splits, s);
@@ -211,8 +213,11 @@ hipError_t go(const StepArgs& a, int splits, hipStream_t s) {
 
 int64_t row_tiles(const AttentionStepDims& d) { return (d.H / d.G + 31) / 32; }
 
-// Ranges of the cache: as many workgroups as CUs, at least one tile for each
-// wavefront where the cache is full.
+// Ranges of the cache: as many as fit in one workgroup for each CU, of at least
+// one tile for each wavefront where the cache is full.  Workgroups that are no
+// divisor of 256 leave CUs idle in the last turn: full caches of 4096 rows of 8
+// x 128 stream at 5.3 TB/s for 32 sequences, 5.6 for 64, 5.0 for 17, 4.2 for 33
+// and 4.4 for 40.
 int splits_of(const AttentionStepDims& d) {
   const int64_t blocks = attention_step_blocks(d);
   const int64_t most = (d.rows + 255) / 256;
